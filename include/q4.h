@@ -328,6 +328,145 @@ q4_status q4_gemv_noalloc(const void *x, q4_dtype xt, int64_t M, int64_t N, int6
                           const void *qw, q4_layout layout, size_t qw_bytes, void *y,
                           q4_dtype yt, q4_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Serving operators: the steps between the qkv product and the o product of
+ * a decoder layer, for requests of any length whose keys and values live in
+ * a blocked cache.  One step of a server runs q4_cache_plan once, then per
+ * layer q4_gemv/q4_gemm (qkv), q4_rope_append, q4_attention, q4_gemv/q4_gemm
+ * (o).  They follow the conventions above (device pointers, no allocation,
+ * host checks before any launch, asynchronous on `stream`).  Lengths, block
+ * tables and slots are device arrays, so a step needs no host round trip and
+ * can be captured in a CUDA graph and replayed.
+ *
+ * The cache: `blocks` blocks of `block_size` tokens; token t of a request is
+ * at offset t % block_size of the block that its table row names at column
+ * t / block_size.  A "slot" is block * block_size + offset (64 bits).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    void *k, *v;          /* device, 16-byte aligned */
+    q4_dtype type;        /* Q4_BF16 or Q4_F16 */
+    int64_t blocks;       /* 1 .. 2^31 - 1 */
+    int64_t heads;        /* KV heads */
+    int64_t block_size;   /* tokens per block, a multiple of 16 */
+    int64_t head_dim;     /* a multiple of 8, at most 128 */
+    /* element strides of k and v alike, multiples of 8; the head_dim elements
+     * of a token are contiguous.  [blocks][heads][block_size][head_dim] and
+     * [blocks][block_size][heads][head_dim] are both views of this form. */
+    int64_t block_stride, head_stride, token_stride;
+} q4_kv_cache;
+
+#define Q4_PLAN_MAX_REQUESTS 16384
+
+/*
+ * The step's plan, from request lengths on the device.  Request b holds
+ * cached[b] tokens in the blocks that its table row lists and brings fresh[b]
+ * new ones (either may be 0).  Writes
+ *   q_start[b]   (B + 1) first row of request b among the step's T token
+ *                rows: the running sum of fresh (never above T)
+ *   kv_len[b]    (B) cached[b] + fresh[b]: its length after this step
+ *   table        [B][table_stride], columns ceil(cached/S) .. ceil((cached +
+ *                fresh)/S) - 1 of each row: the blocks its new tokens need,
+ *                taken from the end of free_blocks in request order (S =
+ *                block_size; block i of the step's total is
+ *                free_blocks[*free_count - 1 - i]); other entries are kept
+ *   position[t]  (T) the token's place in its request
+ *   slot[t]      (T, 64 bits) where its key and value go
+ *   counts[4]    {the running sum's end, tokens of served requests, free
+ *                blocks left, requests not served}
+ * A request is not served when its length does not fit `width` columns or
+ * its tokens do not fit T, when a length is negative (taken as 0 tokens), or
+ * when the running total of new blocks passes *free_count (a request that
+ * needs no block is still served then): its kv_len is 0 and its tokens get
+ * position 0 and slot -1, so the append skips them and their attention is 0.
+ * Token rows past the last request get the same (padding, for graphs of a
+ * fixed T).  A slot whose table entry is negative is -1.  Nothing that is
+ * read is written (free_count and free_blocks are left alone; take
+ * counts[2] as the next count), so a repeated call gives the same result.
+ * INVALID_ARG for NULL pointers, T, B, width, block_size or free_capacity
+ * < 1 or a table_stride below width; UNSUPPORTED above
+ * Q4_PLAN_MAX_REQUESTS requests, or T, width * block_size, free_capacity
+ * beyond 2^31 - 1.
+ */
+q4_status q4_cache_plan(const int32_t *cached, const int32_t *fresh, int64_t B, int64_t block_size,
+                        int32_t *table, int64_t table_stride, int64_t width,
+                        const int32_t *free_blocks, const int32_t *free_count,
+                        int64_t free_capacity, int64_t T, int32_t *q_start, int32_t *kv_len,
+                        int32_t *position, int64_t *slot, int32_t *counts, q4_stream_t stream);
+
+/* How the rotated pairs lie in a head: (i, i + rot/2), or (2i, 2i + 1). */
+typedef enum { Q4_ROPE_HALF = 0, Q4_ROPE_INTERLEAVED = 1 } q4_rope_style;
+
+/*
+ * Rotary positions and cache append.  qkv: T rows of (Hq + 2 * heads) *
+ * head_dim elements of the cache's type, row stride qkv_stride: the query
+ * heads, then the cache's key heads, then its value heads.  Pair i < rot/2 of
+ * each query and key head turns by position[t] * freq[i] radians,
+ *     (a, b) -> factor * (a cos - b sin, a sin + b cos),
+ * the elements from rot on are copied.  The angle is reduced in 64 bits
+ * (exact to 2^-22 of a turn at any 32-bit position), the products are f32
+ * and rounded once.  Queries go to q_out (row stride q_stride; it may be qkv
+ * itself with the same stride, not another overlap), keys and values into
+ * the cache at slot[t]; a slot outside the cache is skipped.  Two tokens may
+ * not share a slot.
+ * freq: f64 [rot/2] on the device; position scalings for long contexts
+ * (stretched, by parts, another base) are choices of freq and factor.
+ * qkv, q_out, k, v 16-byte aligned, every stride a multiple of 8 elements
+ * (MISALIGNED otherwise).  INVALID_ARG for NULL pointers, T or Hq < 1, an odd
+ * rot or one outside [0, head_dim], strides shorter than a row, a bad cache;
+ * UNSUPPORTED for types or sizes beyond q4_kv_cache's limits.
+ */
+q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t Hq, int64_t rot,
+                         q4_rope_style style, const double *freq, float factor,
+                         const int32_t *position, const int64_t *slot, void *q_out,
+                         int64_t q_stride, const q4_kv_cache *cache, q4_stream_t stream);
+
+/*
+ * Attention of each request's new tokens over its cache.  Token row t =
+ * q_start[b] + i of request b (n = q_start[b + 1] - q_start[b] rows) stands
+ * at place p = kv_len[b] - n + i and sees the keys j <= p (j > p - window
+ * too, when window > 0) of the request:
+ *     o = sum_j exp(s_j - lse) v_j,  s_j = scale * q . k_j,  lse = log sum_j exp(s_j)
+ * with f32 sums.  Query head h reads KV head h / (Hq / heads).  A row that
+ * sees no key (p < 0) gets o = 0 and lse = -inf.  The request's last keys
+ * are its new ones: append first.  Only keys j < kv_len[b] are read; what
+ * lies behind them in a block never matters, NaN included.  (A NaN or
+ * infinity in a key or value that some row of the request does see may
+ * reach its other rows too.)
+ * q, o: T rows of Hq * head_dim elements (strides q_stride, o_stride), q of
+ * the cache's type, o of type ot (the cache's type or F32); rows that belong
+ * to no request are left alone.  lse: f32 [T][Hq] or NULL.
+ * table: [B][table_stride], `width` usable columns.  Lengths are cut to the
+ * table's width and T, keys in blocks outside [0, blocks) are taken as
+ * zeros with score 0, so bad device data cannot make the kernels read
+ * outside the buffers.
+ * max_fresh: the largest n of the step as far as the caller knows; it picks
+ * the kernel (few rows per KV head: streamed over the cache; many: tensor
+ * cores), any n is computed correctly with either.
+ * The keys of one (request, KV head) may be split over several CTAs; their
+ * partial sums meet in the workspace in a fixed order, so results do not
+ * depend on timing.  Workspace: q4_attention_workspace_bytes, zero-filled
+ * once; every completed call leaves its counters zero, so it serves any
+ * sequence of q4_attention calls on one stream, whatever their sizes, up to
+ * the bytes it holds.  It is not shared with the products' workspace (whose
+ * rule is stricter) nor with calls on other streams.
+ * INVALID_ARG for NULL pointers, sizes < 1, Hq not a multiple of heads, a
+ * non-finite scale, a negative window, a short workspace; UNSUPPORTED for
+ * types, T * Hq or sizes beyond 2^31 - 1, or a cache beyond q4_kv_cache's
+ * limits; MISALIGNED unless q, o, k, v, workspace are 16-byte aligned and
+ * strides multiples of 8.
+ */
+q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                       const q4_kv_cache *cache, const int32_t *table, int64_t table_stride,
+                       int64_t width, const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                       int64_t max_fresh, float scale, int64_t window, void *o, q4_dtype ot,
+                       int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes,
+                       q4_stream_t stream);
+
+/* Workspace bytes of q4_attention on the current device for steps of up to
+ * max_fresh new tokens per request, whatever their number and lengths (0 for
+ * invalid sizes). */
+size_t q4_attention_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads, int64_t head_dim);
+
 /* Synchronises `stream` and reports errors raised on the device since the
  * last check: Q4_ERR_BOUNDS when, in a library built with -DQ4_DEBUG, a
  * kernel computed a global store outside the buffer it writes (the store was

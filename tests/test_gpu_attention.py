@@ -1,0 +1,260 @@
+"""q4_attention against the definition in 64 bits: types, head layouts,
+lengths from one token up, odd sizes, both cache layouts, windows, rows that
+see nothing, stale NaN in the cache, strides, splits over CTAs, streams,
+graphs and a shared workspace.  Tolerances: serving_ref.py."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from serving_ref import Requests, assert_attention
+
+pytestmark = pytest.mark.gpu
+
+
+def q4():
+    import weight_only_int4_group_gb300 as m
+    return m
+
+
+def run(r, window=0, scale=None, out_dtype=None, ws=None, max_fresh=None, **kw):
+    m = q4()
+    cache = m.KVCache(r.k, r.v)
+    o, lse = m.attention(r.q, cache, r.table, r.q_start, r.kv_len, max_fresh or r.max_fresh, scale=scale,
+                         window=window, out_dtype=out_dtype, return_lse=True, ws=ws, **kw)
+    assert m.check() == m.OK
+    return o, lse
+
+
+def check(r, window=0, scale=None, **kw):
+    o, lse = run(r, window, scale, **kw)
+    assert_attention(o, lse, r.reference(scale, window), f"{r.lengths} window {window}")
+    return o, lse
+
+
+DT = [torch.bfloat16, torch.float16]
+# (cached, fresh) of each request
+FEW = [
+    [(0, 1)],
+    [(15, 1)], [(16, 1)], [(17, 1)],
+    [(127, 1)], [(128, 1)], [(129, 1)],
+    [(776, 1)],
+    [(5000, 1)],
+    [(3, 2), (100, 1), (0, 1), (31, 3)],
+    [(0, 0), (64, 1), (0, 0), (7, 1), (300, 0)],
+    [(i * 37 % 500, 1) for i in range(70)],
+]
+MANY = [
+    [(0, 17)], [(0, 128)], [(0, 129)], [(5, 64)],
+    [(0, 300)], [(777, 100)], [(1000, 257)],
+    [(0, 130), (50, 1), (0, 0), (400, 65), (3, 33)],
+    [(127, 1), (128, 128), (129, 2)],
+]
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("lengths", FEW, ids=lambda x: str(x)[:24])
+@pytest.mark.parametrize("heads,kv", [(8, 1), (4, 4), (14, 2)])
+def test_few_rows(lengths, heads, kv, dtype):
+    check(Requests(lengths, heads, kv, 128, 16, dtype, seed=len(lengths)))
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("lengths", MANY, ids=lambda x: str(x)[:24])
+@pytest.mark.parametrize("heads,kv", [(8, 1), (2, 2), (14, 2)])
+def test_many_rows(lengths, heads, kv, dtype):
+    check(Requests(lengths, heads, kv, 128, 16, dtype, seed=len(lengths)))
+
+
+@pytest.mark.parametrize("D", [8, 16, 40, 64, 72, 80, 96, 112, 120, 128])
+@pytest.mark.parametrize("lengths", [[(200, 1), (33, 1)], [(200, 40), (0, 150)]], ids=["few", "many"])
+def test_head_dims(D, lengths):
+    for dtype in DT:
+        check(Requests(lengths, 6, 2, D, 32, dtype, seed=D))
+
+
+@pytest.mark.parametrize("S", [16, 32, 48, 64, 80, 128, 256, 400])
+@pytest.mark.parametrize("token_major", [False, True])
+def test_block_sizes_and_layouts(S, token_major):
+    for lengths in ([(S, 1), (2 * S + 1, 1), (S - 2, 1)], [(S - 1, 70), (3 * S, 20), (0, 5)]):
+        check(Requests(lengths, 8, 2, 64, S, torch.float16, seed=S, token_major=token_major))
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 128, 129, 1000, 2 ** 31 - 1, 2 ** 40])
+@pytest.mark.parametrize("lengths", [[(500, 1), (20, 1), (0, 1)], [(500, 140), (0, 260), (90, 1)]],
+                         ids=["few", "many"])
+def test_windows(window, lengths):
+    check(Requests(lengths, 8, 2, 128, 16, torch.bfloat16, seed=3), window)
+
+
+@pytest.mark.parametrize("heads", [1, 3, 16, 17, 64, 100, 128, 200])
+def test_one_kv_head_for_all(heads):
+    for lengths in ([(90, 1), (300, 1)], [(90, 5), (0, 9)]):
+        check(Requests(lengths, heads, 1, 64, 16, torch.bfloat16, seed=heads))
+
+
+@pytest.mark.parametrize("lengths", [[(40, 1), (0, 2)], [(40, 30), (0, 200)]], ids=["few", "many"])
+@pytest.mark.parametrize("dtype", DT)
+def test_f32_output_and_scales(lengths, dtype):
+    r = Requests(lengths, 4, 2, 128, 16, dtype, seed=5)
+    for scale in (0.0, 0.3, -0.2, 1e-6):
+        o, lse = run(r, scale=scale, out_dtype=torch.float32)
+        assert o.dtype == torch.float32
+        assert_attention(o, lse, r.reference(scale), f"scale {scale}")
+
+
+@pytest.mark.parametrize("lengths", [[(400, 1), (70, 1)], [(400, 200), (70, 33)]], ids=["few", "many"])
+def test_peaked_and_growing_scores(lengths):
+    """Scores of hundreds whose maximum keeps rising along the keys, so that
+    earlier sums have to be scaled down again and again."""
+    r = Requests(lengths, 4, 1, 64, 16, torch.float16, seed=6, q_scale=8.0)
+    check(r)
+    r.q.fill_(1.0)
+    S = r.k.shape[2]
+    for b, L in enumerate(r.total):
+        for j in range(L):
+            r.k[r.table[b, j // S].item(), :, j % S] = j / 16
+    check(r)
+    check(r, scale=-0.125)
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_rows_that_see_nothing(many):
+    """More new tokens than the length says: the first rows stand before the
+    first key.  A length of 0 (a request that was not served) leaves all."""
+    m = q4()
+    n = 150 if many else 4
+    r = Requests([(0, n), (60, n), (0, n)], 4, 2, 64, 16, torch.bfloat16, seed=7)
+    short = [n - 3, 60 + n, 0]
+    r.kv_len.copy_(torch.tensor(short, dtype=torch.int32))
+    o, lse = run(r)
+    assert (o[:3] == 0).all() and torch.isinf(lse[:3]).all()
+    assert (o[2 * n:] == 0).all() and torch.isinf(lse[2 * n:]).all()
+    r.total = short
+    ref = r.reference()
+    assert_attention(o, lse, ref, "short")
+    assert m.check() == m.OK
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_blocks_outside_the_cache_read_as_zeros(many):
+    n = 40 if many else 1
+    r = Requests([(100, n)], 8, 1, 64, 16, torch.float16, seed=8)
+    bad = [0, 3]
+    for i, x in zip(bad, (-5, r.k.shape[0])):
+        blk = r.table[0, i].item()
+        r.k[blk] = 0
+        r.v[blk] = 0
+    ref = r.reference()
+    r.table[0, 0], r.table[0, 3] = -5, r.k.shape[0]
+    assert_attention(*run(r), ref, "bad blocks")
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_bad_lengths_stay_inside(many):
+    """Lengths past the table and row ranges past T are cut; rows of no
+    request keep what they held."""
+    m = q4()
+    n = 50 if many else 1
+    r = Requests([(30, n), (30, n)], 4, 1, 64, 16, torch.float16, seed=9, width_extra=0)
+    r.k.nan_to_num_(0.0)
+    r.v.nan_to_num_(0.0)
+    r.kv_len[1] = 2 ** 31 - 1
+    r.q_start[2] = 2 ** 31 - 1
+    o, _ = run(r)
+    assert torch.isfinite(o.float()).all()
+    r.q_start[:] = -7
+    out = torch.full_like(r.q, 3.0)
+    run(r, out=out)
+    assert (out == 3.0).all()
+    assert m.check() == m.OK
+
+
+@pytest.mark.parametrize("lengths", [[(300, 1), (50, 1)], [(300, 40), (50, 130)]], ids=["few", "many"])
+def test_strided_rows_and_padding(lengths):
+    """Queries inside wider rows (a qkv product's output), outputs inside
+    wider rows, and token rows behind the last request left alone."""
+    m = q4()
+    r = Requests(lengths, 8, 2, 64, 16, torch.bfloat16, seed=10)
+    T, pad = r.T, 3
+    wide = torch.full((T + pad, 8 * 64 + 256), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:T, :8 * 64] = r.q.view(T, -1)
+    q = wide[:, :8 * 64].unflatten(1, (8, 64))
+    ow = torch.full((T + pad, 8 * 64 + 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = ow[:, :8 * 64].unflatten(1, (8, 64))
+    m.attention(q, m.KVCache(r.k, r.v), r.table, r.q_start, r.kv_len, r.max_fresh, out=out)
+    assert m.check() == m.OK
+    assert_attention(out[:T], None, r.reference(), "strided")
+    assert (ow[T:] == 7.0).all() and (ow[:, 8 * 64:] == 7.0).all()
+
+
+@pytest.mark.parametrize("lengths", [[(9000, 1)], [(6000, 1), (10, 1), (3001, 1)], [(4000, 70)], [(3000, 300), (5, 1)]],
+                         ids=str)
+def test_split_items_are_deterministic(lengths):
+    r = Requests(lengths, 8, 1, 128, 16, torch.bfloat16, seed=11)
+    m = q4()
+    ws = m.attention_workspace(r.max_fresh, 8, 1, 128)
+    o, lse = check(r, ws=ws)
+    for _ in range(5):
+        o2, lse2 = run(r, ws=ws)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert not ws[:4096].any()
+
+
+def test_the_hint_only_picks_the_kernel():
+    for lengths in (FEW[9], MANY[7]):
+        r = Requests(lengths, 8, 2, 128, 16, torch.float16, seed=12)
+        for hint in (1, 2, 3, 40, 100000):
+            check(r, max_fresh=hint)
+
+
+def test_one_workspace_for_any_sequence_of_calls():
+    m = q4()
+    ws = m.attention_workspace(1000, 16, 2, 128)
+    for i, lengths in enumerate((MANY[7], FEW[11], MANY[5], FEW[8], MANY[7])):
+        r = Requests(lengths, 16, 2, (128, 64, 80)[i % 3], 16, DT[i % 2], seed=i)
+        check(r, ws=ws)
+
+
+def test_on_another_stream_and_in_a_graph():
+    m = q4()
+    for lengths in ([(700, 1), (40, 1)], [(700, 60), (40, 130)]):
+        r = Requests(lengths, 8, 2, 128, 16, torch.bfloat16, seed=13)
+        cache = m.KVCache(r.k, r.v)
+        ref = r.reference()
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        o = m.attention(r.q, cache, r.table, r.q_start, r.kv_len, r.max_fresh, stream=s)
+        assert m.check(s) == m.OK
+        assert_attention(o, None, ref, "stream")
+        ws = m.attention_workspace(r.max_fresh, 8, 2, 128)
+        out = torch.empty_like(r.q)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            m.attention(r.q, cache, r.table, r.q_start, r.kv_len, r.max_fresh, out=out, ws=ws)
+        for _ in range(2):
+            out.fill_(math.nan)
+            g.replay()
+            assert m.check() == m.OK
+            assert_attention(out, None, ref, "graph")
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 bytes and 2^31 elements: its first and last blocks."""
+    m = q4()
+    H, S, D = 8, 64, 128
+    blocks = (1 << 31) // (H * S * D) + 3
+    k = torch.zeros((blocks, H, S, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    for lengths in ([(90, 1)], [(90, 30)]):
+        r = Requests(lengths, H, H, D, S, torch.bfloat16, seed=14)
+        ids = r.table[0, :2].long() if lengths[0][1] == 1 else r.table[0, :2].long()
+        far = torch.tensor([blocks - 1, 0], device="cuda")
+        k[far], v[far] = r.k[ids], r.v[ids]
+        ref = r.reference()
+        r.k, r.v = k, v
+        r.table[0, :2] = far.int()
+        assert_attention(*run(r), ref, "far")

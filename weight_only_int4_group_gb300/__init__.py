@@ -8,13 +8,16 @@ fallback of any kind.
 Names follow include/q4.h: quantize, quantize_sym, repack, unpack, xsum,
 gemv, gemm, check, weight_bytes, gemv_workspace_bytes, gemm_workspace_bytes,
 repack_compact, unpack_compact, gemv_noalloc and the two timeout
-self-tests.  A QWeight carries its layout (TILED or COMPACT), and every
+self-tests; the serving operators cache_plan, rope_append and attention over
+a KVCache (rope_frequencies makes their angles).  A QWeight carries its layout (TILED or COMPACT), and every
 product call passes that layout and the buffer's byte count to the library,
 which refuses a mismatch.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 
@@ -36,6 +39,18 @@ LAYOUT_TILED, LAYOUT_COMPACT = 1, 2
 PATH_AUTO, PATH_FMA, PATH_MMA = 0, 1, 2
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+
+
+class _KVCacheArg(ctypes.Structure):
+    """q4_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int),
+                ("blocks", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("block_size", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
 
 
 class Q4Error(RuntimeError):
@@ -73,6 +88,12 @@ def _load():
     lib.q4_gemm.argtypes = prod
     lib.q4_gemm_timeout_selftest.argtypes = prod
     lib.q4_gemv_noalloc.argtypes = [P, S, I, I, I, P, S, Z, P, S, P]
+    F, C = ctypes.c_float, ctypes.POINTER(_KVCacheArg)
+    lib.q4_cache_plan.argtypes = [P, P, I, I, P, I, I, P, P, I, I, P, P, P, P, P, P]
+    lib.q4_rope_append.argtypes = [P, I, I, I, I, S, P, F, P, P, P, I, C, P]
+    lib.q4_attention.argtypes = [P, I, I, I, C, P, I, I, P, P, I, I, F, I, P, S, I, P, P, Z, P]
+    lib.q4_attention_workspace_bytes.argtypes = [I, I, I, I]
+    lib.q4_attention_workspace_bytes.restype = Z
     lib.q4_check.argtypes = [P]
     lib.q4_debug_bounds_selftest.argtypes = [P, P]
     lib.q4_status_str.argtypes = [S]
@@ -81,6 +102,7 @@ def _load():
     for f in ("q4_quantize", "q4_quantize_sym", "q4_repack", "q4_unpack", "q4_repack_compact",
               "q4_unpack_compact", "q4_xsum", "q4_gemv", "q4_gemv_path", "q4_gemv_timeout_selftest",
               "q4_gemm", "q4_gemm_timeout_selftest", "q4_gemv_noalloc", "q4_check",
+              "q4_cache_plan", "q4_rope_append", "q4_attention",
               "q4_debug_bounds_selftest"):
         getattr(lib, f).restype = S
     return lib
@@ -324,6 +346,232 @@ def gemm_timeout_selftest(x: torch.Tensor, qw: QWeight, out: torch.Tensor,
                                       qw.data.data_ptr(), qw.layout, qw.nbytes, out.data_ptr(),
                                       _DTYPE[out.dtype], wsp, wsb, _stream(stream)),
         "q4_gemm_timeout_selftest")
+
+
+# -------------------------------------------------- serving operators
+class KVCache:
+    """A blocked KV cache: k and v, [blocks][heads][block_size][head_dim] in
+    bf16 or f16, both with the same strides; the last dimension is contiguous
+    (a [blocks][block_size][heads][head_dim] buffer is passed as
+    ``t.transpose(1, 2)``).  The tensors are used where they lie."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        for t, n in ((k, "k"), (v, "v")):
+            if not t.is_cuda:
+                raise ValueError(f"{n} must be a CUDA tensor")
+            if t.dim() != 4 or t.dtype not in (torch.bfloat16, torch.float16):
+                raise ValueError(f"{n} must be a 4-D bfloat16 or float16 tensor")
+        if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must have the same shape, strides, type and device")
+        if k.shape[3] > 1 and k.stride(3) != 1:
+            raise ValueError("the last dimension must be contiguous")
+        self.k, self.v = k, v
+        self._arg = _KVCacheArg(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], *k.shape, *k.stride()[:3])
+
+    @classmethod
+    def empty(cls, blocks: int, heads: int, block_size: int, head_dim: int, dtype=torch.bfloat16,
+              device=None) -> "KVCache":
+        shape = (blocks, heads, block_size, head_dim)
+        device = device or torch.cuda.current_device()
+        return cls(torch.empty(shape, dtype=dtype, device=device),
+                   torch.empty(shape, dtype=dtype, device=device))
+
+    @property
+    def dtype(self):
+        return self.k.dtype
+
+    @property
+    def heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def block_size(self) -> int:
+        return self.k.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return self.k.shape[3]
+
+
+@dataclass
+class CachePlan:
+    """What q4_cache_plan writes for one step."""
+    q_start: torch.Tensor   # int32 [B + 1]
+    kv_len: torch.Tensor    # int32 [B]
+    position: torch.Tensor  # int32 [T]
+    slot: torch.Tensor      # int64 [T]
+    counts: torch.Tensor    # int32 [4]: rows used, tokens served, free blocks left, requests not served
+
+    @classmethod
+    def empty(cls, B: int, T: int, device=None) -> "CachePlan":
+        device = device or torch.cuda.current_device()
+
+        def i32(n):
+            return torch.empty(n, dtype=torch.int32, device=device)
+        return cls(i32(B + 1), i32(B), i32(T), torch.empty(T, dtype=torch.int64, device=device), i32(4))
+
+
+def _on(stream):
+    """What a call allocates itself (outputs, a workspace) belongs to the
+    stream it runs on, so that filling, use and reuse stay in order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
+
+
+def _array(t: torch.Tensor, name: str, dtype, shape=None):
+    _cuda(t, name)
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, has {tuple(t.shape)}")
+
+
+def _table(table: torch.Tensor, B: int):
+    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"table must be an int32 CUDA tensor of {B} rows")
+    if table.shape[1] > 1 and table.stride(1) != 1:
+        raise ValueError("the table's rows must be contiguous")
+    # the row stride of a single row is never used
+    return table.data_ptr(), max(table.stride(0), table.shape[1]) if B == 1 else table.stride(0), table.shape[1]
+
+
+def _rows(t: torch.Tensor, name: str, dtype):
+    """Token rows: 2-D or 3-D, contiguous but for the stride between rows."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
+    if t.dim() not in (2, 3) or t.shape[0] < 1 or not t[0].is_contiguous():
+        raise ValueError(f"{name} must be rows of contiguous elements")
+    n = t[0].numel()
+    return t.shape[0], n, max(t.stride(0), n) if t.shape[0] == 1 else t.stride(0)
+
+
+def cache_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor,
+               free_blocks: torch.Tensor, free_count: torch.Tensor, block_size: int, T: int,
+               out: CachePlan | None = None, stream=None) -> CachePlan:
+    """The step's plan from request lengths (q4_cache_plan): int32 ``cached``
+    and ``fresh`` [B]; ``table`` int32 [B][W] gets the blocks of the new tokens,
+    taken from the end of ``free_blocks`` int32, of which the first
+    ``free_count`` (int32 [1]) are free.  T token rows."""
+    B = cached.numel()
+    _array(cached, "cached", torch.int32)
+    _array(fresh, "fresh", torch.int32, tuple(cached.shape))
+    _array(free_blocks, "free_blocks", torch.int32)
+    _array(free_count, "free_count", torch.int32)
+    if free_count.numel() < 1:
+        raise ValueError("free_count must hold one number")
+    tp, ts, width = _table(table, B)
+    if out is None:
+        with _on(stream):
+            out = CachePlan.empty(B, T, cached.device)
+    for t, n, d, k in ((out.q_start, "q_start", torch.int32, B + 1), (out.kv_len, "kv_len", torch.int32, B),
+                       (out.position, "position", torch.int32, T), (out.slot, "slot", torch.int64, T),
+                       (out.counts, "counts", torch.int32, 4)):
+        _array(t, n, d, (k,))
+    _ok(_lib.q4_cache_plan(cached.data_ptr(), fresh.data_ptr(), B, block_size, tp, ts, width,
+                           free_blocks.data_ptr(), free_count.data_ptr(), free_blocks.numel(), T,
+                           out.q_start.data_ptr(), out.kv_len.data_ptr(), out.position.data_ptr(),
+                           out.slot.data_ptr(), out.counts.data_ptr(), _stream(stream)), "q4_cache_plan")
+    return out
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, stretch: float = 1.0, by_parts: bool = False,
+                     length: int = 4096, slow: float = 1.0, fast: float = 32.0, device=None):
+    """(freq f64 [rot / 2], factor) for rope_append: base ** (-2 i / rot), and
+    for contexts ``stretch`` times longer than ``length`` either every
+    frequency over ``stretch`` (position interpolation) or, ``by_parts``,
+    only those of pairs that turn fewer than ``slow`` times over ``length``
+    tokens; those that turn more than ``fast`` times are kept, with a linear
+    ramp between, and cos and sin grow by 0.1 ln(stretch) + 1 (the YaRN
+    paper's formulas, Peng et al. 2023)."""
+    if rot < 0 or rot % 2:
+        raise ValueError("rot must be even")
+    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    factor = 1.0
+    if by_parts:
+        factor = 0.1 * math.log(stretch) + 1.0 if stretch > 1.0 else 1.0
+        keep = [min(1.0, max(0.0, (length * x / (2 * math.pi) - slow) / (fast - slow))) for x in f]
+        f = [x / stretch * (1 - k) + x * k for x, k in zip(f, keep)]
+    else:
+        f = [x / stretch for x in f]
+    device = device or torch.cuda.current_device()
+    return torch.tensor(f, dtype=torch.float64, device=device), factor
+
+
+def rope_append(qkv: torch.Tensor, cache: KVCache, position: torch.Tensor, slot: torch.Tensor,
+                freq: torch.Tensor, heads: int, interleaved: bool = False, factor: float = 1.0,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotate the queries and keys of ``qkv`` [T][(heads + 2 * cache.heads) *
+    head_dim] and append keys and values to the cache (q4_rope_append).
+    2 * len(freq) elements of each head turn.  Returns the queries
+    [T][heads][head_dim] (``out`` may be the query part of qkv itself)."""
+    T, n, stride = _rows(qkv, "qkv", cache.dtype)
+    if n != (heads + 2 * cache.heads) * cache.head_dim:
+        raise ValueError(f"qkv rows have {n} elements, not (heads + 2 * cache heads) * head_dim")
+    _array(position, "position", torch.int32, (T,))
+    _array(slot, "slot", torch.int64, (T,))
+    _array(freq, "freq", torch.float64)
+    if out is None:
+        with _on(stream):
+            out = torch.empty((T, heads, cache.head_dim), dtype=qkv.dtype, device=qkv.device)
+    To, no, ostride = _rows(out, "out", cache.dtype)
+    if To != T or no != heads * cache.head_dim:
+        raise ValueError("out must be T rows of heads * head_dim")
+    _ok(_lib.q4_rope_append(qkv.data_ptr(), stride, T, heads, 2 * freq.numel(),
+                            ROPE_INTERLEAVED if interleaved else ROPE_HALF, freq.data_ptr(), factor,
+                            position.data_ptr(), slot.data_ptr(), out.data_ptr(), ostride,
+                            ctypes.byref(cache._arg), _stream(stream)), "q4_rope_append")
+    return out
+
+
+def attention_workspace_bytes(max_fresh: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_lib.q4_attention_workspace_bytes(max_fresh, heads, kv_heads, head_dim))
+
+
+def attention_workspace(max_fresh: int, heads: int, kv_heads: int, head_dim: int,
+                        device=None) -> torch.Tensor | None:
+    """A zero-filled workspace for attention (not shared with the products')."""
+    return _zeros(attention_workspace_bytes(max_fresh, heads, kv_heads, head_dim), device)
+
+
+def attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: torch.Tensor,
+              kv_len: torch.Tensor, max_fresh: int, scale: float | None = None, window: int = 0,
+              out: torch.Tensor | None = None, out_dtype=None, return_lse: bool = False,
+              lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Attention of each request's new tokens over its cache (q4_attention).
+
+    q [T][heads][head_dim]; request b's rows are q_start[b]..q_start[b + 1],
+    its keys the kv_len[b] first tokens of table row b, its own new ones last.
+    ``window`` > 0: each token sees that many keys, itself included.  Returns
+    o [T][heads][head_dim] (q's type, or float32), with ``return_lse`` also the
+    f32 log-sum-exp [T][heads]."""
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [T][heads][{cache.head_dim}]")
+    T, n, stride = _rows(q, "q", cache.dtype)
+    heads = q.shape[1]
+    B = kv_len.numel()
+    _array(kv_len, "kv_len", torch.int32, (B,))
+    _array(q_start, "q_start", torch.int32, (B + 1,))
+    tp, ts, width = _table(table, B)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, heads, cache.head_dim), dtype=out_dtype or q.dtype, device=q.device)
+        if return_lse and lse is None:
+            lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = attention_workspace(max_fresh, heads, cache.heads, cache.head_dim, q.device)
+    To, no, ostride = _rows(out, "out", out.dtype)
+    if To != T or no != n:
+        raise ValueError("out must be T rows of heads * head_dim")
+    if lse is not None:
+        _array(lse, "lse", torch.float32, (T, heads))
+    wsp, wsb = _ws(ws)
+    _ok(_lib.q4_attention(q.data_ptr(), stride, T, heads, ctypes.byref(cache._arg), tp, ts, width,
+                          q_start.data_ptr(), kv_len.data_ptr(), B, max_fresh,
+                          cache.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                          _DTYPE.get(out.dtype, -1), ostride, 0 if lse is None else lse.data_ptr(),
+                          wsp, wsb, _stream(stream)), "q4_attention")
+    return (out, lse) if return_lse or lse is not None else out
 
 
 def check(stream=None) -> int:

@@ -14,6 +14,7 @@ when Q4_LIBRARY names it.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import glob
 import os
 import platform
 import shutil
@@ -35,6 +36,8 @@ SOURCES = {
     "gemv.cu": [],
     "gemm_tc.cu": [],
     "noalloc.cu": [],
+    "cache.cu": [],
+    "attention.cu": [],
 }
 
 
@@ -47,7 +50,7 @@ def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
     t = os.path.getmtime(obj)
-    deps = [src, os.path.join(CSRC, "common.cuh"), os.path.join(ROOT, "include", "q4.h")]
+    deps = [src, *glob.glob(os.path.join(CSRC, "*.cuh")), os.path.join(ROOT, "include", "q4.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

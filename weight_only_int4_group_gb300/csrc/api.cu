@@ -5,9 +5,10 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <cmath>
 #include <mutex>
 
-#include "common.cuh"
+#include "serve.cuh"
 
 __device__ unsigned int g_q4_error = 0u;
 
@@ -135,6 +136,42 @@ static q4_status gemv_common(const void *x, q4_dtype xt, int64_t M, int64_t N, i
     a.debug_no_copy = debug_no_copy;
     const cudaError_t e = gemv_launch(plan, a, stream);
     return e == cudaSuccess ? Q4_OK : cuda_fail(e);
+}
+
+
+// ------------------------------------------------------- serving operators
+constexpr int64_t INT_MOST = 2147483647;
+
+// The cache's fields, in the order that decides which status is returned.
+static q4_status cache_ok(const q4_kv_cache *c)
+{
+    if (!c || !c->k || !c->v || c->blocks < 1 || c->heads < 1 || c->block_size < 1 || c->head_dim < 1)
+        return Q4_ERR_INVALID_ARG;
+    if (c->type != Q4_BF16 && c->type != Q4_F16) return Q4_ERR_UNSUPPORTED;
+    if (c->blocks > INT_MOST || c->heads > 65536 || c->block_size > 65536 || c->block_size % 16 ||
+        c->head_dim > 128 || c->head_dim % 8)
+        return Q4_ERR_UNSUPPORTED;
+    constexpr int64_t most = 1LL << 40;  // elements; keeps every offset far inside 64 bits
+    if (c->block_stride < 0 || c->head_stride < 0 || c->token_stride < c->head_dim ||
+        c->block_stride > most || c->head_stride > most || c->token_stride > most)
+        return Q4_ERR_INVALID_ARG;
+    // Of several blocks, heads or tokens none may share its elements with
+    // another: sorted by stride, each dimension steps over the ones inside.
+    struct {
+        int64_t n, stride;
+    } d[3] = {{c->block_size, c->token_stride}, {c->heads, c->head_stride}, {c->blocks, c->block_stride}};
+    std::sort(d, d + 3, [](const auto &x, const auto &y) { return x.stride < y.stride; });
+    int64_t extent = c->head_dim;
+    for (const auto &x : d) {
+        if (x.n == 1) continue;
+        if (x.stride < extent) return Q4_ERR_INVALID_ARG;
+        if (x.stride > (1LL << 60) / x.n) return Q4_ERR_UNSUPPORTED;
+        extent += (x.n - 1) * x.stride;
+    }
+    if (!aligned16(c->k) || !aligned16(c->v) || c->block_stride % 8 || c->head_stride % 8 ||
+        c->token_stride % 8)
+        return Q4_ERR_MISALIGNED;
+    return Q4_OK;
 }
 
 }  // namespace q4
@@ -316,6 +353,165 @@ q4_status q4_gemm_timeout_selftest(const void *x, q4_dtype xt, int64_t M, int64_
 {
     return gemm_common(x, xt, M, N, K, qw, layout, qw_bytes, y, yt, workspace, workspace_bytes,
                        stream, 1, 20000000ull);
+}
+
+q4_status q4_cache_plan(const int32_t *cached, const int32_t *fresh, int64_t B, int64_t block_size,
+                        int32_t *table, int64_t table_stride, int64_t width,
+                        const int32_t *free_blocks, const int32_t *free_count,
+                        int64_t free_capacity, int64_t T, int32_t *q_start, int32_t *kv_len,
+                        int32_t *position, int64_t *slot, int32_t *counts, q4_stream_t stream)
+{
+    if (!cached || !fresh || !table || !free_blocks || !free_count || !q_start || !kv_len ||
+        !position || !slot || !counts)
+        return Q4_ERR_INVALID_ARG;
+    if (B < 1 || block_size < 1 || width < 1 || table_stride < width || free_capacity < 1 || T < 1)
+        return Q4_ERR_INVALID_ARG;
+    if (B > Q4_PLAN_MAX_REQUESTS || T > INT_MOST || free_capacity > INT_MOST ||
+        table_stride > (1LL << 40) || width > INT_MOST / block_size)
+        return Q4_ERR_UNSUPPORTED;
+    PlanArgs a{};
+    a.cached = cached;
+    a.fresh = fresh;
+    a.B = static_cast<int>(B);
+    a.S = static_cast<int>(block_size);
+    a.table = table;
+    a.table_stride = table_stride;
+    a.width = static_cast<int>(width);
+    a.free_blocks = free_blocks;
+    a.free_count = free_count;
+    a.free_capacity = static_cast<int>(free_capacity);
+    a.T = static_cast<int>(T);
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.position = position;
+    a.slot = slot;
+    a.counts = counts;
+    a.err = debug_err();
+    const cudaError_t e = cache_plan_launch(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q4_OK : cuda_fail(e);
+}
+
+q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t Hq, int64_t rot,
+                         q4_rope_style style, const double *freq, float factor,
+                         const int32_t *position, const int64_t *slot, void *q_out,
+                         int64_t q_stride, const q4_kv_cache *cache, q4_stream_t stream)
+{
+    if (!qkv || !position || !slot || !q_out) return Q4_ERR_INVALID_ARG;
+    const q4_status st = cache_ok(cache);
+    if (st != Q4_OK) return st;
+    if (T < 1 || Hq < 1 || rot < 0 || rot > cache->head_dim || rot % 2 || (rot > 0 && !freq))
+        return Q4_ERR_INVALID_ARG;
+    if (style != Q4_ROPE_HALF && style != Q4_ROPE_INTERLEAVED) return Q4_ERR_INVALID_ARG;
+    if (T > INT_MOST || Hq > 65536) return Q4_ERR_UNSUPPORTED;
+    if (qkv_stride < (Hq + 2 * cache->heads) * cache->head_dim || q_stride < Hq * cache->head_dim)
+        return Q4_ERR_INVALID_ARG;
+    if (qkv_stride > (1LL << 30) || q_stride > (1LL << 30)) return Q4_ERR_UNSUPPORTED;
+    if (!aligned16(qkv) || !aligned16(q_out) || qkv_stride % 8 || q_stride % 8)
+        return Q4_ERR_MISALIGNED;
+    RopeArgs a{};
+    a.qkv = static_cast<const uint16_t *>(qkv);
+    a.qkv_stride = qkv_stride;
+    a.T = static_cast<int>(T);
+    a.Hq = static_cast<int>(Hq);
+    a.Hkv = static_cast<int>(cache->heads);
+    a.D = static_cast<int>(cache->head_dim);
+    a.rot = static_cast<int>(rot);
+    a.freq = freq;
+    a.factor = factor;
+    a.position = position;
+    a.slot = slot;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.q_stride = q_stride;
+    a.k = static_cast<uint16_t *>(cache->k);
+    a.v = static_cast<uint16_t *>(cache->v);
+    a.block_stride = cache->block_stride;
+    a.head_stride = cache->head_stride;
+    a.token_stride = cache->token_stride;
+    a.blocks = static_cast<int>(cache->blocks);
+    a.S = static_cast<int>(cache->block_size);
+    a.err = debug_err();
+    const cudaError_t e = rope_append_launch(a, cache->type == Q4_F16, style == Q4_ROPE_INTERLEAVED,
+                                             reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q4_OK : cuda_fail(e);
+}
+
+static bool attention_sizes_ok(int64_t max_fresh, int64_t Hq, int64_t heads, int64_t head_dim)
+{
+    return max_fresh >= 1 && max_fresh <= INT_MOST && heads >= 1 && Hq >= heads && Hq % heads == 0 &&
+           Hq <= 65536 && head_dim >= 8 && head_dim <= 128 && head_dim % 8 == 0;
+}
+
+size_t q4_attention_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads, int64_t head_dim)
+{
+    if (!attention_sizes_ok(max_fresh, Hq, heads, head_dim)) return 0;
+    const DevInfo *d = dev_info();
+    if (!d) return 0;
+    return attention_plan(max_fresh, Hq / heads, head_dim, d->sm_count).workspace;
+}
+
+q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                       const q4_kv_cache *cache, const int32_t *table, int64_t table_stride,
+                       int64_t width, const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                       int64_t max_fresh, float scale, int64_t window, void *o, q4_dtype ot,
+                       int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes,
+                       q4_stream_t stream)
+{
+    if (!q || !table || !q_start || !kv_len || !o) return Q4_ERR_INVALID_ARG;
+    const q4_status st = cache_ok(cache);
+    if (st != Q4_OK) return st;
+    if (T < 1 || B < 1 || Hq < 1 || Hq % cache->heads || max_fresh < 1 || width < 1 ||
+        table_stride < width || window < 0 || !std::isfinite(scale))
+        return Q4_ERR_INVALID_ARG;
+    if (ot != Q4_F32 && ot != cache->type) return Q4_ERR_UNSUPPORTED;
+    if (!attention_sizes_ok(max_fresh, Hq, cache->heads, cache->head_dim) || T > INT_MOST / Hq ||
+        B > INT_MOST || table_stride > (1LL << 40) || width > INT_MOST / cache->block_size)
+        return Q4_ERR_UNSUPPORTED;
+    const int64_t row = Hq * cache->head_dim;
+    if (q_stride < row || o_stride < row) return Q4_ERR_INVALID_ARG;
+    if (q_stride > (1LL << 30) || o_stride > (1LL << 30)) return Q4_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || q_stride % 8 || o_stride % 8 ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return Q4_ERR_MISALIGNED;
+    const DevInfo *d = dev_info();
+    if (!d) return cuda_fail(cudaGetLastError());
+    const AttnPlan plan = attention_plan(max_fresh, Hq / cache->heads, cache->head_dim, d->sm_count);
+    if (!workspace || workspace_bytes < plan.workspace) return Q4_ERR_INVALID_ARG;
+    AttnArgs a{};
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(cache->k);
+    a.v = static_cast<const uint16_t *>(cache->v);
+    a.o = o;
+    a.ot = ot;
+    a.lse = lse;
+    a.q_stride = q_stride;
+    a.o_stride = o_stride;
+    a.block_stride = cache->block_stride;
+    a.head_stride = cache->head_stride;
+    a.token_stride = cache->token_stride;
+    a.table = table;
+    a.table_stride = table_stride;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.T = static_cast<int>(T);
+    a.B = static_cast<int>(B);
+    a.Hq = static_cast<int>(Hq);
+    a.Hkv = static_cast<int>(cache->heads);
+    a.GQ = static_cast<int>(Hq / cache->heads);
+    a.D = static_cast<int>(cache->head_dim);
+    a.S = static_cast<int>(cache->block_size);
+    a.blocks = static_cast<int>(cache->blocks);
+    a.width = static_cast<int>(width);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    // a window that no length reaches hides nothing
+    a.window = window > INT_MOST ? 0 : static_cast<int>(window);
+    a.count = static_cast<unsigned int *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ATTN_COUNTER_BYTES);
+    a.count_len = plan.grid;
+    a.part_len = static_cast<int64_t>((plan.workspace - ATTN_COUNTER_BYTES) / sizeof(float));
+    a.err = d->err;
+    const cudaError_t e = attention_launch(plan, a, cache->type == Q4_F16,
+                                           reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q4_OK : cuda_fail(e);
 }
 
 q4_status q4_check(q4_stream_t stream)

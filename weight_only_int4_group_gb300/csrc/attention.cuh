@@ -1,0 +1,248 @@
+// attention.cuh -- what the two attention kernels share: the sequence of
+// work units and how a CTA finds its range of it, and the final store.
+#pragma once
+
+#include "serve.cuh"
+
+namespace q4 {
+
+// A request's new tokens and length as the kernels use them: cut to the token
+// rows and to the table's width, so that no index leaves its buffer whatever
+// the device arrays hold.
+__device__ __forceinline__ void request(const AttnArgs &a, int b, int &t0, int &n, int &kv)
+{
+    t0 = min(max(__ldg(a.q_start + b), 0), a.T);
+    n = max(0, min(max(__ldg(a.q_start + b + 1), 0), a.T) - t0);
+    kv = static_cast<int>(min(static_cast<int64_t>(max(__ldg(a.kv_len + b), 0)),
+                              static_cast<int64_t>(a.width) * a.S));
+}
+
+__device__ __forceinline__ int row_tiles(int n, int GQ, int R)
+{
+    return static_cast<int>((static_cast<int64_t>(n) * GQ + R - 1) / R);
+}
+
+// Rows [row0, row1) of a request's n * GQ rows and the units of TK keys they
+// see: units [kt0, kt0 + units) of the request's keys; one (all masked) when
+// they see none, so that their empty results are written.
+template <int R, int TK>
+struct Span {
+    int t0, kv, base, row0, row1, kt0, units;
+    __device__ __forceinline__ Span(const AttnArgs &a, int b, int rt)
+    {
+        int n;
+        request(a, b, t0, n, kv);
+        init(a, n, rt);
+    }
+    __device__ __forceinline__ Span(const AttnArgs &a, int n, int kv_, int rt) : t0(0), kv(kv_)
+    {
+        init(a, n, rt);
+    }
+
+private:
+    __device__ __forceinline__ void init(const AttnArgs &a, int n, int rt)
+    {
+        base = kv - n;
+        row0 = rt * R;
+        row1 = static_cast<int>(min(static_cast<int64_t>(n) * a.GQ, static_cast<int64_t>(row0) + R));
+        const int lo_t = row0 / a.GQ, hi_t = (row1 - 1) / a.GQ;
+        const int hi = base + hi_t + 1;
+        const int64_t first = static_cast<int64_t>(base) + lo_t - a.window + 1;
+        const int lo = a.window > 0 && first > 0 ? static_cast<int>(first) : 0;
+        kt0 = lo / TK;
+        units = hi > lo ? (hi - 1) / TK - kt0 + 1 : 1;
+    }
+};
+
+struct Item {
+    int b, rt, head;
+    __device__ __forceinline__ void next(const AttnArgs &a, int R)
+    {
+        if (++head < a.Hkv) return;
+        head = 0;
+        int t0, n, kv;
+        request(a, b, t0, n, kv);
+        if (++rt < row_tiles(n, a.GQ, R)) return;
+        rt = 0;
+        for (++b; b < a.B; ++b) {
+            request(a, b, t0, n, kv);
+            if (n > 0) return;
+        }
+    }
+};
+
+struct Range {
+    int64_t u0, u1, total;  // the CTA's units and all units of the call
+    int G;                  // CTAs that share them
+    Item first;             // item of unit u0
+    int kt;                 // u0 within that item
+};
+
+struct LocateScratch {
+    int64_t slab[32];
+    Range r;
+};
+
+// CTA holding unit i of T units cut into G equal ranges [c * T / G, (c + 1) * T / G).
+__device__ __forceinline__ int owner_of(int64_t i, int64_t T, int64_t G)
+{
+    return static_cast<int>(((i + 1) * G - 1) / T);
+}
+
+// Units of all row tiles of request b for one KV head.  Lanes hold one
+// request each; requests of many row tiles are summed by the whole warp.
+template <int R, int TK>
+__device__ __forceinline__ int64_t request_units(const AttnArgs &a, int b, bool in)
+{
+    int t0, n = 0, kv = 0;
+    if (in) request(a, b, t0, n, kv);
+    const int nt = row_tiles(n, a.GQ, R);
+    int64_t sum = 0;
+    if (nt <= 2)
+        for (int rt = 0; rt < nt; ++rt) sum += Span<R, TK>(a, n, kv, rt).units;
+    unsigned big = __ballot_sync(0xffffffffu, nt > 2);
+    const int lane = threadIdx.x & 31;
+    while (big) {
+        const int src = __ffs(big) - 1;
+        big &= big - 1;
+        const int n2 = __shfl_sync(0xffffffffu, n, src), kv2 = __shfl_sync(0xffffffffu, kv, src),
+                  nt2 = __shfl_sync(0xffffffffu, nt, src);
+        int64_t part = 0;
+        for (int rt = lane; rt < nt2; rt += 32) part += Span<R, TK>(a, n2, kv2, rt).units;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+        if (lane == src) sum = part;
+    }
+    return sum;
+}
+
+// The CTA's equal share of the call's units, and where it begins.  Every
+// thread of the CTA calls it (NW warps; two barriers); all get the result.
+// Warps sum slabs of requests, then the warp whose slab holds the CTA's first
+// unit walks it again.
+template <int R, int TK, int NW>
+__device__ Range cta_range(const AttnArgs &a, LocateScratch &ls)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b0 = static_cast<int>(static_cast<int64_t>(a.B) * warp / NW),
+              b1 = static_cast<int>(static_cast<int64_t>(a.B) * (warp + 1) / NW);
+    int64_t slab = 0;
+    for (int b = b0; b < b1; b += 32) slab += request_units<R, TK>(a, b + lane, b + lane < b1);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) slab += __shfl_xor_sync(0xffffffffu, slab, d);
+    if (lane == 0) ls.slab[warp] = slab;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) before += ls.slab[w];
+        all += ls.slab[w];
+    }
+    const int64_t total = all * a.Hkv;
+    // no CTA between two others is left without a unit (the pieces of an item
+    // are counted by their CTAs)
+    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const bool mine_any = static_cast<int>(blockIdx.x) < G;
+    const int64_t u0 = mine_any ? blockIdx.x * total / G : 0, u1 = mine_any ? (blockIdx.x + 1) * total / G : 0;
+    int64_t left = u0 - before * a.Hkv;  // units to pass from the slab's start
+    if (u0 < u1 && left >= 0 && left < slab * a.Hkv) {
+        for (int b = b0; b < b1; b += 32) {
+            const int64_t mine = request_units<R, TK>(a, b + lane, b + lane < b1) * a.Hkv;
+            int64_t incl = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t p = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += p;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, incl > left);
+            if (!past) {
+                left -= __shfl_sync(0xffffffffu, incl, 31);
+                continue;
+            }
+            const int src = __ffs(past) - 1;
+            left -= __shfl_sync(0xffffffffu, incl - mine, src);
+            // within the request: row tiles, 32 at a time
+            int t0, n, kv;
+            request(a, b + src, t0, n, kv);
+            const int nt = row_tiles(n, a.GQ, R);
+            for (int rt = 0; rt < nt; rt += 32) {
+                const int64_t m2 = rt + lane < nt ? static_cast<int64_t>(Span<R, TK>(a, n, kv, rt + lane).units) * a.Hkv : 0;
+                int64_t in2 = m2;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int64_t p = __shfl_up_sync(0xffffffffu, in2, d);
+                    if (lane >= d) in2 += p;
+                }
+                const unsigned past2 = __ballot_sync(0xffffffffu, in2 > left);
+                if (!past2) {
+                    left -= __shfl_sync(0xffffffffu, in2, 31);
+                    continue;
+                }
+                const int s2 = __ffs(past2) - 1;
+                left -= __shfl_sync(0xffffffffu, in2 - m2, s2);
+                if (lane == 0) {
+                    const int64_t per = Span<R, TK>(a, n, kv, rt + s2).units;
+                    ls.r.first.b = b + src;
+                    ls.r.first.rt = rt + s2;
+                    ls.r.first.head = static_cast<int>(left / per);
+                    ls.r.kt = static_cast<int>(left % per);
+                }
+                break;
+            }
+            break;
+        }
+    }
+    __syncthreads();
+    Range r = ls.r;
+    r.u0 = u0;
+    r.u1 = u1;
+    r.total = total;
+    r.G = G;
+    return r;
+}
+
+// 2^x to about 2 ulp; 0 below the normal range.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if (F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Dims d..d + 3 of one row: the accumulated sum over its total, rounded once;
+// the row's log-sum-exp beside dim 0.  top is in units of log 2.
+template <bool F16>
+__device__ __forceinline__ void finish_row(const AttnArgs &a, const Item &it, int t0, int row, int d,
+                                           const float (&acc)[4], float top, float sum)
+{
+    if (d >= a.D) return;
+    const int t = t0 + row / a.GQ, h = it.head * a.GQ + row % a.GQ;
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const int64_t at = t * a.o_stride + static_cast<int64_t>(h) * a.D + d;
+    if (store_ok(at + 3, static_cast<int64_t>(a.T - 1) * a.o_stride + static_cast<int64_t>(a.Hq) * a.D, a.err)) {
+        if (a.ot == Q4_F32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at) =
+                make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+        else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + at) =
+                make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
+    }
+    if (a.lse && d == 0) {
+        const int64_t l = static_cast<int64_t>(t) * a.Hq + h;
+        if (store_ok(l, static_cast<int64_t>(a.T) * a.Hq, a.err))
+            a.lse[l] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
+}
+
+}  // namespace q4
