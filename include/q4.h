@@ -462,6 +462,20 @@ q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
                        int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes,
                        q4_stream_t stream);
 
+/* Diagnostic for the bounded waits of q4_attention's tensor-core kernel:
+ * launches it with its copies switched off, so its waits run out after 20 ms;
+ * every role then stops, tensor memory is freed and the kernel returns
+ * without writing o.  A following q4_check(stream) returns Q4_ERR_TIMEOUT;
+ * the context stays usable.  UNSUPPORTED for sizes that the streaming kernel
+ * takes (it waits on nothing but its own copies). */
+q4_status q4_attention_timeout_selftest(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                                        const q4_kv_cache *cache, const int32_t *table,
+                                        int64_t table_stride, int64_t width, const int32_t *q_start,
+                                        const int32_t *kv_len, int64_t B, int64_t max_fresh,
+                                        float scale, int64_t window, void *o, q4_dtype ot,
+                                        int64_t o_stride, float *lse, void *workspace,
+                                        size_t workspace_bytes, q4_stream_t stream);
+
 /* Workspace bytes of q4_attention on the current device for steps of up to
  * max_fresh new tokens per request, whatever their number and lengths (0 for
  * invalid sizes). */

@@ -258,3 +258,21 @@ def test_offsets_past_32_bits():
         r.k, r.v = k, v
         r.table[0, :2] = far.int()
         assert_attention(*run(r), ref, "far")
+
+
+def test_bounded_waits_report_a_timeout():
+    """With its copies switched off the tensor-core kernel stops after its
+    wait limit, writes nothing, and the same SMs' tensor memory works again."""
+    m = q4()
+    r = Requests([(300, 60), (0, 200)], 8, 2, 128, 16, torch.bfloat16, seed=15)
+    ws = m.attention_workspace(r.max_fresh, 8, 2, 128)
+    out = torch.full_like(r.q, 5.0)
+    m.attention_timeout_selftest(r.q, m.KVCache(r.k, r.v), r.table, r.q_start, r.kv_len, r.max_fresh, out, ws)
+    assert m.check() == m.ERR_TIMEOUT
+    assert (out == 5.0).all()
+    ws.zero_()
+    check(r, ws=ws)
+    one = Requests([(30, 1)], 8, 2, 128, 16, torch.bfloat16, seed=15)
+    with pytest.raises(m.Q4Error):
+        m.attention_timeout_selftest(one.q, m.KVCache(one.k, one.v), one.table, one.q_start, one.kv_len, 1,
+                                        torch.empty_like(one.q), ws)

@@ -92,6 +92,7 @@ def _load():
     lib.q4_cache_plan.argtypes = [P, P, I, I, P, I, I, P, P, I, I, P, P, P, P, P, P]
     lib.q4_rope_append.argtypes = [P, I, I, I, I, S, P, F, P, P, P, I, C, P]
     lib.q4_attention.argtypes = [P, I, I, I, C, P, I, I, P, P, I, I, F, I, P, S, I, P, P, Z, P]
+    lib.q4_attention_timeout_selftest.argtypes = lib.q4_attention.argtypes
     lib.q4_attention_workspace_bytes.argtypes = [I, I, I, I]
     lib.q4_attention_workspace_bytes.restype = Z
     lib.q4_check.argtypes = [P]
@@ -103,6 +104,7 @@ def _load():
               "q4_unpack_compact", "q4_xsum", "q4_gemv", "q4_gemv_path", "q4_gemv_timeout_selftest",
               "q4_gemm", "q4_gemm_timeout_selftest", "q4_gemv_noalloc", "q4_check",
               "q4_cache_plan", "q4_rope_append", "q4_attention",
+              "q4_attention_timeout_selftest",
               "q4_debug_bounds_selftest"):
         getattr(lib, f).restype = S
     return lib
@@ -537,7 +539,8 @@ def attention_workspace(max_fresh: int, heads: int, kv_heads: int, head_dim: int
 def attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: torch.Tensor,
               kv_len: torch.Tensor, max_fresh: int, scale: float | None = None, window: int = 0,
               out: torch.Tensor | None = None, out_dtype=None, return_lse: bool = False,
-              lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+              lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None,
+              _call=_lib.q4_attention):
     """Attention of each request's new tokens over its cache (q4_attention).
 
     q [T][heads][head_dim]; request b's rows are q_start[b]..q_start[b + 1],
@@ -566,12 +569,19 @@ def attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: tor
     if lse is not None:
         _array(lse, "lse", torch.float32, (T, heads))
     wsp, wsb = _ws(ws)
-    _ok(_lib.q4_attention(q.data_ptr(), stride, T, heads, ctypes.byref(cache._arg), tp, ts, width,
+    _ok(_call(q.data_ptr(), stride, T, heads, ctypes.byref(cache._arg), tp, ts, width,
                           q_start.data_ptr(), kv_len.data_ptr(), B, max_fresh,
                           cache.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
                           _DTYPE.get(out.dtype, -1), ostride, 0 if lse is None else lse.data_ptr(),
                           wsp, wsb, _stream(stream)), "q4_attention")
     return (out, lse) if return_lse or lse is not None else out
+
+
+def attention_timeout_selftest(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: torch.Tensor,
+                               kv_len: torch.Tensor, max_fresh: int, out: torch.Tensor, ws: torch.Tensor,
+                               stream=None) -> None:
+    attention(q, cache, table, q_start, kv_len, max_fresh, out=out, ws=ws, stream=stream,
+              _call=_lib.q4_attention_timeout_selftest)
 
 
 def check(stream=None) -> int:

@@ -38,6 +38,7 @@ SOURCES = {
     "noalloc.cu": [],
     "cache.cu": [],
     "attention.cu": [],
+    "attention_tc.cu": [],
 }
 
 

@@ -449,12 +449,13 @@ size_t q4_attention_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads
     return attention_plan(max_fresh, Hq / heads, head_dim, d->sm_count).workspace;
 }
 
-q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
-                       const q4_kv_cache *cache, const int32_t *table, int64_t table_stride,
-                       int64_t width, const int32_t *q_start, const int32_t *kv_len, int64_t B,
-                       int64_t max_fresh, float scale, int64_t window, void *o, q4_dtype ot,
-                       int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes,
-                       q4_stream_t stream)
+static q4_status attention_common(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                                  const q4_kv_cache *cache, const int32_t *table,
+                                  int64_t table_stride, int64_t width, const int32_t *q_start,
+                                  const int32_t *kv_len, int64_t B, int64_t max_fresh, float scale,
+                                  int64_t window, void *o, q4_dtype ot, int64_t o_stride, float *lse,
+                                  void *workspace, size_t workspace_bytes, q4_stream_t stream,
+                                  int debug_no_copy, uint64_t wait_ns)
 {
     if (!q || !table || !q_start || !kv_len || !o) return Q4_ERR_INVALID_ARG;
     const q4_status st = cache_ok(cache);
@@ -475,6 +476,7 @@ q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
     const DevInfo *d = dev_info();
     if (!d) return cuda_fail(cudaGetLastError());
     const AttnPlan plan = attention_plan(max_fresh, Hq / cache->heads, cache->head_dim, d->sm_count);
+    if (debug_no_copy && !plan.tc) return Q4_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < plan.workspace) return Q4_ERR_INVALID_ARG;
     AttnArgs a{};
     a.q = static_cast<const uint16_t *>(q);
@@ -506,12 +508,39 @@ q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
     a.window = window > INT_MOST ? 0 : static_cast<int>(window);
     a.count = static_cast<unsigned int *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ATTN_COUNTER_BYTES);
-    a.count_len = plan.grid;
+    a.count_len = ATTN_COUNTER_BYTES / sizeof(unsigned int);
+    a.wait_ns = wait_ns;
+    a.debug_no_copy = debug_no_copy;
     a.part_len = static_cast<int64_t>((plan.workspace - ATTN_COUNTER_BYTES) / sizeof(float));
     a.err = d->err;
     const cudaError_t e = attention_launch(plan, a, cache->type == Q4_F16,
                                            reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? Q4_OK : cuda_fail(e);
+}
+
+q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                       const q4_kv_cache *cache, const int32_t *table, int64_t table_stride,
+                       int64_t width, const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                       int64_t max_fresh, float scale, int64_t window, void *o, q4_dtype ot,
+                       int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes,
+                       q4_stream_t stream)
+{
+    return attention_common(q, q_stride, T, Hq, cache, table, table_stride, width, q_start, kv_len, B,
+                            max_fresh, scale, window, o, ot, o_stride, lse, workspace, workspace_bytes,
+                            stream, 0, 2000000000ull);
+}
+
+q4_status q4_attention_timeout_selftest(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                                        const q4_kv_cache *cache, const int32_t *table,
+                                        int64_t table_stride, int64_t width, const int32_t *q_start,
+                                        const int32_t *kv_len, int64_t B, int64_t max_fresh,
+                                        float scale, int64_t window, void *o, q4_dtype ot,
+                                        int64_t o_stride, float *lse, void *workspace,
+                                        size_t workspace_bytes, q4_stream_t stream)
+{
+    return attention_common(q, q_stride, T, Hq, cache, table, table_stride, width, q_start, kv_len, B,
+                            max_fresh, scale, window, o, ot, o_stride, lse, workspace, workspace_bytes,
+                            stream, 1, 20000000ull);
 }
 
 q4_status q4_check(q4_stream_t stream)

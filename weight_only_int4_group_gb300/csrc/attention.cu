@@ -335,17 +335,20 @@ cudaError_t launch(const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 
 }  // namespace
 
-AttnPlan attention_plan(int64_t, int64_t, int64_t D, int sm_count)
+AttnPlan attention_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count)
 {
     AttnPlan p{};
-    p.grid = std::min<int>(sm_count, ATTN_COUNTER_BYTES / sizeof(unsigned int));
+    p.grid = std::min<int>(sm_count, ATTN_COUNTER_BYTES / sizeof(unsigned int) / 2);
+    p.tc = max_fresh > R / GQ;
     const size_t slot = R * ((D > 64 ? 128 : 64) + 2) * sizeof(float);
-    p.workspace = ATTN_COUNTER_BYTES + 2 * static_cast<size_t>(p.grid) * slot;
+    const size_t part = p.tc ? attention_tc_part_bytes(D, p.grid) : 2 * static_cast<size_t>(p.grid) * slot;
+    p.workspace = ATTN_COUNTER_BYTES + part;
     return p;
 }
 
 cudaError_t attention_launch(const AttnPlan &p, const AttnArgs &a, bool f16, cudaStream_t s)
 {
+    if (p.tc) return attention_tc_launch(p.grid, a, f16, s);
     if (a.D > 64) return f16 ? launch<true, 128>(p, a, s) : launch<false, 128>(p, a, s);
     return f16 ? launch<true, 64>(p, a, s) : launch<false, 64>(p, a, s);
 }

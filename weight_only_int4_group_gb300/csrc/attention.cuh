@@ -220,29 +220,58 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Dims d..d + 3 of one row: the accumulated sum over its total, rounded once;
-// the row's log-sum-exp beside dim 0.  top is in units of log 2.
+// 1 / a row's sum of weights: 0 for a row that saw nothing, NaN kept.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+
+// Dims d..d + N - 1 (those below head_dim) of query head h of token row t,
+// rounded once.
+template <bool F16, int N>
+__device__ __forceinline__ void store_dims(const AttnArgs &a, int64_t t, int h, int d, const float (&v)[N])
+{
+    constexpr int V = N < 8 ? N : 8;  // head_dim is a multiple of 8
+    const int64_t at = t * a.o_stride + static_cast<int64_t>(h) * a.D + d;
+#pragma unroll
+    for (int i = 0; i < N; i += V) {
+        if (d + i >= a.D) return;
+        if (!store_ok(at + i + V - 1, static_cast<int64_t>(a.T - 1) * a.o_stride + static_cast<int64_t>(a.Hq) * a.D,
+                      a.err))
+            return;
+        if (a.ot == Q4_F32) {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at + i);
+#pragma unroll
+            for (int k = 0; k < V; k += 4) o[k / 4] = make_float4(v[i + k], v[i + k + 1], v[i + k + 2], v[i + k + 3]);
+        } else {
+            uint32_t w[V / 2];
+#pragma unroll
+            for (int k = 0; k < V; k += 2) w[k / 2] = pack2<F16>(v[i + k], v[i + k + 1]);
+            uint16_t *o = static_cast<uint16_t *>(a.o) + at + i;
+            if constexpr (V == 8)
+                *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+                *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+        }
+    }
+}
+
+// The row's log-sum-exp; top is in units of log 2.
+__device__ __forceinline__ void store_lse(const AttnArgs &a, int64_t t, int h, float top, float sum)
+{
+    const int64_t l = t * a.Hq + h;
+    if (a.lse && store_ok(l, static_cast<int64_t>(a.T) * a.Hq, a.err))
+        a.lse[l] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Dims d..d + 3 of one row of an item, from its accumulated sum.
 template <bool F16>
 __device__ __forceinline__ void finish_row(const AttnArgs &a, const Item &it, int t0, int row, int d,
                                            const float (&acc)[4], float top, float sum)
 {
-    if (d >= a.D) return;
-    const int t = t0 + row / a.GQ, h = it.head * a.GQ + row % a.GQ;
-    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    const int64_t at = t * a.o_stride + static_cast<int64_t>(h) * a.D + d;
-    if (store_ok(at + 3, static_cast<int64_t>(a.T - 1) * a.o_stride + static_cast<int64_t>(a.Hq) * a.D, a.err)) {
-        if (a.ot == Q4_F32)
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at) =
-                make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-        else
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + at) =
-                make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
-    }
-    if (a.lse && d == 0) {
-        const int64_t l = static_cast<int64_t>(t) * a.Hq + h;
-        if (store_ok(l, static_cast<int64_t>(a.T) * a.Hq, a.err))
-            a.lse[l] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-    }
+    const int64_t t = t0 + row / a.GQ;
+    const int h = it.head * a.GQ + row % a.GQ;
+    const float inv = inverse(sum);
+    const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+    store_dims<F16, 4>(a, t, h, d, v);
+    if (d == 0) store_lse(a, t, h, top, sum);
 }
 
 }  // namespace q4

@@ -21,7 +21,7 @@ struct AttnArgs {
     int D, S, blocks, width;
     float scale_log2;  // scale * log2(e): scores in units of log 2
     int window;        // 0: none
-    unsigned int *count;  // arrival counters, one per CTA
+    unsigned int *count;  // arrival counters, one or two per CTA
     float *part;          // partial results, two per CTA
     int64_t count_len, part_len;  // their extents, for the store checks
     uint64_t wait_ns;
@@ -29,7 +29,7 @@ struct AttnArgs {
     unsigned int *err;
 };
 
-constexpr size_t ATTN_COUNTER_BYTES = 4096;  // room for 1024 CTAs
+constexpr size_t ATTN_COUNTER_BYTES = 4096;  // room for 512 CTAs
 
 struct AttnPlan {
     bool tc;         // tensor-core kernel (many rows per KV head)
@@ -37,6 +37,8 @@ struct AttnPlan {
     size_t workspace;
 };
 AttnPlan attention_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count);
+size_t attention_tc_part_bytes(int64_t D, int grid);
+cudaError_t attention_tc_launch(int grid, const AttnArgs &a, bool f16, cudaStream_t s);
 cudaError_t attention_launch(const AttnPlan &p, const AttnArgs &a, bool f16, cudaStream_t s);
 
 struct PlanArgs {
