@@ -349,7 +349,7 @@ typedef struct {
     int64_t heads;        /* KV heads */
     int64_t block_size;   /* tokens per block, a multiple of 16 */
     int64_t head_dim;     /* a multiple of 8, at most 128 */
-    /* element strides of k and v alike, multiples of 8; the head_dim elements
+    /* element strides of k and v alike, multiples of 8 below 2^39; the head_dim elements
      * of a token are contiguous.  [blocks][heads][block_size][head_dim] and
      * [blocks][block_size][heads][head_dim] are both views of this form. */
     int64_t block_stride, head_stride, token_stride;
@@ -451,8 +451,8 @@ q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t
  * rule is stricter) nor with calls on other streams.
  * INVALID_ARG for NULL pointers, sizes < 1, Hq not a multiple of heads, a
  * non-finite scale, a negative window, a short workspace; UNSUPPORTED for
- * types, T * Hq or sizes beyond 2^31 - 1, or a cache beyond q4_kv_cache's
- * limits; MISALIGNED unless q, o, k, v, workspace are 16-byte aligned and
+ * types, T * Hq or B beyond 2^31 - 1, width * block_size beyond 2^30 - 1, or a
+ * cache beyond q4_kv_cache's limits; MISALIGNED unless q, o, k, v, workspace are 16-byte aligned and
  * strides multiples of 8.
  */
 q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "serve.cuh"
+#include "tcgen05.cuh"
 
 __device__ unsigned int g_q4_error = 0u;
 
@@ -57,6 +58,21 @@ unsigned int *device_error_word()
 {
     const DevInfo *d = dev_info();
     return d ? d->err : nullptr;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
 }
 
 // The error word for the store checks of the packing kernels: looked up
@@ -165,7 +181,7 @@ static q4_status cache_ok(const q4_kv_cache *c)
     for (const auto &x : d) {
         if (x.n == 1) continue;
         if (x.stride < extent) return Q4_ERR_INVALID_ARG;
-        if (x.stride > (1LL << 60) / x.n) return Q4_ERR_UNSUPPORTED;
+        if (x.stride >= (1LL << 39) || x.stride > (1LL << 60) / x.n) return Q4_ERR_UNSUPPORTED;
         extent += (x.n - 1) * x.stride;
     }
     if (!aligned16(c->k) || !aligned16(c->v) || c->block_stride % 8 || c->head_stride % 8 ||
@@ -465,7 +481,7 @@ static q4_status attention_common(const void *q, int64_t q_stride, int64_t T, in
         return Q4_ERR_INVALID_ARG;
     if (ot != Q4_F32 && ot != cache->type) return Q4_ERR_UNSUPPORTED;
     if (!attention_sizes_ok(max_fresh, Hq, cache->heads, cache->head_dim) || T > INT_MOST / Hq ||
-        B > INT_MOST || table_stride > (1LL << 40) || width > INT_MOST / cache->block_size)
+        B > INT_MOST || table_stride > (1LL << 40) || width > (INT_MOST >> 1) / cache->block_size)
         return Q4_ERR_UNSUPPORTED;
     const int64_t row = Hq * cache->head_dim;
     if (q_stride < row || o_stride < row) return Q4_ERR_INVALID_ARG;
@@ -501,6 +517,8 @@ static q4_status attention_common(const void *q, int64_t q_stride, int64_t T, in
     a.GQ = static_cast<int>(Hq / cache->heads);
     a.D = static_cast<int>(cache->head_dim);
     a.S = static_cast<int>(cache->block_size);
+    a.by_GQ.set(a.GQ);
+    a.by_S.set(a.S);
     a.blocks = static_cast<int>(cache->blocks);
     a.width = static_cast<int>(width);
     a.scale_log2 = scale * 1.4426950408889634f;

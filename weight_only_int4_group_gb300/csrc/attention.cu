@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
         const int *trow = a.table + it.b * a.table_stride;
         auto block_of = [&](int i) {  // table entry of this warp's i-th unit
             const int key = (sp.kt0 + kt + warp + i * NW) * TK;
-            return i < mine && key < sp.kv ? __ldg(trow + key / a.S) : -1;
+            return i < mine && key < sp.kv ? __ldg(trow + a.by_S.div(key)) : -1;
         };
         int next_block = block_of(0);
         auto issue = [&](int i) {
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
                 const int blk = next_block;
                 const int key = (sp.kt0 + kt + warp + i * NW) * TK;
                 const bool in = static_cast<unsigned>(blk) < static_cast<unsigned>(a.blocks);
-                const int64_t off = in ? blk * a.block_stride + (key % a.S) * a.token_stride : 0;
+                const int64_t off = in ? blk * a.block_stride + (key - a.by_S.div(key) * a.S) * a.token_stride : 0;
                 const uint32_t dst = ring + (i % STAGES) * 2 * Z::TILE;
 #pragma unroll
                 for (int l = 0; l < LPT; ++l) {
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
         for (int j = 0; j < 2; ++j) {
             const int r = sp.row0 + lane / 4 + 8 * j;
             const bool in = r < sp.row1;
-            const int t = in ? r / a.GQ : 0, g = in ? r - t * a.GQ : 0;
+            const int t = in ? a.by_GQ.div(r) : 0, g = in ? r - t * a.GQ : 0;
             place[j] = in ? sp.base + t : -1;
             qrow[j] = in ? a.q + (sp.t0 + t) * a.q_stride + static_cast<int64_t>(it.head * a.GQ + g) * a.D
                          : nullptr;

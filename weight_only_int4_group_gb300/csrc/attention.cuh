@@ -45,7 +45,7 @@ private:
         base = kv - n;
         row0 = rt * R;
         row1 = static_cast<int>(min(static_cast<int64_t>(n) * a.GQ, static_cast<int64_t>(row0) + R));
-        const int lo_t = row0 / a.GQ, hi_t = (row1 - 1) / a.GQ;
+        const int lo_t = a.by_GQ.div(row0), hi_t = a.by_GQ.div(row1 - 1);
         const int hi = base + hi_t + 1;
         const int64_t first = static_cast<int64_t>(base) + lo_t - a.window + 1;
         const int lo = a.window > 0 && first > 0 ? static_cast<int>(first) : 0;
@@ -59,6 +59,10 @@ struct Item {
     __device__ __forceinline__ void next(const AttnArgs &a, int R)
     {
         if (++head < a.Hkv) return;
+        next_rows(a, R);
+    }
+    __device__ __forceinline__ void next_rows(const AttnArgs &a, int R)
+    {
         head = 0;
         int t0, n, kv;
         request(a, b, t0, n, kv);
@@ -266,8 +270,9 @@ template <bool F16>
 __device__ __forceinline__ void finish_row(const AttnArgs &a, const Item &it, int t0, int row, int d,
                                            const float (&acc)[4], float top, float sum)
 {
-    const int64_t t = t0 + row / a.GQ;
-    const int h = it.head * a.GQ + row % a.GQ;
+    const int i = a.by_GQ.div(row);
+    const int64_t t = t0 + i;
+    const int h = it.head * a.GQ + row - i * a.GQ;
     const float inv = inverse(sum);
     const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
     store_dims<F16, 4>(a, t, h, d, v);

@@ -14,11 +14,15 @@
 //                   tensor memory, mask, weights back to tensor memory over
 //                   the scores (the A operand of the second product), row sums
 //                   in registers; at the end of an item the row's output;
-//   warps 8-10      producers: queries, keys and values by cp.async into the
-//                   128-byte-swizzled operand layouts (blocks of the cache
-//                   are 16 keys at least, anywhere: an address per row, zeros
-//                   for what lies past the request's end), a ring of four
-//                   32 KB slots holding K0 V0 K1 V1 ..;
+//   warps 8-10      producers of keys, values and queries into the 128-byte
+//                   swizzled operand layouts: tensor copies, one per run of
+//                   keys that lies in one block of the cache for certain (16
+//                   keys at least) and 64 dims, each lane issuing one; two
+//                   slots of 32 KB each for keys and values.  Only the value
+//                   tile that holds the request's end goes by cp.async, which
+//                   puts zeros behind it (0 times a stale NaN would reach the
+//                   sums; stale keys only make scores that are masked), and
+//                   queries whose group of heads does not divide 128;
 //   warp 11         allocates tensor memory; one thread issues the MMAs.
 // Tensor memory (512 columns): the two subtiles' scores (128 columns each)
 // and outputs (head_dim each).  While one subtile's softmax runs, the other's
@@ -38,6 +42,8 @@
 // order.  Every barrier wait is bounded; on expiry the CTA raises the device
 // error word, every role stops, copies and MMAs in flight are waited for,
 // tensor memory is freed and the kernel returns.
+#include <type_traits>
+
 #include "attention.cuh"
 #include "tcgen05.cuh"
 
@@ -47,13 +53,13 @@ namespace {
 constexpr int R = 256;   // rows per item
 constexpr int SR = 128;  // rows per subtile
 constexpr int TK = 128;  // keys per unit
-constexpr int SLOTS = 4;
-constexpr int W_P = 8, NP = 3;  // producers: warps 8..10
+constexpr int W_K = 8, W_V = 9, W_Q = 10;  // producers
 constexpr int W_M = 11;         // MMA issue
 constexpr int NW = 12, THREADS = NW * 32;  // 168 registers per thread; a 13th warp would cost 40 of them
-constexpr int KG = 16;          // keys that lie in one block of the cache for certain
-constexpr int GPW = (TK / KG + NP - 1) / NP;  // groups of them per producer warp and tile
-
+// Registers move from the copying and issuing warpgroup to the softmax ones,
+// which keep a row's 128 scores in registers.
+constexpr int REG_HI = 208, REG_LO = 80;
+static_assert(2 * REG_HI + REG_LO <= 3 * 168, "within the registers of the launch");
 template <int DP>
 struct Sizes {
     static constexpr int CH = DP / 64;           // 64-element chunks of a row
@@ -61,8 +67,9 @@ struct Sizes {
     static constexpr int TILE = CH * CHUNK;      // 128 rows: a subtile's queries, a key or value tile
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_R = 2 * TILE;
-    static constexpr int OFF_B = OFF_R + SLOTS * TILE;
-    static constexpr int NBAR = 2 * SLOTS + 2 + 6 + 1;
+    static constexpr int OFF_O = OFF_R + 4 * TILE;  // output staging, 32 rows x 64 bytes per warp
+    static constexpr int OFF_B = OFF_O + 8 * 2048;
+    static constexpr int NBAR = 8 + 2 + 6 + 1;
     static constexpr int SMEM = OFF_B + NBAR * 8 + 32 + 1024;  // slack to align the base
     static constexpr int PART = SR * (DP + 2);  // floats of a subtile's partial result
     static constexpr uint32_t S_COL = 0, O_COL = 256;
@@ -71,35 +78,64 @@ struct Sizes {
 };
 
 // A CTA's pieces of items, walked alike by every role.
-struct Piece {
+struct Walk {
+    Item it;
+    int64_t u;         // first unit of the piece
     int kt, nu;        // units [kt, kt + nu) of the item
-    bool whole;        // the item's only piece
-    int a[2], b[2];    // units [a, b) of the piece that subtile w sees
-    int lo[2], hi[2];  // places of its first and last row
-};
-__device__ __forceinline__ Piece piece_of(const AttnArgs &a, const Span<R, TK> &sp, int kt, int64_t left)
-{
-    Piece p;
-    p.kt = kt;
-    p.nu = static_cast<int>(min(static_cast<int64_t>(sp.units - kt), left));
-    p.whole = kt == 0 && p.nu == sp.units;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const int r0 = sp.row0 + w * SR, r1 = min(sp.row1, r0 + SR);
-        p.a[w] = p.b[w] = 0;
-        p.lo[w] = p.hi[w] = -1;
-        if (r0 >= r1) continue;
-        p.lo[w] = sp.base + r0 / a.GQ;
-        p.hi[w] = sp.base + (r1 - 1) / a.GQ;
-        if (p.hi[w] < 0) continue;
-        const int64_t first = static_cast<int64_t>(p.lo[w]) - a.window + 1;
-        const int u0 = (a.window > 0 && first > 0 ? static_cast<int>(first) : 0) / TK - sp.kt0 - kt;
-        const int u1 = p.hi[w] / TK + 1 - sp.kt0 - kt;
-        p.a[w] = min(max(u0, 0), p.nu);
-        p.b[w] = max(p.a[w], min(u1, p.nu));
+    int units, kt0;    // the item's units, the first one's index among the request's keys
+    int row0, row1, t0, base, kv;
+    __device__ __forceinline__ Walk(const AttnArgs &a, const Range &r) : it(r.first), u(r.u0), kt(r.kt)
+    {
+        if (u < r.u1) load(a, r);
     }
-    return p;
-}
+    __device__ __forceinline__ void next(const AttnArgs &a, const Range &r)
+    {
+        u += nu;
+        kt = 0;
+        if (u >= r.u1) return;
+        if (++it.head < a.Hkv) {  // the same rows and keys of the next head
+            nu = static_cast<int>(min(static_cast<int64_t>(units), r.u1 - u));
+            return;
+        }
+        it.next_rows(a, R);
+        load(a, r);
+    }
+    __device__ __forceinline__ bool whole() const { return kt == 0 && nu == units; }
+    // Units [lo, hi) of the piece that subtile w sees, and the places of its
+    // first and last row.
+    struct Seen {
+        int a, b, lo, hi;
+    };
+    __device__ __forceinline__ Seen seen(const AttnArgs &a, int w) const
+    {
+        Seen s = {0, 0, -1, -1};
+        const int r0 = row0 + w * SR, r1 = min(row1, r0 + SR);
+        if (r0 >= r1) return s;
+        s.lo = base + a.by_GQ.div(r0);
+        s.hi = base + a.by_GQ.div(r1 - 1);
+        if (s.hi < 0) return s;
+        const int64_t first = static_cast<int64_t>(s.lo) - a.window + 1;
+        const int u0 = (a.window > 0 && first > 0 ? static_cast<int>(first) : 0) / TK - kt0 - kt;
+        const int u1 = s.hi / TK + 1 - kt0 - kt;
+        s.a = min(max(u0, 0), nu);
+        s.b = max(s.a, min(u1, nu));
+        return s;
+    }
+
+private:
+    __device__ __forceinline__ void load(const AttnArgs &a, const Range &r)
+    {
+        const Span<R, TK> sp(a, it.b, it.rt);
+        units = sp.units;
+        kt0 = sp.kt0;
+        row0 = sp.row0;
+        row1 = sp.row1;
+        t0 = sp.t0;
+        base = sp.base;
+        kv = sp.kv;
+        nu = static_cast<int>(min(static_cast<int64_t>(units - kt), r.u1 - u));
+    }
+};
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
 {
@@ -108,18 +144,74 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
                  : "memory");
 }
 
+// This lane's arrival on bar once its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// a * b + c and a + b on pairs of f32
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z)
+{
+    uint64_t a, b, c, d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(y.x), "f"(y.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(z.x), "f"(z.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y)
+{
+    uint64_t a, b, d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(y.x), "f"(y.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+    return r;
+}
+
+// The call's tensor maps and how the producers use them.
+struct Maps {
+    CUtensorMap k, v;  // (dim, token, head, block), boxes of 64 x kb x 1 x 1
+    CUtensorMap q;     // (dim, query head, row), boxes of 64 x GQ x 128 / GQ
+    int kb;            // keys per box: the largest power of two up to 128 that divides block_size
+    int q_boxes;       // GQ divides 128: queries by tensor copies
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                            uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
 template <bool F16, int DP>
-__global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const AttnArgs a)
+__global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ Maps maps, const AttnArgs a)
 {
     using Z = Sizes<DP>;
     constexpr int C8 = DP / 8;  // 16-byte pieces of a row
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    // kfull/kempty: ring slots; qfull/qempty: queries; sfull: scores ready;
-    // pfull: weights stored (and the output rescaled); ofull: output complete
-    uint64_t *kfull = reinterpret_cast<uint64_t *>(smem + Z::OFF_B), *kempty = kfull + SLOTS;
-    uint64_t *qfull = kempty + SLOTS, *qempty = qfull + 1, *sfull = qempty + 1, *pfull = sfull + 2;
+    // kfull/kempty: slots, two for keys then two for values; qfull/qempty:
+    // queries; sfull: scores ready; pfull: weights stored (and the output
+    // rescaled); ofull: output complete.  Each lane of a producer arrives.
+    uint64_t *kfull = reinterpret_cast<uint64_t *>(smem + Z::OFF_B), *kempty = kfull + 4;
+    uint64_t *qfull = kempty + 4, *qempty = qfull + 1, *sfull = qempty + 1, *pfull = sfull + 2;
     uint64_t *ofull = pfull + 2, *drain = ofull + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -128,11 +220,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const AttnArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(&kfull[i], NP * 32);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&kfull[i], 32);
             mbar_init(&kempty[i], 1);
         }
-        mbar_init(qfull, NP * 32);
+        mbar_init(qfull, 32);
         mbar_init(qempty, 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(&sfull[w], 1);
@@ -159,218 +251,250 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const AttnArgs a)
     };
     bool ok = true;
 
-    if (warp >= W_P && warp < W_P + NP) {
-        // ----------------------------------------------------- producers
-        const int pw = warp - W_P;
-        const uint32_t sq = smem_u32(smem + Z::OFF_Q), sr = smem_u32(smem + Z::OFF_R);
-        // a barrier takes each lane's arrival when the lane's copies so far
-        // have landed; the MMA thread fences the proxies after its wait
-        auto issued = [&](uint64_t *bar) {
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-        };
-        Item it = rng.first;
-        int64_t u = rng.u0;
-        int kt = rng.kt, n = 0;  // n: ring position
-        for (int pc = 0; ok && u < rng.u1 && !a.debug_no_copy; ++pc) {
-            const Span<R, TK> sp(a, it.b, it.rt);
-            const Piece p = piece_of(a, sp, kt, rng.u1 - u);
-            // queries: rows dealt over the warps' half-warps (16-byte pieces)
-            if (pc > 0 && !warp_wait(qempty, (pc - 1) & 1)) {
-                ok = false;
-                break;
-            }
-#pragma unroll 4
-            for (int e = pw * 32 + lane; e < R * C8; e += NP * 32) {
-                const int row = e / C8, c = e % C8, r = sp.row0 + row;
-                const bool in = r < sp.row1 && c * 8 < a.D;
-                const int t = in ? r / a.GQ : 0, g = in ? r - t * a.GQ : 0;
-                const uint16_t *src = in ? a.q + (sp.t0 + t) * a.q_stride +
-                                               static_cast<int64_t>(it.head * a.GQ + g) * a.D + c * 8
-                                         : a.q;
-                const int rr = row & (SR - 1);
-                cp_async16(sq + (row / SR) * Z::TILE + (c >> 3) * Z::CHUNK + rr * 128 +
-                               (((c & 7) ^ (rr & 7)) << 4),
-                           src, in);
-            }
-            issued(qfull);
-            // keys and values: groups of 16 keys, each within one block of
-            // the cache, dealt over the warps
-            const uint16_t *kb = a.k + it.head * a.head_stride, *vb = a.v + it.head * a.head_stride;
-            const int *trow = a.table + it.b * a.table_stride;
-            auto block_of = [&](int j, int i) {
-                const int key = (sp.kt0 + kt + j) * TK + (pw + i * NP) * KG;
-                return j < p.nu && pw + i * NP < TK / KG && key < sp.kv ? __ldg(trow + key / a.S) : -1;
-            };
-            int blk[GPW];
-#pragma unroll
-            for (int i = 0; i < GPW; ++i) blk[i] = block_of(0, i);
-            for (int j = 0; ok && j < p.nu; ++j) {
-                const int key0 = (sp.kt0 + kt + j) * TK;
-                int64_t off[GPW];  // element offset of the group's first key; -1: zeros
-#pragma unroll
-                for (int i = 0; i < GPW; ++i) {
-                    const bool in = static_cast<unsigned>(blk[i]) < static_cast<unsigned>(a.blocks);
-                    off[i] = in ? blk[i] * a.block_stride + ((key0 + (pw + i * NP) * KG) % a.S) * a.token_stride : -1;
-                    blk[i] = block_of(j + 1, i);
-                }
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int s = n % SLOTS;
-                    if (n >= SLOTS && !warp_wait(&kempty[s], (n / SLOTS - 1) & 1)) {
-                        ok = false;
-                        break;
+    if (warp == W_K || warp == W_V) {
+        // --------------------------------------------- keys and values
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
+        const bool vals = warp == W_V;
+        const CUtensorMap *map = vals ? &maps.v : &maps.k;
+        const uint16_t *vh = a.v;
+        uint64_t *full = kfull + (vals ? 2 : 0), *empty = kempty + (vals ? 2 : 0);
+        const uint32_t ring = smem_u32(smem + Z::OFF_R) + (vals ? 2 * Z::TILE : 0);
+        // lane: one box of a tile, keys [bk, bk + kb), chunk ch
+        const int bk = lane / Z::CH * maps.kb, ch = lane % Z::CH;
+        const bool boxed = bk < TK;
+        const uint32_t bd = ch * Z::CHUNK + bk * 128;
+        Walk k(a, rng);
+        int g = 0;  // units loaded
+        for (; ok && k.u < rng.u1 && !a.debug_no_copy; k.next(a, rng)) {
+            const int *trow = a.table + k.it.b * a.table_stride;
+            auto block_of = [&](int key) { return key < k.kv ? __ldg(trow + a.by_S.div(key)) : -1; };
+            const int first = (k.kt0 + k.kt) * TK;
+            int blk = boxed ? block_of(first + bk) : -1;
+            for (int j = 0; j < k.nu; ++j, ++g) {
+                const int s = g & 1, key0 = first + j * TK;
+                if (g >= 2 && !(ok = warp_wait(&empty[s], ((g >> 1) - 1) & 1))) break;
+                const uint32_t dst = ring + s * Z::TILE;
+                if (!vals || key0 + TK <= k.kv) {
+                    if (boxed) {
+                        // a block outside the cache reads as zeros
+                        mbar_arrive_expect_tx(&full[s], maps.kb * 128);
+                        const int key = key0 + bk;
+                        tma_load_4d(dst + bd, map, ch * 64, key - a.by_S.div(key) * a.S, k.it.head, blk, &full[s]);
+                        blk = j + 1 < k.nu ? block_of(key + TK) : -1;
+                    } else {
+                        mbar_arrive(&full[s]);
                     }
-                    const uint16_t *base = kv ? vb : kb;
-                    const uint32_t dst = sr + s * Z::TILE;
+                    __syncwarp();
+                } else {
+                    // groups of 16 keys, each within one block of the cache
+                    constexpr int RPI = 32 / C8;
+                    const int c = lane % C8, hi = lane / C8;
+                    const uint32_t dc = dst + (c >> 3) * Z::CHUNK + hi * 128;
+#pragma unroll 1
+                    for (int r0 = 0; r0 < TK; r0 += 16) {
+                        const int key = key0 + r0, b = block_of(key);
+                        const bool in = static_cast<unsigned>(b) < static_cast<unsigned>(a.blocks);
+                        const uint16_t *base = vh + k.it.head * a.head_stride + (in ? b * a.block_stride : 0) +
+                                               (key - a.by_S.div(key) * a.S) * a.token_stride + c * 8;
 #pragma unroll
-                    for (int i = 0; i < GPW; ++i) {
-                        if (pw + i * NP >= TK / KG) break;
-                        const int r0 = (pw + i * NP) * KG;
-#pragma unroll
-                        for (int l = 0; l < KG * C8 / 32; ++l) {
-                            const int e = l * 32 + lane, row = r0 + e / C8, c = e % C8;
-                            const bool v = off[i] >= 0 && key0 + row < sp.kv && c * 8 < a.D;
-                            const uint16_t *src = v ? base + off[i] + (e / C8) * a.token_stride + c * 8 : base;
-                            cp_async16(dst + (c >> 3) * Z::CHUNK + row * 128 + (((c & 7) ^ (row & 7)) << 4), src, v);
+                        for (int l = 0; l < 16 / RPI; ++l) {
+                            const int row = l * RPI + hi;
+                            const bool ok16 = in && key + row < k.kv && c * 8 < a.D;
+                            cp_async16(dc + (r0 + l * RPI) * 128 + (((c & 7) ^ (row & 7)) << 4),
+                                       ok16 ? base + row * a.token_stride : vh, ok16);
                         }
                     }
-                    issued(&kfull[s]);
+                    // the lane's arrival when its copies have landed; the MMA
+                    // warp fences the proxies after its wait
+                    cp_async_arrive(&full[s]);
                 }
             }
-            u += p.nu;
-            kt = 0;
-            it.next(a, R);
+        }
+        // every copy lands before the CTA may exit
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int i = max(0, g - 2); i < g; ++i)
+            mbar_wait_bounded(&full[i & 1], (i >> 1) & 1, abort_flag, a.wait_ns, a.err, false);
+        __syncwarp();
+    } else if (warp == W_Q) {
+        // ------------------------------------------------------ queries
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
+        const uint32_t sq = smem_u32(smem + Z::OFF_Q);
+        Walk k(a, rng);
+        int pc = 0;
+        for (; k.u < rng.u1 && !a.debug_no_copy; ++pc, k.next(a, rng)) {
+            if (pc > 0 && !(ok = warp_wait(qempty, (pc - 1) & 1))) break;
+            if (maps.q_boxes) {
+                // lane: one chunk of one subtile.  Rows past the request's are
+                // other requests' (or zeros past T): their results go nowhere
+                if (lane < 2 * Z::CH) {
+                    const int w = lane / Z::CH, ch = lane % Z::CH;
+                    mbar_arrive_expect_tx(qfull, SR * 128);
+                    tma_load_3d(sq + w * Z::TILE + ch * Z::CHUNK, &maps.q, ch * 64, k.it.head * a.GQ,
+                                k.t0 + a.by_GQ.div(k.row0 + w * SR), qfull);
+                } else {
+                    mbar_arrive(qfull);
+                }
+                __syncwarp();
+            } else {
+                constexpr int RPI = 32 / C8;
+                const int c = lane % C8, hi = lane / C8;
+                const int dt = RPI / a.GQ, dg = RPI - dt * a.GQ;
+                int r = k.row0 + hi, t = a.by_GQ.div(r), g = r - t * a.GQ;
+                const uint16_t *src = a.q + (k.t0 + t) * a.q_stride +
+                                      static_cast<int64_t>(k.it.head * a.GQ + g) * a.D + c * 8;
+                const int64_t step = dt * a.q_stride + static_cast<int64_t>(dg) * a.D;
+                const int64_t wrap = a.q_stride - static_cast<int64_t>(a.GQ) * a.D;
+#pragma unroll 1
+                for (int r0 = 0; r0 < R; r0 += 8) {
+#pragma unroll
+                    for (int l = 0; l < 8 / RPI; ++l) {
+                        const int row = l * RPI + hi;  // within 8 rows
+                        const bool in = k.row0 + r0 + row < k.row1 && c * 8 < a.D;
+                        cp_async16(sq + (r0 / SR) * Z::TILE + (c >> 3) * Z::CHUNK + ((r0 & (SR - 1)) + row) * 128 +
+                                       (((c & 7) ^ row) << 4),
+                                   in ? src : a.q, in);
+                        src += step;
+                        g += dg;
+                        if (g >= a.GQ) {
+                            g -= a.GQ;
+                            src += wrap;
+                        }
+                    }
+                }
+                cp_async_arrive(qfull);
+            }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if (pc > 0) mbar_wait_bounded(qfull, (pc - 1) & 1, abort_flag, a.wait_ns, a.err, false);
+        __syncwarp();
     } else if (warp == W_M) {
         // ---------------------------------------------------- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t AB = F16 ? 0u : 1u;
-            const uint32_t id_qk = idesc_f16(AB, TK), id_pv = idesc_f16(AB, DP) | IDESC_B_MN;
-            const uint64_t dq = sw128_desc(smem_u32(smem + Z::OFF_Q));
-            const uint64_t dk = sw128_desc(smem_u32(smem + Z::OFF_R));
-            const uint64_t dv = sw128_desc(smem_u32(smem + Z::OFF_R), Z::CHUNK);
-            auto qk = [&](int w, int s) {
+        // the warp stays whole (one lane is elected per instruction): operands
+        // that differ by lane would have to be moved for every MMA
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
+        constexpr uint32_t AB = F16 ? 0u : 1u;
+        const uint32_t id_qk = idesc_f16(AB, TK), id_pv = idesc_f16(AB, DP) | IDESC_B_MN;
+        const uint64_t dq = sw128_desc(smem_u32(smem + Z::OFF_Q));
+        const uint64_t dk = sw128_desc(smem_u32(smem + Z::OFF_R));
+        const uint64_t dv = sw128_desc(smem_u32(smem + Z::OFF_R), Z::CHUNK);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        // scores of subtile w with the keys in slot s; output of subtile w
+        // with the values in slot s
+        auto qk = [&](auto w_, int s) {
+            constexpr int w = decltype(w_)::value;
+            const uint64_t b = dk + ((s * Z::TILE) >> 4);
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    const int o = (k / 4) * Z::CHUNK + (k % 4) * 32;
-                    mma_ss(tmem + Z::S_COL + w * 128, dq + ((w * Z::TILE + o) >> 4),
-                           dk + ((s * Z::TILE + o) >> 4), id_qk, k > 0);
-                }
-            };
-            auto pv = [&](int w, int s, bool acc) {
-#pragma unroll
-                for (int k = 0; k < TK / 16; ++k)
-                    mma_ts(tmem + Z::O_COL + w * DP, tmem + Z::S_COL + w * 128 + k * 8,
-                           dv + ((s * Z::TILE + k * 16 * 128) >> 4), id_pv, acc || k > 0);
-            };
-            Item it = rng.first;
-            int64_t u = rng.u0;
-            int kt = rng.kt, n = 0;
-            uint32_t np[2] = {0, 0};  // weights consumed per subtile
-            for (int pc = 0; ok && u < rng.u1; ++pc) {
-                const Span<R, TK> sp(a, it.b, it.rt);
-                const Piece p = piece_of(a, sp, kt, rng.u1 - u);
-                if (!(ok = wait(qfull, pc & 1))) break;
-                if (!(ok = wait(&kfull[n % SLOTS], (n / SLOTS) & 1))) break;
-                fence_proxy_async_smem();
-#pragma unroll
-                for (int w = 0; w < 2; ++w)
-                    if (p.a[w] == 0 && p.b[w] > 0) {
-                        qk(w, n % SLOTS);
-                        mma_commit(&sfull[w]);
-                    }
-                mma_commit(&kempty[n % SLOTS]);
-                if (p.nu == 1) mma_commit(qempty);
-                ++n;
-                for (int j = 0; ok && j < p.nu; ++j) {
-                    const int sv = n % SLOTS, sk = (n + 1) % SLOTS;
-                    const bool more = j + 1 < p.nu;
-                    if (!(ok = wait(&kfull[sv], (n / SLOTS) & 1))) break;
-                    fence_proxy_async_smem();
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        if (j >= p.a[w] && j < p.b[w]) {
-                            if (!(ok = wait(&pfull[w], np[w] & 1))) break;
-                            ++np[w];
-                            tc_fence_after();
-                            pv(w, sv, j > p.a[w]);
-                            if (j == p.b[w] - 1) mma_commit(&ofull[w]);
-                        }
-                        if (more) {
-                            if (w == 0) {
-                                if (!(ok = wait(&kfull[sk], ((n + 1) / SLOTS) & 1))) break;
-                                fence_proxy_async_smem();
-                            }
-                            if (j + 1 >= p.a[w] && j + 1 < p.b[w]) {
-                                qk(w, sk);
-                                mma_commit(&sfull[w]);
-                            }
-                        }
-                    }
-                    if (!ok) break;
-                    mma_commit(&kempty[sv]);
-                    if (more) {
-                        mma_commit(&kempty[sk]);
-                        if (j + 2 == p.nu) mma_commit(qempty);
-                    }
-                    n += more ? 2 : 1;
-                }
-                u += p.nu;
-                kt = 0;
-                it.next(a, R);
+            for (int k = 0; k < DP / 16; ++k) {
+                const int o = (k / 4) * Z::CHUNK + (k % 4) * 32;
+                mma_ss(tm + Z::S_COL + w * 128, dq + ((w * Z::TILE + o) >> 4), b + (o >> 4), id_qk, k > 0);
             }
-            // MMAs in flight end before tensor memory is freed
-            mma_commit(drain);
-            mbar_wait_bounded(drain, 0, abort_flag, a.wait_ns, a.err, false);
+            mma_commit_elected(&sfull[w]);
+        };
+        auto pv = [&](auto w_, int s, bool acc) {
+            constexpr int w = decltype(w_)::value;
+            const uint64_t b = dv + ((s * Z::TILE) >> 4);
+#pragma unroll
+            for (int k = 0; k < TK / 16; ++k)
+                mma_ts(tm + Z::O_COL + w * DP, tm + Z::S_COL + w * 128 + k * 8, b + ((k * 16 * 128) >> 4), id_pv,
+                       acc || k > 0);
+        };
+        Walk k(a, rng);
+        int g = 0;                  // units before this piece
+        uint32_t np0 = 0, np1 = 0;  // weights consumed per subtile
+        using W0 = std::integral_constant<int, 0>;
+        using W1 = std::integral_constant<int, 1>;
+        auto landed = [&](int slot, int unit) {
+            if (!warp_wait(&kfull[slot], (unit >> 1) & 1)) return false;
+            fence_proxy_async_smem();
+            return true;
+        };
+        for (int pc = 0; ok && k.u < rng.u1; ++pc, k.next(a, rng)) {
+            const Walk::Seen s0 = k.seen(a, 0), s1 = k.seen(a, 1);
+            if (!(ok = warp_wait(qfull, pc & 1))) break;
+            if (!(ok = landed(g & 1, g))) break;
+            if (s0.a == 0 && s0.b > 0) qk(W0(), g & 1);
+            if (s1.a == 0 && s1.b > 0) qk(W1(), g & 1);
+            mma_commit_elected(&kempty[g & 1]);
+            if (k.nu == 1) mma_commit_elected(qempty);
+            for (int j = 0; j < k.nu; ++j) {
+                const int v = g & 1, nk = (g + 1) & 1;
+                const bool more = j + 1 < k.nu;
+                if (!(ok = landed(2 + v, g))) break;
+                if (j >= s0.a && j < s0.b) {
+                    if (!(ok = warp_wait(&pfull[0], np0++ & 1))) break;
+                    tc_fence_after();
+                    pv(W0(), 2 + v, j > s0.a);
+                    if (j == s0.b - 1) mma_commit_elected(&ofull[0]);
+                }
+                if (more) {
+                    if (!(ok = landed(nk, g + 1))) break;
+                    if (j + 1 >= s0.a && j + 1 < s0.b) qk(W0(), nk);
+                }
+                if (j >= s1.a && j < s1.b) {
+                    if (!(ok = warp_wait(&pfull[1], np1++ & 1))) break;
+                    tc_fence_after();
+                    pv(W1(), 2 + v, j > s1.a);
+                    if (j == s1.b - 1) mma_commit_elected(&ofull[1]);
+                }
+                mma_commit_elected(&kempty[2 + v]);
+                if (more) {
+                    if (j + 1 >= s1.a && j + 1 < s1.b) qk(W1(), nk);
+                    mma_commit_elected(&kempty[nk]);
+                    if (j + 2 == k.nu) mma_commit_elected(qempty);
+                }
+                ++g;
+            }
         }
+        // MMAs in flight end before tensor memory is freed
+        mma_commit_elected(drain);
+        mbar_wait_bounded(drain, 0, abort_flag, a.wait_ns, a.err, false);
         __syncwarp();
     } else {
         // ------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HI));
         const int w = warp >> 2, rr = tid & (SR - 1);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field: 32 * (warp % 4) << 16
         const uint32_t ts = tmem + lanes + Z::S_COL + w * 128, to = tmem + lanes + Z::O_COL + w * DP;
         const bool neg = a.scale_log2 < 0.0f;
-        Item it = rng.first;
-        int64_t u = rng.u0;
-        int kt = rng.kt;
         uint32_t ns = 0, no = 0;
-        while (u < rng.u1) {
-            const Span<R, TK> sp(a, it.b, it.rt);
-            const Piece p = piece_of(a, sp, kt, rng.u1 - u);
-            const int r = sp.row0 + w * SR + rr;
-            const bool in = r < sp.row1;
-            const int place = in ? sp.base + r / a.GQ : -1;
+        for (Walk k(a, rng); k.u < rng.u1; k.next(a, rng)) {
+            const Walk::Seen p = k.seen(a, w);
+            const int r = k.row0 + w * SR + rr;
+            const bool in = r < k.row1;
+            const int place = in ? k.base + a.by_GQ.div(r) : -1;
             float m = -INFINITY, l = 0.0f;
-            for (int j = p.a[w]; ok && j < p.b[w]; ++j, ++ns) {
+            for (int j = p.a; ok && j < p.b; ++j, ++ns) {
                 if (!(ok = warp_wait(&sfull[w], ns & 1))) break;
                 tc_fence_after();
-                const int key0 = (sp.kt0 + kt + j) * TK;
+                const int key0 = (k.kt0 + k.kt + j) * TK;
                 // columns [c0, c1] are the keys this row sees
-                const bool part = key0 + TK - 1 > p.lo[w] ||
-                                  (a.window > 0 && key0 <= p.hi[w] - a.window) || p.lo[w] < 0;
+                const bool part = key0 + TK - 1 > p.lo || (a.window > 0 && key0 <= p.hi - a.window) || p.lo < 0;
                 const int c1 = place - key0;
                 const int c0 = a.window > 0 && place - a.window + 1 > key0 ? place - a.window + 1 - key0 : 0;
-                float mx = -INFINITY;
-                uint32_t v[32];
+                uint32_t v[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32x(ts + c * 32, v);
-                    tmem_wait_ld();
-                    if (part || neg) {
+                for (int c = 0; c < 4; ++c) tmem_ld32x(ts + c * 32, v[c]);
+                tmem_wait_ld();
+                const bool pre = part || neg;  // scores scaled and masked first
+                if (pre) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float x = __uint_as_float(v[i]) * a.scale_log2;
-                            if (c * 32 + i >= c0 && c * 32 + i <= c1) mx = fmaxf(mx, x);
-                        }
-                    } else {
-                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(v[i]));
-                        mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                    for (int i = 0; i < TK; ++i) {
+                        const float x = __uint_as_float(v[i / 32][i % 32]) * a.scale_log2;
+                        v[i / 32][i % 32] = __float_as_uint(i >= c0 && i <= c1 ? x : -INFINITY);
                     }
                 }
-                if (!(part || neg)) mx *= a.scale_log2;
+                const float sc = pre ? 1.0f : a.scale_log2;
+                float m4[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(v[c][0]);
+#pragma unroll
+                for (int i = 1; i < 31; i += 2)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(v[c][31]));
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
                 bool move = false;
                 float f = 1.0f;
                 if (m == -INFINITY) {
@@ -381,46 +505,43 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const AttnArgs a)
                     l *= f;
                     move = true;
                 }
-                if (__any_sync(0xffffffffu, move) && j > p.a[w]) {
-#pragma unroll
-                    for (int c = 0; c < DP / 32; ++c) {
-                        tmem_ld32x(to + c * 32, v);
+                if (__any_sync(0xffffffffu, move) && j > p.a) {
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 16) {
+                        uint32_t x[16];
+                        tmem_ld16x(to + c, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                        tmem_st32(to + c * 32, v);
+                        for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                        tmem_st16(to + c, x);
                     }
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
-                float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const float2 sc2 = make_float2(sc, sc), rf2 = make_float2(-ref, -ref);
+                float2 s2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32x(ts + c * 32, v);
-                    tmem_wait_ld();
-                    uint32_t pk[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pk[32];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float x = fmaf(__uint_as_float(v[i]), a.scale_log2, -ref);
-                        float y = fmaf(__uint_as_float(v[i + 1]), a.scale_log2, -ref);
-                        if (part) {
-                            if (c * 32 + i < c0 || c * 32 + i > c1) x = -INFINITY;
-                            if (c * 32 + i + 1 < c0 || c * 32 + i + 1 > c1) y = -INFINITY;
-                        }
-                        x = ex2(x);
-                        y = ex2(y);
-                        s4[i & 2] += x;
-                        s4[(i & 2) + 1] += y;
-                        pk[i / 2] = pack2<F16>(x, y);
+                    for (int i = 0; i < 64; i += 2) {
+                        float2 x = make_float2(__uint_as_float(v[2 * c + i / 32][i % 32]),
+                                               __uint_as_float(v[2 * c + i / 32][i % 32 + 1]));
+                        x = fma2(x, sc2, rf2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        s2[(i / 2) & 1] = add2(s2[(i / 2) & 1], x);
+                        pk[i / 2] = pack2<F16>(x.x, x.y);
                     }
-                    tmem_st16(ts + c * 16, pk);
+                    tmem_st32(ts + c * 32, pk);
                 }
-                l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                s2[0] = add2(s2[0], s2[1]);
+                l += s2[0].x + s2[0].y;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pfull[w]);
             }
-            const bool any = p.b[w] > p.a[w];
+            const bool any = p.b > p.a;
             if (ok && any) {
                 ok = warp_wait(&ofull[w], no & 1);
                 ++no;
@@ -431,31 +552,72 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const AttnArgs a)
                 ok = false;
                 break;
             }
-            const bool rows = sp.row0 + w * SR < sp.row1;
-            const int64_t t_row = sp.t0 + (in ? r / a.GQ : 0);
-            const int h_row = it.head * a.GQ + (in ? r % a.GQ : 0);
-            if (p.whole) {
-                uint32_t v[32];
-                const float inv = inverse(l);
-#pragma unroll
-                for (int c = 0; c < DP / 32; ++c) {
-                    __syncwarp();
-                    if (any) {
-                        tmem_ld32x(to + c * 32, v);
-                        tmem_wait_ld();
-                    }
-                    if (in) {
+            const bool rows = k.row0 + w * SR < k.row1;
+            const int64_t t_row = k.t0 + (in ? a.by_GQ.div(r) : 0);
+            const int h_row = k.it.head * a.GQ + (in ? r - a.by_GQ.div(r) * a.GQ : 0);
+            if (k.whole()) {
+                const float inv = any ? inverse(l) : 0.0f;
+                if (a.ot == Q4_F32) {
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t v[32] = {};
+                        __syncwarp();
+                        if (any) {
+                            tmem_ld32x(to + c, v);
+                            tmem_wait_ld();
+                        }
                         float o[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = any ? __uint_as_float(v[i]) * inv : 0.0f;
-                        store_dims<F16, 32>(a, t_row, h_row, c * 32, o);
+                        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * inv;
+                        if (in) store_dims<F16, 32>(a, t_row, h_row, c, o);
+                    }
+                } else {
+                    // 32 dims of the warp's 32 rows turn through shared
+                    // memory, so that 4 lanes store 64 bytes of one row
+                    uint8_t *st = smem + Z::OFF_O + warp * 2048;
+                    const int q = lane & 3;
+                    int64_t at[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int x = k.row0 + w * SR + (warp & 3) * 32 + i * 8 + lane / 4;
+                        const int t = a.by_GQ.div(x);
+                        at[i] = x < k.row1 ? (k.t0 + t) * a.o_stride +
+                                                 static_cast<int64_t>(k.it.head * a.GQ + x - t * a.GQ) * a.D + q * 8
+                                           : -1;
+                    }
+                    const int64_t o_len = static_cast<int64_t>(a.T - 1) * a.o_stride + static_cast<int64_t>(a.Hq) * a.D;
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t v[32] = {};
+                        __syncwarp();
+                        if (any) {
+                            tmem_ld32x(to + c, v);
+                            tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint4 x;
+                            uint32_t *y = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = pack2<F16>(__uint_as_float(v[i + 2 * e]) * inv, __uint_as_float(v[i + 2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(st + lane * 64 + (((i / 8) ^ ((lane >> 1) & 3)) << 4)) = x;
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int x = i * 8 + lane / 4;
+                            const uint4 y = *reinterpret_cast<const uint4 *>(st + x * 64 + ((q ^ ((x >> 1) & 3)) << 4));
+                            if (at[i] >= 0 && c + q * 8 < a.D && store_ok(at[i] + c + 7, o_len, a.err))
+                                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + at[i] + c) = y;
+                        }
                     }
                 }
                 if (in) store_lse(a, t_row, h_row, m, l);
                 __syncwarp();
             } else if (rows) {
                 // [dim][row], so that a warp's stores and loads are whole lines
-                float *ps = a.part + ((2 * static_cast<int64_t>(blockIdx.x) + (kt == 0)) * 2 + w) * Z::PART;
+                float *ps = a.part + ((2 * static_cast<int64_t>(blockIdx.x) + (k.kt == 0)) * 2 + w) * Z::PART;
                 const bool fits = store_ok(ps + Z::PART - 1 - a.part, a.part_len, a.err);
                 uint32_t v[32];
 #pragma unroll
@@ -473,7 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const AttnArgs a)
                     ps[DP * SR + rr] = m;
                     ps[(DP + 1) * SR + rr] = l;
                 }
-                const int64_t i0 = u - kt, i1 = i0 + sp.units;
+                const int64_t i0 = k.u - k.kt, i1 = i0 + k.units;
                 const int f0 = owner_of(i0, rng.total, rng.G), f1 = owner_of(i1 - 1, rng.total, rng.G);
                 named_barrier_sync(1 + w, SR);
                 if (rr == 0) {
@@ -518,15 +680,31 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const AttnArgs a)
                 __syncwarp();
             }
             tc_fence_before();  // this piece's tensor-memory reads end before the next one's products
-            u += p.nu;
-            kt = 0;
-            it.next(a, R);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == W_M) tmem_dealloc(tmem, 512);
+}
+
+// Tensor map of n dimensions; a dimension of extent 1 has no stride of its own.
+bool encode(CUtensorMap *map, const void *base, bool f16, int n, const uint64_t *extent, const int64_t *stride,
+            const uint32_t *box)
+{
+    const auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[4], bytes[3];
+    cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+    for (int i = 0; i < n; ++i) {
+        dims[i] = extent[i];
+        b[i] = box[i];
+        if (i > 0) bytes[i - 1] = extent[i] > 1 ? static_cast<cuuint64_t>(stride[i]) * 2 : 16;
+    }
+    return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n,
+              const_cast<void *>(base), dims, bytes, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool F16, int DP>
@@ -536,7 +714,22 @@ cudaError_t launch(int grid, const AttnArgs &a, cudaStream_t s)
     auto kern = k_attn_tc<F16, DP>;
     const cudaError_t e = allow_smem(kern, Sizes<DP>::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(grid), THREADS, Sizes<DP>::SMEM, s, a);
+    Maps m = {};
+    m.kb = std::min(a.S & -a.S, TK);
+    m.q_boxes = SR % a.GQ == 0;
+    const auto u = [](int x) { return static_cast<uint64_t>(x); };
+    const uint64_t kv_ext[4] = {u(a.D), u(a.S), u(a.Hkv), u(a.blocks)};
+    const int64_t kv_str[4] = {1, a.token_stride, a.head_stride, a.block_stride};
+    const uint32_t kv_box[4] = {64, static_cast<uint32_t>(m.kb), 1, 1};
+    bool ok = encode(&m.k, a.k, F16, 4, kv_ext, kv_str, kv_box) && encode(&m.v, a.v, F16, 4, kv_ext, kv_str, kv_box);
+    if (ok && m.q_boxes) {
+        const uint64_t ext[3] = {u(a.D), u(a.Hq), u(a.T)};
+        const int64_t str[3] = {1, a.D, a.q_stride};
+        const uint32_t box[3] = {64, static_cast<uint32_t>(a.GQ), static_cast<uint32_t>(SR / a.GQ)};
+        ok = encode(&m.q, a.q, F16, 3, ext, str, box);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    return launch_dependent(kern, dim3(grid), THREADS, Sizes<DP>::SMEM, s, m, a);
 }
 
 }  // namespace

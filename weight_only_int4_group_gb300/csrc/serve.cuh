@@ -6,6 +6,26 @@
 
 namespace q4 {
 
+// Division of 0 <= n < 2^31 by a divisor fixed for the launch: with
+// 2^(s - 32) < d <= 2^(s - 31), n / d = n * (floor(2^s / d) + 1) >> s exactly
+// (Granlund and Montgomery 1994, for 31-bit n).
+struct FastDiv {
+    uint32_t mul, shift;
+    int d;
+    void set(int divisor)
+    {
+        d = divisor;
+        int l = 0;
+        while ((1ll << l) < divisor) ++l;
+        shift = 31 + l;
+        mul = static_cast<uint32_t>((1ull << shift) / static_cast<unsigned>(divisor) + 1);
+    }
+    __device__ __forceinline__ int div(int n) const
+    {
+        return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+    }
+};
+
 // One q4_attention call as its kernels see it.
 struct AttnArgs {
     const uint16_t *q, *k, *v;  // 16-bit elements, bf16 or f16
@@ -18,6 +38,7 @@ struct AttnArgs {
     int64_t table_stride;
     const int *q_start, *kv_len;
     int T, B, Hq, Hkv, GQ;  // GQ: query heads per KV head
+    FastDiv by_GQ, by_S;
     int D, S, blocks, width;
     float scale_log2;  // scale * log2(e): scores in units of log 2
     int window;        // 0: none
