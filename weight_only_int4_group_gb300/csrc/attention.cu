@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
 
     grid_dep_launch_dependents();
     grid_dep_wait();
-    const Range rng = cta_range<R, TK, NW>(a, ls);
+    const Range rng = cta_range<R, TK, NW, 1, 0>(a, ls);
     if (rng.u0 >= rng.u1) return;
 
     const uint32_t ring = smem_u32(smem) + warp * (STAGES * 2 * Z::TILE);

@@ -76,9 +76,9 @@ struct Item {
 };
 
 struct Range {
-    int64_t u0, u1, total;  // the CTA's units and all units of the call
+    int64_t u0, u1, total;  // the CTA's places and all places of the call's sequence
     int G;                  // CTAs that share them
-    Item first;             // item of unit u0
+    Item first;             // item of place u0
     int kt;                 // u0 within that item
 };
 
@@ -93,9 +93,10 @@ __device__ __forceinline__ int owner_of(int64_t i, int64_t T, int64_t G)
     return static_cast<int>(((i + 1) * G - 1) / T);
 }
 
-// Units of all row tiles of request b for one KV head.  Lanes hold one
+// Places of all row tiles of request b for one KV head: their units and PAD
+// more each.  Lanes hold one
 // request each; requests of many row tiles are summed by the whole warp.
-template <int R, int TK>
+template <int R, int TK, int PAD>
 __device__ __forceinline__ int64_t request_units(const AttnArgs &a, int b, bool in)
 {
     int t0, n = 0, kv = 0;
@@ -103,7 +104,7 @@ __device__ __forceinline__ int64_t request_units(const AttnArgs &a, int b, bool 
     const int nt = row_tiles(n, a.GQ, R);
     int64_t sum = 0;
     if (nt <= 2)
-        for (int rt = 0; rt < nt; ++rt) sum += Span<R, TK>(a, n, kv, rt).units;
+        for (int rt = 0; rt < nt; ++rt) sum += Span<R, TK>(a, n, kv, rt).units + PAD;
     unsigned big = __ballot_sync(0xffffffffu, nt > 2);
     const int lane = threadIdx.x & 31;
     while (big) {
@@ -112,7 +113,7 @@ __device__ __forceinline__ int64_t request_units(const AttnArgs &a, int b, bool 
         const int n2 = __shfl_sync(0xffffffffu, n, src), kv2 = __shfl_sync(0xffffffffu, kv, src),
                   nt2 = __shfl_sync(0xffffffffu, nt, src);
         int64_t part = 0;
-        for (int rt = lane; rt < nt2; rt += 32) part += Span<R, TK>(a, n2, kv2, rt).units;
+        for (int rt = lane; rt < nt2; rt += 32) part += Span<R, TK>(a, n2, kv2, rt).units + PAD;
 #pragma unroll
         for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
         if (lane == src) sum = part;
@@ -120,18 +121,18 @@ __device__ __forceinline__ int64_t request_units(const AttnArgs &a, int b, bool 
     return sum;
 }
 
-// The CTA's equal share of the call's units, and where it begins.  Every
+// The CTA's equal share of the call's sequence, and where it begins.  Every
 // thread of the CTA calls it (NW warps; two barriers); all get the result.
 // Warps sum slabs of requests, then the warp whose slab holds the CTA's first
 // unit walks it again.
-template <int R, int TK, int NW>
+template <int R, int TK, int NW, int MIN_UNITS, int PAD>
 __device__ Range cta_range(const AttnArgs &a, LocateScratch &ls)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b0 = static_cast<int>(static_cast<int64_t>(a.B) * warp / NW),
               b1 = static_cast<int>(static_cast<int64_t>(a.B) * (warp + 1) / NW);
     int64_t slab = 0;
-    for (int b = b0; b < b1; b += 32) slab += request_units<R, TK>(a, b + lane, b + lane < b1);
+    for (int b = b0; b < b1; b += 32) slab += request_units<R, TK, PAD>(a, b + lane, b + lane < b1);
 #pragma unroll
     for (int d = 16; d; d >>= 1) slab += __shfl_xor_sync(0xffffffffu, slab, d);
     if (lane == 0) ls.slab[warp] = slab;
@@ -143,15 +144,15 @@ __device__ Range cta_range(const AttnArgs &a, LocateScratch &ls)
         all += ls.slab[w];
     }
     const int64_t total = all * a.Hkv;
-    // no CTA between two others is left without a unit (the pieces of an item
-    // are counted by their CTAs)
-    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    // as many CTAs as get MIN_UNITS units each; none between two others is
+    // left without a unit (the pieces of an item are counted by their CTAs)
+    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + MIN_UNITS - 1) / MIN_UNITS));
     const bool mine_any = static_cast<int>(blockIdx.x) < G;
     const int64_t u0 = mine_any ? blockIdx.x * total / G : 0, u1 = mine_any ? (blockIdx.x + 1) * total / G : 0;
     int64_t left = u0 - before * a.Hkv;  // units to pass from the slab's start
     if (u0 < u1 && left >= 0 && left < slab * a.Hkv) {
         for (int b = b0; b < b1; b += 32) {
-            const int64_t mine = request_units<R, TK>(a, b + lane, b + lane < b1) * a.Hkv;
+            const int64_t mine = request_units<R, TK, PAD>(a, b + lane, b + lane < b1) * a.Hkv;
             int64_t incl = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -170,7 +171,7 @@ __device__ Range cta_range(const AttnArgs &a, LocateScratch &ls)
             request(a, b + src, t0, n, kv);
             const int nt = row_tiles(n, a.GQ, R);
             for (int rt = 0; rt < nt; rt += 32) {
-                const int64_t m2 = rt + lane < nt ? static_cast<int64_t>(Span<R, TK>(a, n, kv, rt + lane).units) * a.Hkv : 0;
+                const int64_t m2 = rt + lane < nt ? static_cast<int64_t>(Span<R, TK>(a, n, kv, rt + lane).units + PAD) * a.Hkv : 0;
                 int64_t in2 = m2;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -185,7 +186,7 @@ __device__ Range cta_range(const AttnArgs &a, LocateScratch &ls)
                 const int s2 = __ffs(past2) - 1;
                 left -= __shfl_sync(0xffffffffu, in2 - m2, s2);
                 if (lane == 0) {
-                    const int64_t per = Span<R, TK>(a, n, kv, rt + s2).units;
+                    const int64_t per = Span<R, TK>(a, n, kv, rt + s2).units + PAD;
                     ls.r.first.b = b + src;
                     ls.r.first.rt = rt + s2;
                     ls.r.first.head = static_cast<int>(left / per);

@@ -26,7 +26,8 @@
 //   warp 11         allocates tensor memory; one thread issues the MMAs.
 // Tensor memory (512 columns): the two subtiles' scores (128 columns each)
 // and outputs (head_dim each).  While one subtile's softmax runs, the other's
-// products do: the issue order is P0 V(j), Q0 K(j+1), P1 V(j), Q1 K(j+1).
+// products do: the issue order is P0 V(j), Q0 K(j+1), P1 V(j), Q1 K(j+1), on
+// through the ends of items.
 // MMAs of one thread run in order, so a subtile's next scores may be issued
 // right behind the product that reads the weights they overwrite, and scores
 // being complete implies that every earlier product is.
@@ -53,6 +54,10 @@ namespace {
 constexpr int R = 256;   // rows per item
 constexpr int SR = 128;  // rows per subtile
 constexpr int TK = 128;  // keys per unit
+// Places of the sequence that each item takes beside its units: beginning and
+// finishing an item costs about as much as two units.
+constexpr int PAD = 2;
+constexpr int MIN_UNITS = 4;  // per CTA: a piece that is joined costs about as much as two units
 constexpr int W_K = 8, W_V = 9, W_Q = 10;  // producers
 constexpr int W_M = 11;         // MMA issue
 constexpr int NW = 12, THREADS = NW * 32;  // 168 registers per thread; a 13th warp would cost 40 of them
@@ -67,9 +72,9 @@ struct Sizes {
     static constexpr int TILE = CH * CHUNK;      // 128 rows: a subtile's queries, a key or value tile
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_R = 2 * TILE;
-    static constexpr int OFF_O = OFF_R + 4 * TILE;  // output staging, 32 rows x 64 bytes per warp
-    static constexpr int OFF_B = OFF_O + 8 * 2048;
-    static constexpr int NBAR = 8 + 2 + 6 + 1;
+    static constexpr int OFF_O = OFF_R + 4 * TILE;  // output staging, 32 rows x 128 bytes per warp
+    static constexpr int OFF_B = OFF_O + 8 * 4096;
+    static constexpr int NBAR = 8 + 4 + 8 + 1;
     static constexpr int SMEM = OFF_B + NBAR * 8 + 32 + 1024;  // slack to align the base
     static constexpr int PART = SR * (DP + 2);  // floats of a subtile's partial result
     static constexpr uint32_t S_COL = 0, O_COL = 256;
@@ -80,25 +85,26 @@ struct Sizes {
 // A CTA's pieces of items, walked alike by every role.
 struct Walk {
     Item it;
-    int64_t u;         // first unit of the piece
+    int64_t v0, vu;    // the item's and the piece's place in the call's sequence
+    int vn;            // and its length there
     int kt, nu;        // units [kt, kt + nu) of the item
     int units, kt0;    // the item's units, the first one's index among the request's keys
     int row0, row1, t0, base, kv;
-    __device__ __forceinline__ Walk(const AttnArgs &a, const Range &r) : it(r.first), u(r.u0), kt(r.kt)
+    bool same;         // all but the head as in the piece before
+    __device__ __forceinline__ Walk(const AttnArgs &a, const Range &r) : it(r.first), same(false)
     {
-        if (u < r.u1) load(a, r);
+        vu = r.u0;
+        if (vu >= r.u1) return;
+        load(a, r);
+        cut(r, r.kt);
+        while (nu <= 0 && vu < r.u1) step(a, r);
     }
+    __device__ __forceinline__ bool more(const Range &r) const { return vu < r.u1; }
+    // The next piece that holds a unit.
     __device__ __forceinline__ void next(const AttnArgs &a, const Range &r)
     {
-        u += nu;
-        kt = 0;
-        if (u >= r.u1) return;
-        if (++it.head < a.Hkv) {  // the same rows and keys of the next head
-            nu = static_cast<int>(min(static_cast<int64_t>(units), r.u1 - u));
-            return;
-        }
-        it.next_rows(a, R);
-        load(a, r);
+        do step(a, r);
+        while (nu <= 0 && vu < r.u1);
     }
     __device__ __forceinline__ bool whole() const { return kt == 0 && nu == units; }
     // Units [lo, hi) of the piece that subtile w sees, and the places of its
@@ -133,7 +139,38 @@ private:
         t0 = sp.t0;
         base = sp.base;
         kv = sp.kv;
-        nu = static_cast<int>(min(static_cast<int64_t>(units - kt), r.u1 - u));
+    }
+    // The piece of the item from its place v on: the first PAD places of an
+    // item hold no unit.
+    __device__ __forceinline__ void cut(const Range &r, int v)
+    {
+        v0 = vu - v;
+        vn = static_cast<int>(min(static_cast<int64_t>(units + PAD - v), r.u1 - vu));
+        kt = max(v - PAD, 0);
+        nu = max(v + vn - PAD, 0) - kt;
+    }
+    __device__ __forceinline__ void step(const AttnArgs &a, const Range &r)
+    {
+        const bool was_whole = whole();
+        vu += vn;
+        same = false;
+        if (vu >= r.u1) return;
+        if (++it.head < a.Hkv) {  // the same rows and keys of the next head
+            cut(r, 0);
+            same = was_whole && nu == units;
+            return;
+        }
+        it.next_rows(a, R);
+        load(a, r);
+        cut(r, 0);
+    }
+
+public:
+    // First and last CTA that hold units of the item.
+    __device__ __forceinline__ void holders(const Range &r, int &first, int &last) const
+    {
+        first = owner_of(v0 + PAD, r.total, r.G);
+        last = owner_of(v0 + PAD + units - 1, r.total, r.G);
     }
 };
 
@@ -211,8 +248,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
     // queries; sfull: scores ready; pfull: weights stored (and the output
     // rescaled); ofull: output complete.  Each lane of a producer arrives.
     uint64_t *kfull = reinterpret_cast<uint64_t *>(smem + Z::OFF_B), *kempty = kfull + 4;
-    uint64_t *qfull = kempty + 4, *qempty = qfull + 1, *sfull = qempty + 1, *pfull = sfull + 2;
-    uint64_t *ofull = pfull + 2, *drain = ofull + 2;
+    uint64_t *qfull = kempty + 4, *qempty = qfull + 2, *sfull = qempty + 2, *pfull = sfull + 2;
+    uint64_t *ofull = pfull + 4, *drain = ofull + 2;  // pfull: [subtile][half of the tile's keys]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_s = reinterpret_cast<volatile int *>(tmem_slot + 2);  // [2]
@@ -224,11 +261,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
             mbar_init(&kfull[i], 32);
             mbar_init(&kempty[i], 1);
         }
-        mbar_init(qfull, 32);
-        mbar_init(qempty, 1);
         for (int w = 0; w < 2; ++w) {
+            mbar_init(&qfull[w], 32);
+            mbar_init(&qempty[w], 1);
             mbar_init(&sfull[w], 1);
-            mbar_init(&pfull[w], 4);
+            mbar_init(&pfull[2 * w], 4);
+            mbar_init(&pfull[2 * w + 1], 4);
             mbar_init(&ofull[w], 1);
         }
         mbar_init(drain, 1);
@@ -239,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
     grid_dep_launch_dependents();
     grid_dep_wait();
     tc_fence_before();
-    const Range rng = cta_range<R, TK, NW>(a, ls);  // barriers inside
+    const Range rng = cta_range<R, TK, NW, MIN_UNITS, PAD>(a, ls);  // barriers inside
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -265,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         const uint32_t bd = ch * Z::CHUNK + bk * 128;
         Walk k(a, rng);
         int g = 0;  // units loaded
-        for (; ok && k.u < rng.u1 && !a.debug_no_copy; k.next(a, rng)) {
+        for (; ok && k.more(rng) && !a.debug_no_copy; k.next(a, rng)) {
             const int *trow = a.table + k.it.b * a.table_stride;
             auto block_of = [&](int key) { return key < k.kv ? __ldg(trow + a.by_S.div(key)) : -1; };
             const int first = (k.kt0 + k.kt) * TK;
@@ -320,52 +358,57 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
         const uint32_t sq = smem_u32(smem + Z::OFF_Q);
         Walk k(a, rng);
-        int pc = 0;
-        for (; k.u < rng.u1 && !a.debug_no_copy; ++pc, k.next(a, rng)) {
-            if (pc > 0 && !(ok = warp_wait(qempty, (pc - 1) & 1))) break;
-            if (maps.q_boxes) {
-                // lane: one chunk of one subtile.  Rows past the request's are
-                // other requests' (or zeros past T): their results go nowhere
-                if (lane < 2 * Z::CH) {
-                    const int w = lane / Z::CH, ch = lane % Z::CH;
-                    mbar_arrive_expect_tx(qfull, SR * 128);
-                    tma_load_3d(sq + w * Z::TILE + ch * Z::CHUNK, &maps.q, ch * 64, k.it.head * a.GQ,
-                                k.t0 + a.by_GQ.div(k.row0 + w * SR), qfull);
+        int pc = 0, loaded = 0;
+        for (; ok && k.more(rng) && !a.debug_no_copy; ++pc, k.next(a, rng)) {
+            for (int w = 0; w < 2; ++w) {
+                if (pc > 0 && !(ok = warp_wait(&qempty[w], (pc - 1) & 1))) break;
+                ++loaded;
+                const uint32_t dst = sq + w * Z::TILE;
+                if (maps.q_boxes) {
+                    // lane: one chunk.  Rows past the request's are other
+                    // requests' (or zeros past T): their results go nowhere
+                    if (lane < Z::CH) {
+                        mbar_arrive_expect_tx(&qfull[w], SR * 128);
+                        tma_load_3d(dst + lane * Z::CHUNK, &maps.q, lane * 64, k.it.head * a.GQ,
+                                    k.t0 + a.by_GQ.div(k.row0 + w * SR), &qfull[w]);
+                    } else {
+                        mbar_arrive(&qfull[w]);
+                    }
+                    __syncwarp();
                 } else {
-                    mbar_arrive(qfull);
-                }
-                __syncwarp();
-            } else {
-                constexpr int RPI = 32 / C8;
-                const int c = lane % C8, hi = lane / C8;
-                const int dt = RPI / a.GQ, dg = RPI - dt * a.GQ;
-                int r = k.row0 + hi, t = a.by_GQ.div(r), g = r - t * a.GQ;
-                const uint16_t *src = a.q + (k.t0 + t) * a.q_stride +
-                                      static_cast<int64_t>(k.it.head * a.GQ + g) * a.D + c * 8;
-                const int64_t step = dt * a.q_stride + static_cast<int64_t>(dg) * a.D;
-                const int64_t wrap = a.q_stride - static_cast<int64_t>(a.GQ) * a.D;
+                    constexpr int RPI = 32 / C8;
+                    const int c = lane % C8, hi = lane / C8;
+                    const int dt = RPI / a.GQ, dg = RPI - dt * a.GQ;
+                    const int r = k.row0 + w * SR + hi, t = a.by_GQ.div(r);
+                    int g = r - t * a.GQ, left = k.row1 - r;  // rows from this one on
+                    const uint16_t *src = a.q + (k.t0 + t) * a.q_stride +
+                                          static_cast<int64_t>(k.it.head * a.GQ + g) * a.D + c * 8;
+                    const int64_t step = dt * a.q_stride + static_cast<int64_t>(dg) * a.D;
+                    const int64_t wrap = a.q_stride - static_cast<int64_t>(a.GQ) * a.D;
 #pragma unroll 1
-                for (int r0 = 0; r0 < R; r0 += 8) {
+                    for (int r0 = 0; r0 < SR; r0 += 8) {
 #pragma unroll
-                    for (int l = 0; l < 8 / RPI; ++l) {
-                        const int row = l * RPI + hi;  // within 8 rows
-                        const bool in = k.row0 + r0 + row < k.row1 && c * 8 < a.D;
-                        cp_async16(sq + (r0 / SR) * Z::TILE + (c >> 3) * Z::CHUNK + ((r0 & (SR - 1)) + row) * 128 +
-                                       (((c & 7) ^ row) << 4),
-                                   in ? src : a.q, in);
-                        src += step;
-                        g += dg;
-                        if (g >= a.GQ) {
-                            g -= a.GQ;
-                            src += wrap;
+                        for (int l = 0; l < 8 / RPI; ++l) {
+                            const int row = l * RPI + hi;  // within 8 rows
+                            const bool in = left > 0 && c * 8 < a.D;
+                            cp_async16(dst + (c >> 3) * Z::CHUNK + (r0 + row) * 128 + (((c & 7) ^ row) << 4),
+                                       in ? src : a.q, in);
+                            left -= RPI;
+                            src += step;
+                            g += dg;
+                            if (g >= a.GQ) {
+                                g -= a.GQ;
+                                src += wrap;
+                            }
                         }
                     }
+                    cp_async_arrive(&qfull[w]);
                 }
-                cp_async_arrive(qfull);
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (pc > 0) mbar_wait_bounded(qfull, (pc - 1) & 1, abort_flag, a.wait_ns, a.err, false);
+        for (int i = max(0, loaded - 2); i < loaded; ++i)
+            mbar_wait_bounded(&qfull[i & 1], (i >> 1) & 1, abort_flag, a.wait_ns, a.err, false);
         __syncwarp();
     } else if (warp == W_M) {
         // ---------------------------------------------------- MMA issue
@@ -390,16 +433,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
             }
             mma_commit_elected(&sfull[w]);
         };
-        auto pv = [&](auto w_, int s, bool acc) {
+        auto pv = [&](auto w_, int s, bool acc, uint32_t parity) {
             constexpr int w = decltype(w_)::value;
             const uint64_t b = dv + ((s * Z::TILE) >> 4);
 #pragma unroll
-            for (int k = 0; k < TK / 16; ++k)
-                mma_ts(tm + Z::O_COL + w * DP, tm + Z::S_COL + w * 128 + k * 8, b + ((k * 16 * 128) >> 4), id_pv,
-                       acc || k > 0);
+            for (int h = 0; h < 2; ++h) {
+                if (!warp_wait(&pfull[2 * w + h], parity)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = h * TK / 32; k < (h + 1) * TK / 32; ++k)
+                    mma_ts(tm + Z::O_COL + w * DP, tm + Z::S_COL + w * 128 + k * 8, b + ((k * 16 * 128) >> 4), id_pv,
+                           acc || k > 0);
+            }
+            return true;
         };
         Walk k(a, rng);
-        int g = 0;                  // units before this piece
+        int g = 0;                  // units so far
         uint32_t np0 = 0, np1 = 0;  // weights consumed per subtile
         using W0 = std::integral_constant<int, 0>;
         using W1 = std::integral_constant<int, 1>;
@@ -408,42 +457,64 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
             fence_proxy_async_smem();
             return true;
         };
-        for (int pc = 0; ok && k.u < rng.u1; ++pc, k.next(a, rng)) {
-            const Walk::Seen s0 = k.seen(a, 0), s1 = k.seen(a, 1);
-            if (!(ok = warp_wait(qfull, pc & 1))) break;
-            if (!(ok = landed(g & 1, g))) break;
-            if (s0.a == 0 && s0.b > 0) qk(W0(), g & 1);
-            if (s1.a == 0 && s1.b > 0) qk(W1(), g & 1);
-            mma_commit_elected(&kempty[g & 1]);
-            if (k.nu == 1) mma_commit_elected(qempty);
-            for (int j = 0; j < k.nu; ++j) {
-                const int v = g & 1, nk = (g + 1) & 1;
-                const bool more = j + 1 < k.nu;
-                if (!(ok = landed(2 + v, g))) break;
-                if (j >= s0.a && j < s0.b) {
-                    if (!(ok = warp_wait(&pfull[0], np0++ & 1))) break;
-                    tc_fence_after();
-                    pv(W0(), 2 + v, j > s0.a);
-                    if (j == s0.b - 1) mma_commit_elected(&ofull[0]);
-                }
-                if (more) {
-                    if (!(ok = landed(nk, g + 1))) break;
-                    if (j + 1 >= s0.a && j + 1 < s0.b) qk(W0(), nk);
-                }
-                if (j >= s1.a && j < s1.b) {
-                    if (!(ok = warp_wait(&pfull[1], np1++ & 1))) break;
-                    tc_fence_after();
-                    pv(W1(), 2 + v, j > s1.a);
-                    if (j == s1.b - 1) mma_commit_elected(&ofull[1]);
-                }
-                mma_commit_elected(&kempty[2 + v]);
-                if (more) {
-                    if (j + 1 >= s1.a && j + 1 < s1.b) qk(W1(), nk);
-                    mma_commit_elected(&kempty[nk]);
-                    if (j + 2 == k.nu) mma_commit_elected(qempty);
-                }
-                ++g;
+        // The subtiles' streams run over the pieces' ends: while one subtile's
+        // rows finish an item, the other's, and its own next scores, go on.
+        Walk::Seen s0 = {}, s1 = {};
+        int j = 0, pc = 0;
+        if (k.more(rng)) {
+            s0 = k.seen(a, 0);
+            s1 = k.seen(a, 1);
+            ok = warp_wait(&qfull[0], 0) && warp_wait(&qfull[1], 0) && landed(0, 0);
+            if (ok) {
+                if (s0.a == 0 && s0.b > 0) qk(W0(), 0);
+                if (k.nu == 1) mma_commit_elected(&qempty[0]);
+                if (s1.a == 0 && s1.b > 0) qk(W1(), 0);
+                if (k.nu == 1) mma_commit_elected(&qempty[1]);
+                mma_commit_elected(&kempty[0]);
             }
+        }
+        while (ok && k.more(rng)) {
+            const int v = g & 1, nk = (g + 1) & 1;
+            // the unit after this one: of this piece or the first of the next
+            const bool turn = j + 1 == k.nu;
+            const int was0 = j - s0.a, was1 = j - s1.a;
+            const bool on0 = was0 >= 0 && j < s0.b, on1 = was1 >= 0 && j < s1.b;
+            const bool end0 = j == s0.b - 1, end1 = j == s1.b - 1;
+            if (turn) {
+                k.next(a, rng);
+                j = 0;
+                ++pc;
+                if (!k.same && k.more(rng)) {
+                    s0 = k.seen(a, 0);
+                    s1 = k.seen(a, 1);
+                }
+            } else {
+                ++j;
+            }
+            const bool more = k.more(rng), last = j + 1 == k.nu;
+            if (!(ok = landed(2 + v, g))) break;
+            if (on0) {
+                if (!(ok = pv(W0(), 2 + v, was0 > 0, np0++ & 1))) break;
+                if (end0) mma_commit_elected(&ofull[0]);
+            }
+            if (more) {
+                if (turn && !(ok = warp_wait(&qfull[0], pc & 1))) break;
+                if (!(ok = landed(nk, g + 1))) break;
+                if (j >= s0.a && j < s0.b) qk(W0(), nk);
+                if (last) mma_commit_elected(&qempty[0]);
+            }
+            if (on1) {
+                if (!(ok = pv(W1(), 2 + v, was1 > 0, np1++ & 1))) break;
+                if (end1) mma_commit_elected(&ofull[1]);
+            }
+            mma_commit_elected(&kempty[2 + v]);
+            if (more) {
+                if (turn && !(ok = warp_wait(&qfull[1], pc & 1))) break;
+                if (j >= s1.a && j < s1.b) qk(W1(), nk);
+                if (last) mma_commit_elected(&qempty[1]);
+                mma_commit_elected(&kempty[nk]);
+            }
+            ++g;
         }
         // MMAs in flight end before tensor memory is freed
         mma_commit_elected(drain);
@@ -455,13 +526,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         const int w = warp >> 2, rr = tid & (SR - 1);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field: 32 * (warp % 4) << 16
         const uint32_t ts = tmem + lanes + Z::S_COL + w * 128, to = tmem + lanes + Z::O_COL + w * DP;
-        const bool neg = a.scale_log2 < 0.0f;
+        const bool neg = a.scale_log2 <= 0.0f;
         uint32_t ns = 0, no = 0;
-        for (Walk k(a, rng); k.u < rng.u1; k.next(a, rng)) {
-            const Walk::Seen p = k.seen(a, w);
-            const int r = k.row0 + w * SR + rr;
-            const bool in = r < k.row1;
-            const int place = in ? k.base + a.by_GQ.div(r) : -1;
+        Walk::Seen p;
+        int r, place;
+        bool in;
+        for (Walk k(a, rng); k.more(rng); k.next(a, rng)) {
+            if (!k.same) {
+                p = k.seen(a, w);
+                r = k.row0 + w * SR + rr;
+                in = r < k.row1;
+                place = in ? k.base + a.by_GQ.div(r) : -1;
+            }
             float m = -INFINITY, l = 0.0f;
             for (int j = p.a; ok && j < p.b; ++j, ++ns) {
                 if (!(ok = warp_wait(&sfull[w], ns & 1))) break;
@@ -475,15 +551,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32x(ts + c * 32, v[c]);
                 tmem_wait_ld();
-                const bool pre = part || neg;  // scores scaled and masked first
-                if (pre) {
+                if (neg) {  // the maximum is taken of scaled scores (hidden ones are -inf, not -inf * 0)
 #pragma unroll
-                    for (int i = 0; i < TK; ++i) {
-                        const float x = __uint_as_float(v[i / 32][i % 32]) * a.scale_log2;
-                        v[i / 32][i % 32] = __float_as_uint(i >= c0 && i <= c1 ? x : -INFINITY);
+                    for (int i = 0; i < TK; ++i)
+                        v[i / 32][i % 32] = __float_as_uint(__uint_as_float(v[i / 32][i % 32]) * a.scale_log2);
+                }
+                if (part) {
+                    constexpr uint32_t HIDDEN = 0xFF800000u;  // -inf
+#pragma unroll
+                    for (int i = 0; i < TK; ++i)
+                        if (i > c1) v[i / 32][i % 32] = HIDDEN;
+                    if (a.window > 0) {
+#pragma unroll
+                        for (int i = 0; i < TK; ++i)
+                            if (i < c0) v[i / 32][i % 32] = HIDDEN;
                     }
                 }
-                const float sc = pre ? 1.0f : a.scale_log2;
+                const float sc = neg ? 1.0f : a.scale_log2;
                 float m4[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(v[c][0]);
@@ -520,26 +604,27 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 const float2 sc2 = make_float2(sc, sc), rf2 = make_float2(-ref, -ref);
                 float2 s2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t pk[32];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
-                        float2 x = make_float2(__uint_as_float(v[2 * c + i / 32][i % 32]),
-                                               __uint_as_float(v[2 * c + i / 32][i % 32 + 1]));
+                    for (int i = 0; i < 32; i += 2) {
+                        float2 x = make_float2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
                         x = fma2(x, sc2, rf2);
                         x.x = ex2(x.x);
                         x.y = ex2(x.y);
                         s2[(i / 2) & 1] = add2(s2[(i / 2) & 1], x);
                         pk[i / 2] = pack2<F16>(x.x, x.y);
                     }
-                    tmem_st32(ts + c * 32, pk);
+                    tmem_st16(ts + c * 16, pk);
+                    if (c & 1) {  // half of the keys: the second product may begin
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&pfull[2 * w + c / 2]);
+                    }
                 }
                 s2[0] = add2(s2[0], s2[1]);
                 l += s2[0].x + s2[0].y;
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&pfull[w]);
             }
             const bool any = p.b > p.a;
             if (ok && any) {
@@ -572,44 +657,40 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                         if (in) store_dims<F16, 32>(a, t_row, h_row, c, o);
                     }
                 } else {
-                    // 32 dims of the warp's 32 rows turn through shared
-                    // memory, so that 4 lanes store 64 bytes of one row
-                    uint8_t *st = smem + Z::OFF_O + warp * 2048;
-                    const int q = lane & 3;
-                    int64_t at[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int x = k.row0 + w * SR + (warp & 3) * 32 + i * 8 + lane / 4;
-                        const int t = a.by_GQ.div(x);
-                        at[i] = x < k.row1 ? (k.t0 + t) * a.o_stride +
-                                                 static_cast<int64_t>(k.it.head * a.GQ + x - t * a.GQ) * a.D + q * 8
-                                           : -1;
-                    }
+                    // 64 dims of the warp's 32 rows turn through shared
+                    // memory, so that 8 lanes store 128 bytes of one row
+                    uint8_t *st = smem + Z::OFF_O + warp * 4096;
+                    const int q = lane & 7;
                     const int64_t o_len = static_cast<int64_t>(a.T - 1) * a.o_stride + static_cast<int64_t>(a.Hq) * a.D;
 #pragma unroll 1
-                    for (int c = 0; c < DP; c += 32) {
-                        uint32_t v[32] = {};
+                    for (int c = 0; c < DP; c += 64) {
+                        uint32_t v[2][32] = {};
                         __syncwarp();
                         if (any) {
-                            tmem_ld32x(to + c, v);
+                            tmem_ld32x(to + c, v[0]);
+                            tmem_ld32x(to + c + 32, v[1]);
                             tmem_wait_ld();
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
+                        for (int i = 0; i < 64; i += 8) {
                             uint4 x;
                             uint32_t *y = reinterpret_cast<uint32_t *>(&x);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                y[e] = pack2<F16>(__uint_as_float(v[i + 2 * e]) * inv, __uint_as_float(v[i + 2 * e + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(st + lane * 64 + (((i / 8) ^ ((lane >> 1) & 3)) << 4)) = x;
+                                y[e] = pack2<F16>(__uint_as_float(v[i / 32][i % 32 + 2 * e]) * inv,
+                                                  __uint_as_float(v[i / 32][i % 32 + 2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(st + lane * 128 + (((i / 8) ^ (lane & 7)) << 4)) = x;
                         }
                         __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int x = i * 8 + lane / 4;
-                            const uint4 y = *reinterpret_cast<const uint4 *>(st + x * 64 + ((q ^ ((x >> 1) & 3)) << 4));
-                            if (at[i] >= 0 && c + q * 8 < a.D && store_ok(at[i] + c + 7, o_len, a.err))
-                                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + at[i] + c) = y;
+                        for (int i = 0; i < 8; ++i) {
+                            const int x = i * 4 + lane / 8, gr = k.row0 + w * SR + (warp & 3) * 32 + x;
+                            const uint4 y = *reinterpret_cast<const uint4 *>(st + x * 128 + ((q ^ (x & 7)) << 4));
+                            const int t = a.by_GQ.div(gr);
+                            const int64_t at = (k.t0 + t) * a.o_stride +
+                                               static_cast<int64_t>(k.it.head * a.GQ + gr - t * a.GQ) * a.D + c + q * 8;
+                            if (gr < k.row1 && c + q * 8 < a.D && store_ok(at + 7, o_len, a.err))
+                                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + at) = y;
                         }
                     }
                 }
@@ -635,8 +716,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                     ps[DP * SR + rr] = m;
                     ps[(DP + 1) * SR + rr] = l;
                 }
-                const int64_t i0 = k.u - k.kt, i1 = i0 + k.units;
-                const int f0 = owner_of(i0, rng.total, rng.G), f1 = owner_of(i1 - 1, rng.total, rng.G);
+                int f0, f1;
+                k.holders(rng, f0, f1);
                 named_barrier_sync(1 + w, SR);
                 if (rr == 0) {
                     const int at = 2 * f0 + w;
@@ -646,36 +727,61 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                     last_s[w] = last;
                 }
                 named_barrier_sync(1 + w, SR);
-                if (last_s[w] && in) {
+                if (last_s[w]) {  // whole warps: they read tensor memory
                     auto slot = [&](int f) {
                         return a.part + ((2 * static_cast<int64_t>(f) + (f == f0)) * 2 + w) * Z::PART + rr;
                     };
+                    // each part's weight once, kept in shared memory while
+                    // there are few parts
+                    constexpr int KEPT = 32;
+                    float *kept = reinterpret_cast<float *>(smem + Z::OFF_O + warp * 4096) + lane;  // [part][lane]
                     float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
                     for (int f = f0; f <= f1; ++f) top = fmaxf(top, __ldcg(slot(f) + DP * SR));
                     const float ref = top == -INFINITY ? 0.0f : top;
+                    auto weight = [&](int f) { return ex2(__ldcg(slot(f) + DP * SR) - ref); };
+#pragma unroll 4
+                    for (int f = f0; f <= f1; ++f) {
+                        const float g = weight(f);
+                        sum += g * __ldcg(slot(f) + (DP + 1) * SR);
+                        if (f - f0 < KEPT) kept[(f - f0) * 32] = g;
+                    }
+                    const float inv = inverse(sum);
+                    // the CTA's own part is still in tensor memory
+                    const int mine = static_cast<int>(blockIdx.x);
 #pragma unroll 1
-                    for (int d = 0; d < DP; d += 32) {
-                        float o[32];
+                    for (int d = 0; d < DP; d += 64) {
+                        float o[64];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-                        sum = 0.0f;
+                        for (int i = 0; i < 64; ++i) o[i] = 0.0f;
 #pragma unroll 1
                         for (int f = f0; f <= f1; ++f) {
                             const float *x = slot(f);
-                            float y[32];
+                            uint32_t y[64];
+                            if (f != mine) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) y[i] = __ldcg(x + (d + i) * SR);
-                            const float g = ex2(__ldcg(x + DP * SR) - ref);
-                            sum += g * __ldcg(x + (DP + 1) * SR);
+                                for (int i = 0; i < 64; ++i) y[i] = __float_as_uint(__ldcg(x + (d + i) * SR));
+                            } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] += g * y[i];
+                                for (int i = 0; i < 64; i += 32) {
+                                    uint32_t z[32] = {};
+                                    if (any) {
+                                        tmem_ld32x(to + d + i, z);
+                                        tmem_wait_ld();
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) y[i + e] = z[e];
+                                }
+                            }
+                            const float g = f - f0 < KEPT ? kept[(f - f0) * 32] : weight(f);
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) o[i] = fmaf(g, __uint_as_float(y[i]), o[i]);
                         }
-                        const float inv = inverse(sum);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= inv;
-                        store_dims<F16, 32>(a, t_row, h_row, d, o);
+                        for (int i = 0; i < 64; ++i) o[i] *= inv;
+                        if (in) store_dims<F16, 64>(a, t_row, h_row, d, o);
                     }
-                    store_lse(a, t_row, h_row, top, sum);
+                    if (in) store_lse(a, t_row, h_row, top, sum);
                 }
                 __syncwarp();
             }
