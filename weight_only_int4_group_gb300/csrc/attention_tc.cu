@@ -74,8 +74,8 @@ struct Sizes {
     static constexpr int OFF_R = 2 * TILE;
     static constexpr int OFF_O = OFF_R + 4 * TILE;  // output staging, 32 rows x 128 bytes per warp
     static constexpr int OFF_B = OFF_O + 8 * 4096;
-    static constexpr int NBAR = 8 + 4 + 8 + 1;
-    static constexpr int SMEM = OFF_B + NBAR * 8 + 32 + 1024;  // slack to align the base
+    static constexpr int NBAR = 8 + 4 + 6 + 1;
+    static constexpr int SMEM = OFF_B + NBAR * 8 + 64 + 1024;  // slack to align the base
     static constexpr int PART = SR * (DP + 2);  // floats of a subtile's partial result
     static constexpr uint32_t S_COL = 0, O_COL = 256;
     static_assert(O_COL + 2 * DP <= 512, "scores and outputs fit tensor memory");
@@ -100,6 +100,8 @@ struct Walk {
         while (nu <= 0 && vu < r.u1) step(a, r);
     }
     __device__ __forceinline__ bool more(const Range &r) const { return vu < r.u1; }
+    // Another piece follows (one that would be padding alone does not count).
+    __device__ __forceinline__ bool follows(const Range &r) const { return r.u1 - (vu + vn) > PAD; }
     // The next piece that holds a unit.
     __device__ __forceinline__ void next(const AttnArgs &a, const Range &r)
     {
@@ -181,10 +183,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
                  : "memory");
 }
 
-// This lane's arrival on bar once its copies so far have landed.
+// This lane's arrival on bar after its copies so far have landed, in order
+// with the tensor cores' reads.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
 {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    mbar_arrive(bar);
 }
 
 // a * b + c and a + b on pairs of f32
@@ -249,10 +254,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
     // rescaled); ofull: output complete.  Each lane of a producer arrives.
     uint64_t *kfull = reinterpret_cast<uint64_t *>(smem + Z::OFF_B), *kempty = kfull + 4;
     uint64_t *qfull = kempty + 4, *qempty = qfull + 2, *sfull = qempty + 2, *pfull = sfull + 2;
-    uint64_t *ofull = pfull + 4, *drain = ofull + 2;  // pfull: [subtile][half of the tile's keys]
+    uint64_t *ofull = pfull + 2, *drain = ofull + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_s = reinterpret_cast<volatile int *>(tmem_slot + 2);  // [2]
+    // what the MMA warp needs of a piece, written by the query producer before
+    // it arrives on qfull[0] (pieces in turn): units, each subtile's first and
+    // last of them, whether another piece follows
+    volatile int *note = reinterpret_cast<volatile int *>(tmem_slot + 4);  // [2][6]
     __shared__ LocateScratch ls;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -265,8 +274,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
             mbar_init(&qfull[w], 32);
             mbar_init(&qempty[w], 1);
             mbar_init(&sfull[w], 1);
-            mbar_init(&pfull[2 * w], 4);
-            mbar_init(&pfull[2 * w + 1], 4);
+            mbar_init(&pfull[w], 4);
             mbar_init(&ofull[w], 1);
         }
         mbar_init(drain, 1);
@@ -342,8 +350,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                                        ok16 ? base + row * a.token_stride : vh, ok16);
                         }
                     }
-                    // the lane's arrival when its copies have landed; the MMA
-                    // warp fences the proxies after its wait
                     cp_async_arrive(&full[s]);
                 }
             }
@@ -358,11 +364,28 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
         const uint32_t sq = smem_u32(smem + Z::OFF_Q);
         Walk k(a, rng);
+        Walk::Seen s0, s1;
         int pc = 0, loaded = 0;
         for (; ok && k.more(rng) && !a.debug_no_copy; ++pc, k.next(a, rng)) {
             for (int w = 0; w < 2; ++w) {
+                if (w == 0 && !k.same) {
+                    s0 = k.seen(a, 0);
+                    s1 = k.seen(a, 1);
+                }
                 if (pc > 0 && !(ok = warp_wait(&qempty[w], (pc - 1) & 1))) break;
                 ++loaded;
+                if (w == 0) {
+                    if (lane == 0) {
+                        volatile int *x = note + (pc & 1) * 6;
+                        x[0] = k.nu;
+                        x[1] = s0.a;
+                        x[2] = s0.b;
+                        x[3] = s1.a;
+                        x[4] = s1.b;
+                        x[5] = k.follows(rng);
+                    }
+                    __syncwarp();
+                }
                 const uint32_t dst = sq + w * Z::TILE;
                 if (maps.q_boxes) {
                     // lane: one chunk.  Rows past the request's are other
@@ -425,93 +448,90 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         // with the values in slot s
         auto qk = [&](auto w_, int s) {
             constexpr int w = decltype(w_)::value;
-            const uint64_t b = dk + ((s * Z::TILE) >> 4);
+            const uint64_t k0 = dk + ((s * Z::TILE) >> 4);
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
                 const int o = (k / 4) * Z::CHUNK + (k % 4) * 32;
-                mma_ss(tm + Z::S_COL + w * 128, dq + ((w * Z::TILE + o) >> 4), b + (o >> 4), id_qk, k > 0);
+                mma_ss(tm + Z::S_COL + w * 128, dq + ((w * Z::TILE + o) >> 4), k0 + (o >> 4), id_qk, k > 0);
             }
             mma_commit_elected(&sfull[w]);
         };
         auto pv = [&](auto w_, int s, bool acc, uint32_t parity) {
             constexpr int w = decltype(w_)::value;
-            const uint64_t b = dv + ((s * Z::TILE) >> 4);
+            if (!warp_wait(&pfull[w], parity)) return false;
+            tc_fence_after();
+            const uint64_t v0 = dv + (((2 + s) * Z::TILE) >> 4);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!warp_wait(&pfull[2 * w + h], parity)) return false;
-                tc_fence_after();
-#pragma unroll
-                for (int k = h * TK / 32; k < (h + 1) * TK / 32; ++k)
-                    mma_ts(tm + Z::O_COL + w * DP, tm + Z::S_COL + w * 128 + k * 8, b + ((k * 16 * 128) >> 4), id_pv,
-                           acc || k > 0);
-            }
+            for (int k = 0; k < TK / 16; ++k)
+                mma_ts(tm + Z::O_COL + w * DP, tm + Z::S_COL + w * 128 + k * 8, v0 + ((k * 16 * 128) >> 4), id_pv,
+                       acc || k > 0);
             return true;
         };
-        Walk k(a, rng);
         int g = 0;                  // units so far
         uint32_t np0 = 0, np1 = 0;  // weights consumed per subtile
-        using W0 = std::integral_constant<int, 0>;
-        using W1 = std::integral_constant<int, 1>;
-        auto landed = [&](int slot, int unit) {
-            if (!warp_wait(&kfull[slot], (unit >> 1) & 1)) return false;
-            fence_proxy_async_smem();
-            return true;
-        };
+        using C0 = std::integral_constant<int, 0>;
+        using C1 = std::integral_constant<int, 1>;
         // The subtiles' streams run over the pieces' ends: while one subtile's
         // rows finish an item, the other's, and its own next scores, go on.
-        Walk::Seen s0 = {}, s1 = {};
+        int nu = 0, a0 = 0, b0 = 0, a1 = 0, b1 = 0, follows = 0;  // the piece
         int j = 0, pc = 0;
-        if (k.more(rng)) {
-            s0 = k.seen(a, 0);
-            s1 = k.seen(a, 1);
-            ok = warp_wait(&qfull[0], 0) && warp_wait(&qfull[1], 0) && landed(0, 0);
+        bool more = Walk(a, rng).more(rng);  // there is a next unit
+        auto read_note = [&]() {
+            const volatile int *x = note + (pc & 1) * 6;
+            nu = x[0];
+            a0 = x[1];
+            b0 = x[2];
+            a1 = x[3];
+            b1 = x[4];
+            follows = x[5];
+        };
+        if (more) {
+            ok = warp_wait(&qfull[0], 0) && warp_wait(&qfull[1], 0) && warp_wait(&kfull[0], 0);
             if (ok) {
-                if (s0.a == 0 && s0.b > 0) qk(W0(), 0);
-                if (k.nu == 1) mma_commit_elected(&qempty[0]);
-                if (s1.a == 0 && s1.b > 0) qk(W1(), 0);
-                if (k.nu == 1) mma_commit_elected(&qempty[1]);
+                read_note();
+                if (a0 == 0 && b0 > 0) qk(C0(), 0);
+                if (nu == 1) mma_commit_elected(&qempty[0]);
+                if (a1 == 0 && b1 > 0) qk(C1(), 0);
+                if (nu == 1) mma_commit_elected(&qempty[1]);
                 mma_commit_elected(&kempty[0]);
             }
         }
-        while (ok && k.more(rng)) {
-            const int v = g & 1, nk = (g + 1) & 1;
+        while (ok && more) {
+            // unit g: its values in slot v of theirs, the next unit's keys in
+            // slot nk of theirs
+            const int v = g & 1, nk = v ^ 1;
             // the unit after this one: of this piece or the first of the next
-            const bool turn = j + 1 == k.nu;
-            const int was0 = j - s0.a, was1 = j - s1.a;
-            const bool on0 = was0 >= 0 && j < s0.b, on1 = was1 >= 0 && j < s1.b;
-            const bool end0 = j == s0.b - 1, end1 = j == s1.b - 1;
-            if (turn) {
-                k.next(a, rng);
-                j = 0;
-                ++pc;
-                if (!k.same && k.more(rng)) {
-                    s0 = k.seen(a, 0);
-                    s1 = k.seen(a, 1);
-                }
-            } else {
-                ++j;
+            const bool turn = j + 1 == nu;
+            more = !turn || follows;
+            // what the unit needs beside the weights has usually landed: asked
+            // for while the products issued last still run
+            if (!(ok = warp_wait(&kfull[2 + v], (g >> 1) & 1))) break;
+            if (more && !(ok = warp_wait(&kfull[nk], ((g + 1) >> 1) & 1))) break;
+            if (j >= a0 && j < b0) {
+                if (!(ok = pv(C0(), v, j > a0, np0++ & 1))) break;
+                if (j == b0 - 1) mma_commit_elected(&ofull[0]);
             }
-            const bool more = k.more(rng), last = j + 1 == k.nu;
-            if (!(ok = landed(2 + v, g))) break;
-            if (on0) {
-                if (!(ok = pv(W0(), 2 + v, was0 > 0, np0++ & 1))) break;
-                if (end0) mma_commit_elected(&ofull[0]);
-            }
+            const bool on1 = j >= a1 && j < b1, acc1 = j > a1, end1 = j == b1 - 1;
+            ++j;
             if (more) {
-                if (turn && !(ok = warp_wait(&qfull[0], pc & 1))) break;
-                if (!(ok = landed(nk, g + 1))) break;
-                if (j >= s0.a && j < s0.b) qk(W0(), nk);
-                if (last) mma_commit_elected(&qempty[0]);
+                if (turn) {
+                    j = 0;
+                    ++pc;
+                    if (!(ok = warp_wait(&qfull[0], pc & 1))) break;
+                    read_note();
+                }
+                if (j >= a0 && j < b0) qk(C0(), nk);
+                if (j + 1 == nu) mma_commit_elected(&qempty[0]);
             }
             if (on1) {
-                if (!(ok = pv(W1(), 2 + v, was1 > 0, np1++ & 1))) break;
+                if (!(ok = pv(C1(), v, acc1, np1++ & 1))) break;
                 if (end1) mma_commit_elected(&ofull[1]);
             }
             mma_commit_elected(&kempty[2 + v]);
             if (more) {
                 if (turn && !(ok = warp_wait(&qfull[1], pc & 1))) break;
-                if (j >= s1.a && j < s1.b) qk(W1(), nk);
-                if (last) mma_commit_elected(&qempty[1]);
+                if (j >= a1 && j < b1) qk(C1(), nk);
+                if (j + 1 == nu) mma_commit_elected(&qempty[1]);
                 mma_commit_elected(&kempty[nk]);
             }
             ++g;
@@ -616,13 +636,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                         pk[i / 2] = pack2<F16>(x.x, x.y);
                     }
                     tmem_st16(ts + c * 16, pk);
-                    if (c & 1) {  // half of the keys: the second product may begin
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&pfull[2 * w + c / 2]);
-                    }
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[w]);
                 s2[0] = add2(s2[0], s2[1]);
                 l += s2[0].x + s2[0].y;
             }
