@@ -15,7 +15,6 @@ which refuses a mismatch.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -368,7 +367,9 @@ class KVCache:
         if k.shape[3] > 1 and k.stride(3) != 1:
             raise ValueError("the last dimension must be contiguous")
         self.k, self.v = k, v
+        self.dtype, (_, self.heads, self.block_size, self.head_dim) = k.dtype, k.shape
         self._arg = _KVCacheArg(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], *k.shape, *k.stride()[:3])
+        self._ref = ctypes.byref(self._arg)
 
     @classmethod
     def empty(cls, blocks: int, heads: int, block_size: int, head_dim: int, dtype=torch.bfloat16,
@@ -377,22 +378,6 @@ class KVCache:
         device = device or torch.cuda.current_device()
         return cls(torch.empty(shape, dtype=dtype, device=device),
                    torch.empty(shape, dtype=dtype, device=device))
-
-    @property
-    def dtype(self):
-        return self.k.dtype
-
-    @property
-    def heads(self) -> int:
-        return self.k.shape[1]
-
-    @property
-    def block_size(self) -> int:
-        return self.k.shape[2]
-
-    @property
-    def head_dim(self) -> int:
-        return self.k.shape[3]
 
 
 @dataclass
@@ -407,45 +392,62 @@ class CachePlan:
     @classmethod
     def empty(cls, B: int, T: int, device=None) -> "CachePlan":
         device = device or torch.cuda.current_device()
+        parts = torch.empty(2 * B + 5 + T, dtype=torch.int32, device=device).split_with_sizes((B + 1, B, T, 4))
+        return cls(parts[0], parts[1], parts[2], torch.empty(T, dtype=torch.int64, device=device), parts[3])
 
-        def i32(n):
-            return torch.empty(n, dtype=torch.int32, device=device)
-        return cls(i32(B + 1), i32(B), i32(T), torch.empty(T, dtype=torch.int64, device=device), i32(4))
+
+# The checks below are a call's whole host cost beside the launch: a few tenths
+# of a microsecond each, where a decode step's kernels take several.
+def _raw_stream(stream, device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
 
 
 def _on(stream):
     """What a call allocates itself (outputs, a workspace) belongs to the
     stream it runs on, so that filling, use and reuse stay in order."""
-    if stream is None:
-        return contextlib.nullcontext()
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
 
 
-def _array(t: torch.Tensor, name: str, dtype, shape=None):
-    _cuda(t, name)
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, has {tuple(t.shape)}")
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _array(t: torch.Tensor, name: str, dtype, n: int | None = None) -> int:
+    """Address of a contiguous CUDA array of n elements."""
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and (n is None or t.numel() == n)):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor" +
+                         ("" if n is None else f" of {n} elements") + f", is {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _table(table: torch.Tensor, B: int):
-    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B:
+    """Address, row stride and width of a block table."""
+    if not (table.is_cuda and table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B):
         raise ValueError(f"table must be an int32 CUDA tensor of {B} rows")
-    if table.shape[1] > 1 and table.stride(1) != 1:
+    width = table.shape[1]
+    stride, one = table.stride()
+    if one != 1 and width > 1:
         raise ValueError("the table's rows must be contiguous")
     # the row stride of a single row is never used
-    return table.data_ptr(), max(table.stride(0), table.shape[1]) if B == 1 else table.stride(0), table.shape[1]
+    return table.data_ptr(), stride if B > 1 else max(stride, width), width
 
 
 def _rows(t: torch.Tensor, name: str, dtype):
-    """Token rows: 2-D or 3-D, contiguous but for the stride between rows."""
-    if not t.is_cuda or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
-    if t.dim() not in (2, 3) or t.shape[0] < 1 or not t[0].is_contiguous():
-        raise ValueError(f"{name} must be rows of contiguous elements")
-    n = t[0].numel()
-    return t.shape[0], n, max(t.stride(0), n) if t.shape[0] == 1 else t.stride(0)
+    """Token rows, 2-D or 3-D, contiguous but for the stride between rows:
+    their address, number, elements and stride."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        n = shape[1] * shape[2]
+        dense = (stride[2] == 1 or shape[2] == 1) and (stride[1] == shape[2] or shape[1] == 1)
+    else:
+        n = shape[-1] if len(shape) == 2 else 0
+        dense = len(shape) == 2 and (stride[1] == 1 or n == 1)
+    if not (dense and t.is_cuda and t.dtype == dtype and shape[0] >= 1):
+        raise ValueError(f"{name} must be {dtype} CUDA rows of contiguous elements, is {t.dtype} {tuple(shape)}")
+    return t.data_ptr(), shape[0], n, stride[0] if shape[0] > 1 else max(stride[0], n)
 
 
 def cache_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor,
@@ -456,24 +458,20 @@ def cache_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor,
     taken from the end of ``free_blocks`` int32, of which the first
     ``free_count`` (int32 [1]) are free.  T token rows."""
     B = cached.numel()
-    _array(cached, "cached", torch.int32)
-    _array(fresh, "fresh", torch.int32, tuple(cached.shape))
-    _array(free_blocks, "free_blocks", torch.int32)
-    _array(free_count, "free_count", torch.int32)
-    if free_count.numel() < 1:
-        raise ValueError("free_count must hold one number")
     tp, ts, width = _table(table, B)
     if out is None:
-        with _on(stream):
+        if stream is None:
             out = CachePlan.empty(B, T, cached.device)
-    for t, n, d, k in ((out.q_start, "q_start", torch.int32, B + 1), (out.kv_len, "kv_len", torch.int32, B),
-                       (out.position, "position", torch.int32, T), (out.slot, "slot", torch.int64, T),
-                       (out.counts, "counts", torch.int32, 4)):
-        _array(t, n, d, (k,))
-    _ok(_lib.q4_cache_plan(cached.data_ptr(), fresh.data_ptr(), B, block_size, tp, ts, width,
-                           free_blocks.data_ptr(), free_count.data_ptr(), free_blocks.numel(), T,
-                           out.q_start.data_ptr(), out.kv_len.data_ptr(), out.position.data_ptr(),
-                           out.slot.data_ptr(), out.counts.data_ptr(), _stream(stream)), "q4_cache_plan")
+        else:
+            with _on(stream):
+                out = CachePlan.empty(B, T, cached.device)
+    i32 = torch.int32
+    _ok(_lib.q4_cache_plan(_array(cached, "cached", i32), _array(fresh, "fresh", i32, B), B, block_size, tp, ts,
+                           width, _array(free_blocks, "free_blocks", i32), _array(free_count, "free_count", i32, 1),
+                           free_blocks.numel(), T, _array(out.q_start, "q_start", i32, B + 1),
+                           _array(out.kv_len, "kv_len", i32, B), _array(out.position, "position", i32, T),
+                           _array(out.slot, "slot", torch.int64, T), _array(out.counts, "counts", i32, 4),
+                           _raw_stream(stream, cached.device)), "q4_cache_plan")
     return out
 
 
@@ -507,22 +505,18 @@ def rope_append(qkv: torch.Tensor, cache: KVCache, position: torch.Tensor, slot:
     head_dim] and append keys and values to the cache (q4_rope_append).
     2 * len(freq) elements of each head turn.  Returns the queries
     [T][heads][head_dim] (``out`` may be the query part of qkv itself)."""
-    T, n, stride = _rows(qkv, "qkv", cache.dtype)
+    qp, T, n, stride = _rows(qkv, "qkv", cache.dtype)
     if n != (heads + 2 * cache.heads) * cache.head_dim:
         raise ValueError(f"qkv rows have {n} elements, not (heads + 2 * cache heads) * head_dim")
-    _array(position, "position", torch.int32, (T,))
-    _array(slot, "slot", torch.int64, (T,))
-    _array(freq, "freq", torch.float64)
     if out is None:
-        with _on(stream):
-            out = torch.empty((T, heads, cache.head_dim), dtype=qkv.dtype, device=qkv.device)
-    To, no, ostride = _rows(out, "out", cache.dtype)
+        out = _empty((T, heads, cache.head_dim), cache.dtype, qkv.device, stream)
+    op, To, no, ostride = _rows(out, "out", cache.dtype)
     if To != T or no != heads * cache.head_dim:
         raise ValueError("out must be T rows of heads * head_dim")
-    _ok(_lib.q4_rope_append(qkv.data_ptr(), stride, T, heads, 2 * freq.numel(),
-                            ROPE_INTERLEAVED if interleaved else ROPE_HALF, freq.data_ptr(), factor,
-                            position.data_ptr(), slot.data_ptr(), out.data_ptr(), ostride,
-                            ctypes.byref(cache._arg), _stream(stream)), "q4_rope_append")
+    _ok(_lib.q4_rope_append(qp, stride, T, heads, 2 * freq.numel(), ROPE_INTERLEAVED if interleaved else ROPE_HALF,
+                            _array(freq, "freq", torch.float64), factor, _array(position, "position", torch.int32, T),
+                            _array(slot, "slot", torch.int64, T), op, ostride, cache._ref,
+                            _raw_stream(stream, qkv.device)), "q4_rope_append")
     return out
 
 
@@ -548,33 +542,29 @@ def attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: tor
     ``window`` > 0: each token sees that many keys, itself included.  Returns
     o [T][heads][head_dim] (q's type, or float32), with ``return_lse`` also the
     f32 log-sum-exp [T][heads]."""
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError(f"q must be [T][heads][{cache.head_dim}]")
-    T, n, stride = _rows(q, "q", cache.dtype)
+    qp, T, n, stride = _rows(q, "q", cache.dtype)
+    D = cache.head_dim
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q must be [T][heads][{D}]")
     heads = q.shape[1]
     B = kv_len.numel()
-    _array(kv_len, "kv_len", torch.int32, (B,))
-    _array(q_start, "q_start", torch.int32, (B + 1,))
     tp, ts, width = _table(table, B)
-    with _on(stream):
-        if out is None:
-            out = torch.empty((T, heads, cache.head_dim), dtype=out_dtype or q.dtype, device=q.device)
-        if return_lse and lse is None:
-            lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
-        if ws is None:
-            ws = attention_workspace(max_fresh, heads, cache.heads, cache.head_dim, q.device)
-    To, no, ostride = _rows(out, "out", out.dtype)
+    if out is None:
+        out = _empty((T, heads, D), out_dtype or cache.dtype, q.device, stream)
+    op, To, no, ostride = _rows(out, "out", out.dtype)
     if To != T or no != n:
         raise ValueError("out must be T rows of heads * head_dim")
-    if lse is not None:
-        _array(lse, "lse", torch.float32, (T, heads))
-    wsp, wsb = _ws(ws)
-    _ok(_call(q.data_ptr(), stride, T, heads, ctypes.byref(cache._arg), tp, ts, width,
-                          q_start.data_ptr(), kv_len.data_ptr(), B, max_fresh,
-                          cache.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
-                          _DTYPE.get(out.dtype, -1), ostride, 0 if lse is None else lse.data_ptr(),
-                          wsp, wsb, _stream(stream)), "q4_attention")
-    return (out, lse) if return_lse or lse is not None else out
+    if return_lse and lse is None:
+        lse = _empty((T, heads), torch.float32, q.device, stream)
+    if ws is None:
+        with _on(stream if stream is not None else torch.cuda.current_stream()):
+            ws = attention_workspace(max_fresh, heads, cache.heads, D, q.device)
+    _ok(_call(qp, stride, T, heads, cache._ref, tp, ts, width, _array(q_start, "q_start", torch.int32, B + 1),
+              _array(kv_len, "kv_len", torch.int32, B), B, max_fresh, D ** -0.5 if scale is None else scale, window,
+              op, _DTYPE.get(out.dtype, -1), ostride,
+              0 if lse is None else _array(lse, "lse", torch.float32, T * heads),
+              *_ws(ws), _raw_stream(stream, q.device)), "q4_attention")
+    return (out, lse) if lse is not None else out
 
 
 def attention_timeout_selftest(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: torch.Tensor,

@@ -9,18 +9,17 @@
 //
 // Work.  (request, row tile, KV head) are the items, a unit is 16 keys of
 // one item.  All units of the call form one sequence, request-major, cut into
-// equal contiguous ranges, one per CTA (one CTA per SM): every SM streams the
-// same number of bytes whatever the lengths.  A CTA finds its range from the
-// lengths on the device (locate()), so no host plan and no second launch is
-// needed.  Within a piece of an item the CTA's 8 warps take its units in
-// turn; each warp has its own ring of STAGES units in shared memory filled by
-// cp.async (16 bytes per lane; keys past the request's end, blocks outside
+// equal contiguous ranges, one per warp (8 warps per SM): every warp streams
+// the same number of bytes whatever the lengths, finds its range from the
+// lengths on the device (no host plan, no second launch), and shares nothing
+// with its neighbours, so that one that finishes an item does not hold up the
+// others' loads.  Each warp has a ring of STAGES units in shared memory filled
+// by cp.async (16 bytes per lane; keys past the request's end, blocks outside
 // the cache and the padding of head_dim are filled with zeros, so nothing
-// stale is ever multiplied), its own running maximum, sum and f32
-// accumulator, and no barrier with the others until the piece ends, where the
-// warps' results meet in shared memory.  An item cut by a range boundary
-// leaves its pieces in the workspace; the last CTA to arrive adds them in CTA
-// order, so results do not depend on timing.
+// stale is ever multiplied); the loads run ahead through the ends of items.
+// An item cut by a range boundary leaves its pieces in the workspace, in the
+// lanes' own order; the last warp to arrive adds them in sequence order, so
+// results do not depend on timing.
 #include "serve.cuh"
 #include "attention.cuh"
 
@@ -32,15 +31,16 @@ constexpr int TK = 16;       // keys per unit
 constexpr int NW = 8;        // warps
 constexpr int STAGES = 3;    // units in flight per warp
 constexpr int THREADS = NW * 32;
+// Places that an item takes beside its units (its beginning and end), and the
+// least that a warp gets.
+constexpr int PAD = 1, MIN_UNITS = 2;
 
 template <int DP>
 struct Sizes {
     static constexpr int ROW = DP * 2;             // bytes of a key
     static constexpr int TILE = TK * ROW;          // bytes of a unit's keys
-    static constexpr int RING = NW * STAGES * 2 * TILE;
-    static constexpr int MERGE = NW * R * (DP + 2) * 4;  // aliases the ring
-    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
-    static constexpr int SLOT = R * (DP + 2);      // floats of a partial result
+    static constexpr int SMEM = NW * STAGES * 2 * TILE;
+    static constexpr int SLOT = R * (DP + 8);      // floats of a partial result: sums, (reference, sum) per lane and row
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
@@ -94,66 +94,76 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
     constexpr int LPT = TK * CH / 32;                      // 16-byte loads per lane per operand
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LocateScratch ls;
-    __shared__ int last_s;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     grid_dep_launch_dependents();
     grid_dep_wait();
-    const Range rng = cta_range<R, TK, NW, 1, 0>(a, ls);
+    sum_slabs<R, TK, NW, PAD>(a, ls);
+    // neighbours in the sequence on different SMs: few units use many SMs
+    const int me = warp * gridDim.x + blockIdx.x;
+    const Range rng = find_share<R, TK, NW, MIN_UNITS, PAD>(a, ls, me, NW * gridDim.x);
     if (rng.u0 >= rng.u1) return;
 
+    using Pieces = Walk<R, TK, PAD>;
+    Pieces k(a, rng), ld = k;  // being summed; being loaded
     const uint32_t ring = smem_u32(smem) + warp * (STAGES * 2 * Z::TILE);
-    Item it = rng.first;
-    int64_t u = rng.u0;
-    int kt = rng.kt;  // first unit of the piece within the item
-    while (u < rng.u1) {
-        const Span<R, TK> sp(a, it.b, it.rt);
-        const int nu = static_cast<int>(min(static_cast<int64_t>(sp.units - kt), rng.u1 - u));
-
-        // ---- this warp's units of the piece: kt + warp, kt + warp + NW, ...
-        const int mine = nu > warp ? (nu - warp + NW - 1) / NW : 0;
-        const uint16_t *kbase = a.k + it.head * a.head_stride, *vbase = a.v + it.head * a.head_stride;
-        const int *trow = a.table + it.b * a.table_stride;
-        auto block_of = [&](int i) {  // table entry of this warp's i-th unit
-            const int key = (sp.kt0 + kt + warp + i * NW) * TK;
-            return i < mine && key < sp.kv ? __ldg(trow + a.by_S.div(key)) : -1;
-        };
-        int next_block = block_of(0);
-        auto issue = [&](int i) {
-            if (i < mine) {
-                const int blk = next_block;
-                const int key = (sp.kt0 + kt + warp + i * NW) * TK;
-                const bool in = static_cast<unsigned>(blk) < static_cast<unsigned>(a.blocks);
-                const int64_t off = in ? blk * a.block_stride + (key - a.by_S.div(key) * a.S) * a.token_stride : 0;
-                const uint32_t dst = ring + (i % STAGES) * 2 * Z::TILE;
+    int ld_i = 0, ld_slot = 0;  // unit of ld, ring slot
+    auto block_of = [&]() {  // table entry of the unit to load
+        const int key = (ld.kt0 + ld.kt + ld_i) * TK;
+        return ld.more(rng) && key < ld.kv ? __ldg(a.table + ld.it.b * a.table_stride + a.by_S.div(key)) : -1;
+    };
+    int blk = block_of();
+    auto issue = [&]() {
+        if (ld.more(rng)) {
+            const int key = (ld.kt0 + ld.kt + ld_i) * TK;
+            const bool in = static_cast<unsigned>(blk) < static_cast<unsigned>(a.blocks);
+            const uint32_t dst = ring + ld_slot * 2 * Z::TILE;
+            // lane: 16-byte piece c of rows hi, hi + RPI, ..
+            constexpr int RPI = 32 / CH;
+            const int c = lane % CH, hi = lane / CH;
+            int64_t at = in ? blk * a.block_stride + (key - a.by_S.div(key) * a.S + hi) * a.token_stride +
+                                  ld.it.head * a.head_stride + c * 8
+                            : 0;
+            const int rows = in && c * 8 < a.D ? ld.kv - key : 0;  // keys that exist
 #pragma unroll
-                for (int l = 0; l < LPT; ++l) {
-                    const int e = l * 32 + lane, row = e / CH, c = e % CH;
-                    const bool ok = in && key + row < sp.kv && c * 8 < a.D;
-                    const int64_t at = ok ? off + row * a.token_stride + c * 8 : 0;
-                    const uint32_t d = dst + row * Z::ROW + ((c ^ (row & 7)) << 4);
-                    cp_async16(d, kbase + at, ok);
-                    cp_async16(d + Z::TILE, vbase + at, ok);
-                }
-                next_block = block_of(i + 1);
+            for (int l = 0; l < LPT; ++l) {
+                const int row = l * RPI + hi;
+                const bool ok = row < rows;
+                const uint32_t d = dst + row * Z::ROW + ((c ^ (row & 7)) << 4);
+                cp_async16(d, a.k + (ok ? at : 0), ok);
+                cp_async16(d + Z::TILE, a.v + (ok ? at : 0), ok);
+                at += RPI * a.token_stride;
             }
-            cp_async_commit();
-        };
+            ld_slot = ld_slot + 1 == STAGES ? 0 : ld_slot + 1;
+            if (++ld_i == ld.nu) {
+                ld.next(a, rng);
+                ld_i = 0;
+            }
+            blk = block_of();
+        }
+        cp_async_commit();
+    };
 #pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) issue(i);
+    for (int i = 0; i < STAGES - 1; ++i) issue();
 
+    int slot = 0;
+    for (; k.more(rng); k.next(a, rng)) {
         // ---- queries as A fragments: rows lane / 4 and + 8
         uint32_t qf[KS][4];
         const uint16_t *qrow[2];
         int place[2];  // the row's place in its request (its last visible key)
+        int64_t trow[2];
+        int hrow[2];
+        const bool two = k.row1 - k.row0 > 8;  // rows 8..15 are there
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int r = sp.row0 + lane / 4 + 8 * j;
-            const bool in = r < sp.row1;
+            const int r = k.row0 + lane / 4 + 8 * j;
+            const bool in = r < k.row1;
             const int t = in ? a.by_GQ.div(r) : 0, g = in ? r - t * a.GQ : 0;
-            place[j] = in ? sp.base + t : -1;
-            qrow[j] = in ? a.q + (sp.t0 + t) * a.q_stride + static_cast<int64_t>(it.head * a.GQ + g) * a.D
-                         : nullptr;
+            place[j] = in ? k.base + t : -1;
+            trow[j] = in ? k.t0 + t : -1;
+            hrow[j] = k.it.head * a.GQ + g;
+            qrow[j] = in ? a.q + trow[j] * a.q_stride + static_cast<int64_t>(hrow[j]) * a.D : nullptr;
         }
 #pragma unroll
         for (int s = 0; s < KS; ++s)
@@ -167,11 +177,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
 #pragma unroll
         for (int i = 0; i < NO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
-        for (int i = 0; i < mine; ++i) {
+        for (int i = 0; i < k.nu; ++i) {
             cp_async_wait<STAGES - 2>();
             __syncwarp();  // the other lanes' copies too; and all lanes are done with the slot below
-            issue(i + STAGES - 1);
-            const uint32_t ks = ring + (i % STAGES) * 2 * Z::TILE, vs = ks + Z::TILE;
+            issue();
+            const uint32_t ks = ring + slot * 2 * Z::TILE, vs = ks + Z::TILE;
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
             float sc[2][4];
 #pragma unroll
             for (int n = 0; n < 2; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
@@ -185,7 +196,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
                 mma16816<F16>(sc[1], qf[s], b[2], b[3]);
             }
             // ---- mask and softmax in units of log 2
-            const int key0 = (sp.kt0 + kt + warp + i * NW) * TK + (lane & 3) * 2;
+            const int key0 = (k.kt0 + k.kt + i) * TK + (lane & 3) * 2;
             uint32_t p[4];
             float f[2];
 #pragma unroll
@@ -230,97 +241,88 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
                 mma16816<F16>(o[n + 1], p, b[2], b[3]);
             }
         }
-        cp_async_wait<0>();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
             l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
         }
 
-        // ---- the warps' results meet: [warp][row][DP + 2]
-        __syncthreads();  // every warp is done with the rings
-        float *mg = reinterpret_cast<float *>(smem);
+        bool store = k.whole();
+        if (!store) {
+            int w0, w1;
+            k.holders(rng, w0, w1);
+            // [dim pair][row half][lane], then (reference, sum) [row half][lane]
+            auto part = [&](int w) {
+                return reinterpret_cast<float2 *>(a.part + (2 * static_cast<int64_t>(w) + (w == w0)) * Z::SLOT) + lane;
+            };
+            float2 *ps = part(me);
+            if (store_ok(reinterpret_cast<float *>(ps - lane) + Z::SLOT - 1 - a.part, a.part_len, a.err)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float *w = mg + (warp * R + lane / 4 + 8 * j) * (DP + 2);
+                for (int j = 0; j < 2; ++j) {
+                    if (j == 1 && !two) break;
 #pragma unroll
-            for (int n = 0; n < NO; ++n)
-                *reinterpret_cast<float2 *>(w + n * 8 + (lane & 3) * 2) = make_float2(o[n][2 * j], o[n][2 * j + 1]);
-            if ((lane & 3) == 0) {
-                w[DP] = m[j];
-                w[DP + 1] = l[j];
+                    for (int n = 0; n < NO; ++n) ps[(n * 2 + j) * 32] = make_float2(o[n][2 * j], o[n][2 * j + 1]);
+                    ps[(NO * 2 + j) * 32] = make_float2(m[j], l[j]);
+                }
             }
-        }
-        __syncthreads();
-        const bool whole = kt == 0 && nu == sp.units;
-        const int rows = sp.row1 - sp.row0;
-        // a thread takes 4 dims of a row; warps without a unit hold nothing
-        const bool use[NW] = {nu > 0, nu > 1, nu > 2, nu > 3, nu > 4, nu > 5, nu > 6, nu > 7};
-        for (int e = tid; e < rows * (DP / 4); e += THREADS) {
-            const int r = e / (DP / 4), d = e % (DP / 4) * 4;
-            float top = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < NW; ++w)
-                if (use[w]) top = fmaxf(top, mg[(w * R + r) * (DP + 2) + DP]);
-            const float ref = top == -INFINITY ? 0.0f : top;
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                if (!use[w]) continue;
-                const float *x = mg + (w * R + r) * (DP + 2);
-                const float g = ex2(x[DP] - ref);
-                sum += g * x[DP + 1];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[c] += g * x[d + c];
+            __threadfence();
+            __syncwarp();
+            int last = 0;
+            if (lane == 0) {
+                last = store_ok(w0, a.count_len, a.err) &&
+                       atomic_add_acq_rel_gpu(a.count + w0, 1u) == static_cast<unsigned>(w1 - w0);
+                if (last) a.count[w0] = 0u;
             }
-            if (whole) {
-                finish_row<F16>(a, it, sp.t0, sp.row0 + r, d, acc, top, sum);
-            } else {
-                float *ps = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (kt == 0)) * Z::SLOT + r * (DP + 2);
-                if (store_ok(ps + DP + 1 - a.part, a.part_len, a.err)) {
+            store = __shfl_sync(0xffffffffu, last, 0) != 0;
+            if (store) {
+                m[0] = m[1] = -INFINITY;
+                l[0] = l[1] = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) ps[d + c] = acc[c];
-                    if (d == 0) {
-                        ps[DP] = top;
-                        ps[DP + 1] = sum;
+                for (int i = 0; i < NO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+                for (int w = w0; w <= w1; ++w) {
+                    const float2 *x = part(w);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (j == 1 && !two) break;
+                        float2 y[NO];
+#pragma unroll
+                        for (int n = 0; n < NO; ++n) y[n] = __ldcg(x + (n * 2 + j) * 32);
+                        const float2 ml = __ldcg(x + (NO * 2 + j) * 32);
+                        const float mn = fmaxf(m[j], ml.x), ref = mn == -INFINITY ? 0.0f : mn;
+                        const float g0 = ex2(m[j] - ref), g1 = ex2(ml.x - ref);
+                        m[j] = mn;
+                        l[j] = l[j] * g0 + ml.y * g1;
+#pragma unroll
+                        for (int n = 0; n < NO; ++n) {
+                            o[n][2 * j] = o[n][2 * j] * g0 + y[n].x * g1;
+                            o[n][2 * j + 1] = o[n][2 * j + 1] * g0 + y[n].y * g1;
+                        }
                     }
                 }
             }
         }
-        if (!whole) {
-            // CTAs holding pieces of this item, in order
-            const int64_t i0 = u - kt, i1 = i0 + sp.units;
-            const int c0 = owner_of(i0, rng.total, rng.G), c1 = owner_of(i1 - 1, rng.total, rng.G);
-            __syncthreads();
-            if (tid == 0) {
-                last_s = store_ok(c0, a.count_len, a.err) &&
-                         atomic_add_acq_rel_gpu(a.count + c0, 1u) == static_cast<unsigned>(c1 - c0);
-                if (last_s) a.count[c0] = 0u;
-            }
-            __syncthreads();
-            if (last_s) {
-                for (int e = tid; e < rows * (DP / 4); e += THREADS) {
-                    const int r = e / (DP / 4), d = e % (DP / 4) * 4;
-                    float top = -INFINITY, sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (int c = c0; c <= c1; ++c) {
-                        const float *x = a.part + (2 * static_cast<int64_t>(c) + (c == c0)) * Z::SLOT + r * (DP + 2);
-                        const float mx = __ldcg(x + DP), ls2 = __ldcg(x + DP + 1);
-                        const float mn = fmaxf(top, mx), ref = mn == -INFINITY ? 0.0f : mn;
-                        const float g0 = ex2(top - ref), g1 = ex2(mx - ref);
-                        top = mn;
-                        sum = sum * g0 + ls2 * g1;
+        if (store) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) acc[k] = acc[k] * g0 + __ldcg(x + d + k) * g1;
-                    }
-                    finish_row<F16>(a, it, sp.t0, sp.row0 + r, d, acc, top, sum);
+            for (int j = 0; j < 2; ++j) {
+                if (trow[j] < 0) continue;
+                const float inv = inverse(l[j]);
+                const int64_t at = trow[j] * a.o_stride + static_cast<int64_t>(hrow[j]) * a.D + (lane & 3) * 2;
+                const int64_t o_len = static_cast<int64_t>(a.T - 1) * a.o_stride + static_cast<int64_t>(a.Hq) * a.D;
+#pragma unroll
+                for (int n = 0; n < NO; ++n) {
+                    if (n * 8 >= a.D || !store_ok(at + n * 8 + 1, o_len, a.err)) break;
+                    const float x = o[n][2 * j] * inv, y = o[n][2 * j + 1] * inv;
+                    if (a.ot == Q4_F32)
+                        *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + at + n * 8) = make_float2(x, y);
+                    else
+                        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.o) + at + n * 8) = pack2<F16>(x, y);
                 }
+                if ((lane & 3) == 0) store_lse(a, trow[j], hrow[j], m[j], l[j]);
             }
         }
-        __syncthreads();  // the merge buffer becomes the rings again
-        u += nu;
-        kt = 0;
-        it.next(a, R);
+        __syncwarp();
     }
+    cp_async_wait<0>();
 }
 
 template <bool F16, int DP>
@@ -338,10 +340,10 @@ cudaError_t launch(const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 AttnPlan attention_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count)
 {
     AttnPlan p{};
-    p.grid = std::min<int>(sm_count, ATTN_COUNTER_BYTES / sizeof(unsigned int) / 2);
+    p.grid = std::min<int>(sm_count, ATTN_COUNTER_BYTES / sizeof(unsigned int) / NW);
     p.tc = max_fresh > R / GQ;
-    const size_t slot = R * ((D > 64 ? 128 : 64) + 2) * sizeof(float);
-    const size_t part = p.tc ? attention_tc_part_bytes(D, p.grid) : 2 * static_cast<size_t>(p.grid) * slot;
+    const size_t slot = (D > 64 ? Sizes<128>::SLOT : Sizes<64>::SLOT) * sizeof(float);
+    const size_t part = p.tc ? attention_tc_part_bytes(D, p.grid) : 2 * static_cast<size_t>(p.grid) * NW * slot;
     p.workspace = ATTN_COUNTER_BYTES + part;
     return p;
 }

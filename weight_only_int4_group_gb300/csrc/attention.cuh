@@ -1,5 +1,6 @@
-// attention.cuh -- what the two attention kernels share: the sequence of
-// work units and how a CTA finds its range of it, and the final store.
+// attention.cuh -- what the two attention kernels share: the sequence of work
+// units, how a worker (a CTA or a warp) finds and walks its range of it, and
+// the final store.
 #pragma once
 
 #include "serve.cuh"
@@ -76,8 +77,8 @@ struct Item {
 };
 
 struct Range {
-    int64_t u0, u1, total;  // the CTA's places and all places of the call's sequence
-    int G;                  // CTAs that share them
+    int64_t u0, u1, total;  // the worker's places and all places of the call's sequence
+    int G;                  // workers that share them
     Item first;             // item of place u0
     int kt;                 // u0 within that item
 };
@@ -87,7 +88,7 @@ struct LocateScratch {
     Range r;
 };
 
-// CTA holding unit i of T units cut into G equal ranges [c * T / G, (c + 1) * T / G).
+// Worker holding place i of T cut into G equal ranges [c * T / G, (c + 1) * T / G).
 __device__ __forceinline__ int owner_of(int64_t i, int64_t T, int64_t G)
 {
     return static_cast<int>(((i + 1) * G - 1) / T);
@@ -121,12 +122,9 @@ __device__ __forceinline__ int64_t request_units(const AttnArgs &a, int b, bool 
     return sum;
 }
 
-// The CTA's equal share of the call's sequence, and where it begins.  Every
-// thread of the CTA calls it (NW warps; two barriers); all get the result.
-// Warps sum slabs of requests, then the warp whose slab holds the CTA's first
-// unit walks it again.
-template <int R, int TK, int NW, int MIN_UNITS, int PAD>
-__device__ Range cta_range(const AttnArgs &a, LocateScratch &ls)
+// Sums of slabs of requests, one per warp; a barrier.
+template <int R, int TK, int NW, int PAD>
+__device__ __forceinline__ void sum_slabs(const AttnArgs &a, LocateScratch &ls)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b0 = static_cast<int>(static_cast<int64_t>(a.B) * warp / NW),
@@ -137,74 +135,164 @@ __device__ Range cta_range(const AttnArgs &a, LocateScratch &ls)
     for (int d = 16; d; d >>= 1) slab += __shfl_xor_sync(0xffffffffu, slab, d);
     if (lane == 0) ls.slab[warp] = slab;
     __syncthreads();
-    int64_t before = 0, all = 0;
+}
+
+__device__ __forceinline__ int64_t inclusive_sum(int64_t v)
+{
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += ls.slab[w];
-        all += ls.slab[w];
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t p = __shfl_up_sync(0xffffffffu, v, d);
+        if (static_cast<int>(threadIdx.x & 31) >= d) v += p;
     }
-    const int64_t total = all * a.Hkv;
-    // as many CTAs as get MIN_UNITS units each; none between two others is
-    // left without a unit (the pieces of an item are counted by their CTAs)
-    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + MIN_UNITS - 1) / MIN_UNITS));
-    const bool mine_any = static_cast<int>(blockIdx.x) < G;
-    const int64_t u0 = mine_any ? blockIdx.x * total / G : 0, u1 = mine_any ? (blockIdx.x + 1) * total / G : 0;
-    int64_t left = u0 - before * a.Hkv;  // units to pass from the slab's start
-    if (u0 < u1 && left >= 0 && left < slab * a.Hkv) {
-        for (int b = b0; b < b1; b += 32) {
-            const int64_t mine = request_units<R, TK, PAD>(a, b + lane, b + lane < b1) * a.Hkv;
-            int64_t incl = mine;
+    return v;
+}
+
+// Equal share `worker` of the sequence among as many of `workers` as get
+// MIN_UNITS places each (none between two others is left without one: the
+// pieces of an item are counted by their workers), and the item it begins in.
+// Called by a whole warp after sum_slabs.
+template <int R, int TK, int NW, int MIN_UNITS, int PAD>
+__device__ Range find_share(const AttnArgs &a, const LocateScratch &ls, int worker, int workers)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t all = 0;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t p = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += p;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, incl > left);
-            if (!past) {
-                left -= __shfl_sync(0xffffffffu, incl, 31);
+    for (int w = 0; w < NW; ++w) all += ls.slab[w];
+    Range r = {};
+    r.total = all * a.Hkv;
+    r.G = static_cast<int>(min(static_cast<int64_t>(workers), (r.total + MIN_UNITS - 1) / MIN_UNITS));
+    if (worker >= r.G) return r;
+    r.u0 = worker * r.total / r.G;
+    r.u1 = (worker + 1) * r.total / r.G;
+    if (r.u0 >= r.u1) return r;
+    // the slab, then the request, then the row tile that holds place u0
+    int64_t left = r.u0;
+    int slab = 0;
+    while (left >= ls.slab[slab] * a.Hkv) left -= ls.slab[slab++] * a.Hkv;
+    const int b0 = static_cast<int>(static_cast<int64_t>(a.B) * slab / NW),
+              b1 = static_cast<int>(static_cast<int64_t>(a.B) * (slab + 1) / NW);
+    for (int b = b0; b < b1; b += 32) {
+        const int64_t mine = request_units<R, TK, PAD>(a, b + lane, b + lane < b1) * a.Hkv;
+        const int64_t incl = inclusive_sum(mine);
+        const unsigned past = __ballot_sync(0xffffffffu, incl > left);
+        if (!past) {
+            left -= __shfl_sync(0xffffffffu, incl, 31);
+            continue;
+        }
+        const int src = __ffs(past) - 1;
+        left -= __shfl_sync(0xffffffffu, incl - mine, src);
+        int t0, n, kv;
+        request(a, b + src, t0, n, kv);
+        const int nt = row_tiles(n, a.GQ, R);
+        for (int rt = 0; rt < nt; rt += 32) {
+            const int per = rt + lane < nt ? Span<R, TK>(a, n, kv, rt + lane).units + PAD : 0;
+            const int64_t m2 = static_cast<int64_t>(per) * a.Hkv, in2 = inclusive_sum(m2);
+            const unsigned past2 = __ballot_sync(0xffffffffu, in2 > left);
+            if (!past2) {
+                left -= __shfl_sync(0xffffffffu, in2, 31);
                 continue;
             }
-            const int src = __ffs(past) - 1;
-            left -= __shfl_sync(0xffffffffu, incl - mine, src);
-            // within the request: row tiles, 32 at a time
-            int t0, n, kv;
-            request(a, b + src, t0, n, kv);
-            const int nt = row_tiles(n, a.GQ, R);
-            for (int rt = 0; rt < nt; rt += 32) {
-                const int64_t m2 = rt + lane < nt ? static_cast<int64_t>(Span<R, TK>(a, n, kv, rt + lane).units + PAD) * a.Hkv : 0;
-                int64_t in2 = m2;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int64_t p = __shfl_up_sync(0xffffffffu, in2, d);
-                    if (lane >= d) in2 += p;
-                }
-                const unsigned past2 = __ballot_sync(0xffffffffu, in2 > left);
-                if (!past2) {
-                    left -= __shfl_sync(0xffffffffu, in2, 31);
-                    continue;
-                }
-                const int s2 = __ffs(past2) - 1;
-                left -= __shfl_sync(0xffffffffu, in2 - m2, s2);
-                if (lane == 0) {
-                    const int64_t per = Span<R, TK>(a, n, kv, rt + s2).units + PAD;
-                    ls.r.first.b = b + src;
-                    ls.r.first.rt = rt + s2;
-                    ls.r.first.head = static_cast<int>(left / per);
-                    ls.r.kt = static_cast<int>(left % per);
-                }
-                break;
-            }
+            const int s2 = __ffs(past2) - 1;
+            left -= __shfl_sync(0xffffffffu, in2 - m2, s2);
+            const int pl = __shfl_sync(0xffffffffu, per, s2);
+            r.first.b = b + src;
+            r.first.rt = rt + s2;
+            r.first.head = static_cast<int>(left / pl);
+            r.kt = static_cast<int>(left % pl);
             break;
         }
+        break;
     }
-    __syncthreads();
-    Range r = ls.r;
-    r.u0 = u0;
-    r.u1 = u1;
-    r.total = total;
-    r.G = G;
     return r;
 }
+
+// The share of one worker per CTA, by one warp for all; barriers.
+template <int R, int TK, int NW, int MIN_UNITS, int PAD>
+__device__ Range share(const AttnArgs &a, LocateScratch &ls, int worker, int workers)
+{
+    sum_slabs<R, TK, NW, PAD>(a, ls);
+    if (threadIdx.x < 32) {
+        const Range r = find_share<R, TK, NW, MIN_UNITS, PAD>(a, ls, worker, workers);
+        if (threadIdx.x == 0) ls.r = r;
+    }
+    __syncthreads();
+    return ls.r;
+}
+
+// A worker's pieces of items.
+template <int R, int TK, int PAD>
+struct Walk {
+    Item it;
+    int64_t v0, vu;    // the item's and the piece's place in the call's sequence
+    int vn;            // and its length there
+    int kt, nu;        // units [kt, kt + nu) of the item
+    int units, kt0;    // the item's units, the first one's index among the request's keys
+    int row0, row1, t0, base, kv;
+    bool same;         // all but the head as in the piece before
+    __device__ __forceinline__ Walk(const AttnArgs &a, const Range &r) : it(r.first), same(false)
+    {
+        vu = r.u0;
+        if (vu >= r.u1) return;
+        load(a, r);
+        cut(r, r.kt);
+        while (nu <= 0 && vu < r.u1) step(a, r);
+    }
+    __device__ __forceinline__ bool more(const Range &r) const { return vu < r.u1; }
+    // Another piece follows (one that would be padding alone does not count).
+    __device__ __forceinline__ bool follows(const Range &r) const { return r.u1 - (vu + vn) > PAD; }
+    // The next piece that holds a unit.
+    __device__ __forceinline__ void next(const AttnArgs &a, const Range &r)
+    {
+        do step(a, r);
+        while (nu <= 0 && vu < r.u1);
+    }
+    __device__ __forceinline__ bool whole() const { return kt == 0 && nu == units; }
+
+private:
+    __device__ __forceinline__ void load(const AttnArgs &a, const Range &r)
+    {
+        const Span<R, TK> sp(a, it.b, it.rt);
+        units = sp.units;
+        kt0 = sp.kt0;
+        row0 = sp.row0;
+        row1 = sp.row1;
+        t0 = sp.t0;
+        base = sp.base;
+        kv = sp.kv;
+    }
+    // The piece of the item from its place v on: the first PAD places of an
+    // item hold no unit.
+    __device__ __forceinline__ void cut(const Range &r, int v)
+    {
+        v0 = vu - v;
+        vn = static_cast<int>(min(static_cast<int64_t>(units + PAD - v), r.u1 - vu));
+        kt = max(v - PAD, 0);
+        nu = max(v + vn - PAD, 0) - kt;
+    }
+    __device__ __forceinline__ void step(const AttnArgs &a, const Range &r)
+    {
+        const bool was_whole = whole();
+        vu += vn;
+        same = false;
+        if (vu >= r.u1) return;
+        if (++it.head < a.Hkv) {  // the same rows and keys of the next head
+            cut(r, 0);
+            same = was_whole && nu == units;
+            return;
+        }
+        it.next_rows(a, R);
+        load(a, r);
+        cut(r, 0);
+    }
+
+public:
+    // First and last worker that hold units of the item.
+    __device__ __forceinline__ void holders(const Range &r, int &first, int &last) const
+    {
+        first = owner_of(v0 + PAD, r.total, r.G);
+        last = owner_of(v0 + PAD + units - 1, r.total, r.G);
+    }
+};
 
 // 2^x to about 2 ulp; 0 below the normal range.
 __device__ __forceinline__ float ex2(float x)
@@ -264,20 +352,6 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int64_t t, int h, f
     const int64_t l = t * a.Hq + h;
     if (a.lse && store_ok(l, static_cast<int64_t>(a.T) * a.Hq, a.err))
         a.lse[l] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-}
-
-// Dims d..d + 3 of one row of an item, from its accumulated sum.
-template <bool F16>
-__device__ __forceinline__ void finish_row(const AttnArgs &a, const Item &it, int t0, int row, int d,
-                                           const float (&acc)[4], float top, float sum)
-{
-    const int i = a.by_GQ.div(row);
-    const int64_t t = t0 + i;
-    const int h = it.head * a.GQ + row - i * a.GQ;
-    const float inv = inverse(sum);
-    const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
-    store_dims<F16, 4>(a, t, h, d, v);
-    if (d == 0) store_lse(a, t, h, top, sum);
 }
 
 }  // namespace q4

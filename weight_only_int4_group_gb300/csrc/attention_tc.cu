@@ -82,99 +82,28 @@ struct Sizes {
     static_assert(SMEM <= 227 * 1024, "one CTA per SM");
 };
 
-// A CTA's pieces of items, walked alike by every role.
-struct Walk {
-    Item it;
-    int64_t v0, vu;    // the item's and the piece's place in the call's sequence
-    int vn;            // and its length there
-    int kt, nu;        // units [kt, kt + nu) of the item
-    int units, kt0;    // the item's units, the first one's index among the request's keys
-    int row0, row1, t0, base, kv;
-    bool same;         // all but the head as in the piece before
-    __device__ __forceinline__ Walk(const AttnArgs &a, const Range &r) : it(r.first), same(false)
-    {
-        vu = r.u0;
-        if (vu >= r.u1) return;
-        load(a, r);
-        cut(r, r.kt);
-        while (nu <= 0 && vu < r.u1) step(a, r);
-    }
-    __device__ __forceinline__ bool more(const Range &r) const { return vu < r.u1; }
-    // Another piece follows (one that would be padding alone does not count).
-    __device__ __forceinline__ bool follows(const Range &r) const { return r.u1 - (vu + vn) > PAD; }
-    // The next piece that holds a unit.
-    __device__ __forceinline__ void next(const AttnArgs &a, const Range &r)
-    {
-        do step(a, r);
-        while (nu <= 0 && vu < r.u1);
-    }
-    __device__ __forceinline__ bool whole() const { return kt == 0 && nu == units; }
-    // Units [lo, hi) of the piece that subtile w sees, and the places of its
-    // first and last row.
-    struct Seen {
-        int a, b, lo, hi;
-    };
-    __device__ __forceinline__ Seen seen(const AttnArgs &a, int w) const
-    {
-        Seen s = {0, 0, -1, -1};
-        const int r0 = row0 + w * SR, r1 = min(row1, r0 + SR);
-        if (r0 >= r1) return s;
-        s.lo = base + a.by_GQ.div(r0);
-        s.hi = base + a.by_GQ.div(r1 - 1);
-        if (s.hi < 0) return s;
-        const int64_t first = static_cast<int64_t>(s.lo) - a.window + 1;
-        const int u0 = (a.window > 0 && first > 0 ? static_cast<int>(first) : 0) / TK - kt0 - kt;
-        const int u1 = s.hi / TK + 1 - kt0 - kt;
-        s.a = min(max(u0, 0), nu);
-        s.b = max(s.a, min(u1, nu));
-        return s;
-    }
+using Pieces = Walk<R, TK, PAD>;
 
-private:
-    __device__ __forceinline__ void load(const AttnArgs &a, const Range &r)
-    {
-        const Span<R, TK> sp(a, it.b, it.rt);
-        units = sp.units;
-        kt0 = sp.kt0;
-        row0 = sp.row0;
-        row1 = sp.row1;
-        t0 = sp.t0;
-        base = sp.base;
-        kv = sp.kv;
-    }
-    // The piece of the item from its place v on: the first PAD places of an
-    // item hold no unit.
-    __device__ __forceinline__ void cut(const Range &r, int v)
-    {
-        v0 = vu - v;
-        vn = static_cast<int>(min(static_cast<int64_t>(units + PAD - v), r.u1 - vu));
-        kt = max(v - PAD, 0);
-        nu = max(v + vn - PAD, 0) - kt;
-    }
-    __device__ __forceinline__ void step(const AttnArgs &a, const Range &r)
-    {
-        const bool was_whole = whole();
-        vu += vn;
-        same = false;
-        if (vu >= r.u1) return;
-        if (++it.head < a.Hkv) {  // the same rows and keys of the next head
-            cut(r, 0);
-            same = was_whole && nu == units;
-            return;
-        }
-        it.next_rows(a, R);
-        load(a, r);
-        cut(r, 0);
-    }
-
-public:
-    // First and last CTA that hold units of the item.
-    __device__ __forceinline__ void holders(const Range &r, int &first, int &last) const
-    {
-        first = owner_of(v0 + PAD, r.total, r.G);
-        last = owner_of(v0 + PAD + units - 1, r.total, r.G);
-    }
+// Units [a, b) of a piece that subtile w sees, and the places of its first and
+// last row.
+struct Seen {
+    int a, b, lo, hi;
 };
+__device__ __forceinline__ Seen seen(const AttnArgs &a, const Pieces &k, int w)
+{
+    Seen s = {0, 0, -1, -1};
+    const int r0 = k.row0 + w * SR, r1 = min(k.row1, r0 + SR);
+    if (r0 >= r1) return s;
+    s.lo = k.base + a.by_GQ.div(r0);
+    s.hi = k.base + a.by_GQ.div(r1 - 1);
+    if (s.hi < 0) return s;
+    const int64_t first = static_cast<int64_t>(s.lo) - a.window + 1;
+    const int u0 = (a.window > 0 && first > 0 ? static_cast<int>(first) : 0) / TK - k.kt0 - k.kt;
+    const int u1 = s.hi / TK + 1 - k.kt0 - k.kt;
+    s.a = min(max(u0, 0), k.nu);
+    s.b = max(s.a, min(u1, k.nu));
+    return s;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
 {
@@ -285,7 +214,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
     grid_dep_launch_dependents();
     grid_dep_wait();
     tc_fence_before();
-    const Range rng = cta_range<R, TK, NW, MIN_UNITS, PAD>(a, ls);  // barriers inside
+    const Range rng = share<R, TK, NW, MIN_UNITS, PAD>(a, ls, blockIdx.x, gridDim.x);  // barriers inside
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -309,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         const int bk = lane / Z::CH * maps.kb, ch = lane % Z::CH;
         const bool boxed = bk < TK;
         const uint32_t bd = ch * Z::CHUNK + bk * 128;
-        Walk k(a, rng);
+        Pieces k(a, rng);
         int g = 0;  // units loaded
         for (; ok && k.more(rng) && !a.debug_no_copy; k.next(a, rng)) {
             const int *trow = a.table + k.it.b * a.table_stride;
@@ -363,14 +292,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         // ------------------------------------------------------ queries
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LO));
         const uint32_t sq = smem_u32(smem + Z::OFF_Q);
-        Walk k(a, rng);
-        Walk::Seen s0, s1;
+        Pieces k(a, rng);
+        Seen s0, s1;
         int pc = 0, loaded = 0;
         for (; ok && k.more(rng) && !a.debug_no_copy; ++pc, k.next(a, rng)) {
             for (int w = 0; w < 2; ++w) {
                 if (w == 0 && !k.same) {
-                    s0 = k.seen(a, 0);
-                    s1 = k.seen(a, 1);
+                    s0 = seen(a, k, 0);
+                    s1 = seen(a, k, 1);
                 }
                 if (pc > 0 && !(ok = warp_wait(&qempty[w], (pc - 1) & 1))) break;
                 ++loaded;
@@ -475,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         // rows finish an item, the other's, and its own next scores, go on.
         int nu = 0, a0 = 0, b0 = 0, a1 = 0, b1 = 0, follows = 0;  // the piece
         int j = 0, pc = 0;
-        bool more = Walk(a, rng).more(rng);  // there is a next unit
+        bool more = Pieces(a, rng).more(rng);  // there is a next unit
         auto read_note = [&]() {
             const volatile int *x = note + (pc & 1) * 6;
             nu = x[0];
@@ -548,12 +477,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         const uint32_t ts = tmem + lanes + Z::S_COL + w * 128, to = tmem + lanes + Z::O_COL + w * DP;
         const bool neg = a.scale_log2 <= 0.0f;
         uint32_t ns = 0, no = 0;
-        Walk::Seen p;
+        Seen p;
         int r, place;
         bool in;
-        for (Walk k(a, rng); k.more(rng); k.next(a, rng)) {
+        for (Pieces k(a, rng); k.more(rng); k.next(a, rng)) {
             if (!k.same) {
-                p = k.seen(a, w);
+                p = seen(a, k, w);
                 r = k.row0 + w * SR + rr;
                 in = r < k.row1;
                 place = in ? k.base + a.by_GQ.div(r) : -1;
