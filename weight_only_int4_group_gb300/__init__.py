@@ -392,8 +392,10 @@ class CachePlan:
     @classmethod
     def empty(cls, B: int, T: int, device=None) -> "CachePlan":
         device = device or torch.cuda.current_device()
-        parts = torch.empty(2 * B + 5 + T, dtype=torch.int32, device=device).split_with_sizes((B + 1, B, T, 4))
-        return cls(parts[0], parts[1], parts[2], torch.empty(T, dtype=torch.int64, device=device), parts[3])
+        i32 = torch.int32
+        return cls(torch.empty(B + 1, dtype=i32, device=device), torch.empty(B, dtype=i32, device=device),
+                   torch.empty(T, dtype=i32, device=device), torch.empty(T, dtype=torch.int64, device=device),
+                   torch.empty(4, dtype=i32, device=device))
 
 
 # The checks below are a call's whole host cost beside the launch: a few tenths

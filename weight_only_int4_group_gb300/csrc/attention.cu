@@ -17,9 +17,10 @@
 // by cp.async (16 bytes per lane; keys past the request's end, blocks outside
 // the cache and the padding of head_dim are filled with zeros, so nothing
 // stale is ever multiplied); the loads run ahead through the ends of items.
-// An item cut by a range boundary leaves its pieces in the workspace, in the
-// lanes' own order; the last warp to arrive adds them in sequence order, so
-// results do not depend on timing.
+// An item cut by range boundaries leaves its pieces in the workspace, in the
+// lanes' own order; the last warp to arrive adds them (eight at a time, in a
+// tree, when there are many), always in sequence order, so results do not
+// depend on timing.
 #include "serve.cuh"
 #include "attention.cuh"
 
@@ -33,7 +34,12 @@ constexpr int STAGES = 3;    // units in flight per warp
 constexpr int THREADS = NW * 32;
 // Places that an item takes beside its units (its beginning and end), and the
 // least that a warp gets.
-constexpr int PAD = 1, MIN_UNITS = 2;
+constexpr int PAD = 4, MIN_UNITS = 4;
+// Parts that are added at a time where an item is split (4 levels hold 4096
+// workers, the most there are).
+constexpr int MERGE = 8, LEVELS = 4, MOST_CTAS = 256;
+static_assert(MERGE * MERGE * MERGE * MERGE >= NW * MOST_CTAS, "levels");
+static_assert(LEVELS * 2 * NW * MOST_CTAS * sizeof(unsigned int) <= ATTN_COUNTER_BYTES, "counters");
 
 template <int DP>
 struct Sizes {
@@ -249,38 +255,50 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
 
         bool store = k.whole();
         if (!store) {
+            // the item's pieces are the leaves of a tree of MERGE-fold nodes
+            // over the workers that hold them; whoever completes a node adds
+            // its parts in order, leaves the sum in the first part's place and
+            // goes on to the next level.  A node's counter goes by its first
+            // worker, which may also hold the end of another item.
             int w0, w1;
             k.holders(rng, w0, w1);
             // [dim pair][row half][lane], then (reference, sum) [row half][lane]
             auto part = [&](int w) {
                 return reinterpret_cast<float2 *>(a.part + (2 * static_cast<int64_t>(w) + (w == w0)) * Z::SLOT) + lane;
             };
-            float2 *ps = part(me);
-            if (store_ok(reinterpret_cast<float *>(ps - lane) + Z::SLOT - 1 - a.part, a.part_len, a.err)) {
+            int at = me;            // where this warp's sum goes
+            int nodes = w1 - w0 + 1, idx = me - w0, stride = 1;  // of the level
+            unsigned int *count = a.count;
+            for (;;) {
+                float2 *ps = part(at);
+                if (store_ok(reinterpret_cast<float *>(ps - lane) + Z::SLOT - 1 - a.part, a.part_len, a.err)) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (j == 1 && !two) break;
+                    for (int j = 0; j < 2; ++j) {
+                        if (j == 1 && !two) break;
 #pragma unroll
-                    for (int n = 0; n < NO; ++n) ps[(n * 2 + j) * 32] = make_float2(o[n][2 * j], o[n][2 * j + 1]);
-                    ps[(NO * 2 + j) * 32] = make_float2(m[j], l[j]);
+                        for (int n = 0; n < NO; ++n) ps[(n * 2 + j) * 32] = make_float2(o[n][2 * j], o[n][2 * j + 1]);
+                        ps[(NO * 2 + j) * 32] = make_float2(m[j], l[j]);
+                    }
                 }
-            }
-            __threadfence();
-            __syncwarp();
-            int last = 0;
-            if (lane == 0) {
-                last = store_ok(w0, a.count_len, a.err) &&
-                       atomic_add_acq_rel_gpu(a.count + w0, 1u) == static_cast<unsigned>(w1 - w0);
-                if (last) a.count[w0] = 0u;
-            }
-            store = __shfl_sync(0xffffffffu, last, 0) != 0;
-            if (store) {
+                __threadfence();
+                __syncwarp();
+                const int first = idx / MERGE * MERGE, n_parts = min(MERGE, nodes - first);
+                at = w0 + first * stride;
+                int last = 0;
+                if (lane == 0) {
+                    unsigned int *c = count + 2 * at + (first == 0);
+                    last = store_ok(c - a.count, a.count_len, a.err) &&
+                           atomic_add_acq_rel_gpu(c, 1u) == static_cast<unsigned>(n_parts - 1);
+                    if (last) *c = 0u;
+                }
+                if (!__shfl_sync(0xffffffffu, last, 0)) break;
                 m[0] = m[1] = -INFINITY;
                 l[0] = l[1] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-                for (int w = w0; w <= w1; ++w) {
-                    const float2 *x = part(w);
+#pragma unroll 2
+                for (int i = 0; i < n_parts; ++i) {
+                    const float2 *x = part(at + i * stride);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         if (j == 1 && !two) break;
@@ -298,6 +316,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
                             o[n][2 * j + 1] = o[n][2 * j + 1] * g0 + y[n].y * g1;
                         }
                     }
+                }
+                idx = first / MERGE;
+                nodes = (nodes + MERGE - 1) / MERGE;
+                stride *= MERGE;
+                count += 2 * NW * gridDim.x;
+                if (nodes == 1) {
+                    store = true;
+                    break;
                 }
             }
         }
@@ -340,7 +366,7 @@ cudaError_t launch(const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 AttnPlan attention_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count)
 {
     AttnPlan p{};
-    p.grid = std::min<int>(sm_count, ATTN_COUNTER_BYTES / sizeof(unsigned int) / NW);
+    p.grid = std::min<int>(sm_count, MOST_CTAS);
     p.tc = max_fresh > R / GQ;
     const size_t slot = (D > 64 ? Sizes<128>::SLOT : Sizes<64>::SLOT) * sizeof(float);
     const size_t part = p.tc ? attention_tc_part_bytes(D, p.grid) : 2 * static_cast<size_t>(p.grid) * NW * slot;

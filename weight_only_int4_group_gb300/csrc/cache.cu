@@ -40,18 +40,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_cache_plan(const PlanArgs a)
     int *start = plan_smem;           // [B + 1]
     int *first = plan_smem + a.B + 1; // [B] first entry of the free stack taken; -1: not served
     __shared__ int64_t wsum[2][PLAN_THREADS / 32];
-    __shared__ int unserved;
-    __shared__ unsigned long long used_s, tok_s;
+    __shared__ unsigned int tally[3];  // blocks taken, tokens served, requests not served
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool lead = blockIdx.x == 0;
 
     grid_dep_launch_dependents();
     grid_dep_wait();
-    if (tid == 0) {
-        unserved = 0;
-        used_s = 0;
-        tok_s = 0;
-    }
+    if (tid < 3) tally[tid] = 0;
     const int64_t avail = max(0, min(*a.free_count, a.free_capacity));
 
     // contiguous requests per thread, then an exclusive scan over the threads
@@ -82,8 +77,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_cache_plan(const PlanArgs a)
         rn += wsum[0][w];
         rb += wsum[1][w];
     }
-    unsigned long long my_used = 0, my_tok = 0;
-    int my_un = 0;
+    unsigned int mine[3] = {0, 0, 0};  // at most avail, T and B in all
     for (int b = b0; b < b1; ++b) {
         const Need r = need_of(a, b);
         const bool served = r.fits && rn + r.n <= a.T && (r.nb == 0 || rb + r.nb <= avail);
@@ -93,10 +87,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_cache_plan(const PlanArgs a)
             if (store_ok(b, static_cast<int64_t>(a.B) + 1, a.err)) a.q_start[b] = start[b];
             if (store_ok(b, a.B, a.err)) a.kv_len[b] = served ? a.cached[b] + a.fresh[b] : 0;
             if (served) {
-                my_used += r.nb;
-                my_tok += r.n;
+                mine[0] += static_cast<unsigned int>(r.nb);
+                mine[1] += static_cast<unsigned int>(r.n);
             } else {
-                ++my_un;
+                ++mine[2];
             }
         }
         rn += r.n;
@@ -107,15 +101,19 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_cache_plan(const PlanArgs a)
         start[a.B] = static_cast<int>(min(rn, static_cast<int64_t>(a.T)));
         if (lead && store_ok(a.B, static_cast<int64_t>(a.B) + 1, a.err)) a.q_start[a.B] = start[a.B];
     }
-    if (lead && my_used) atomicAdd(&used_s, my_used);
-    if (lead && my_tok) atomicAdd(&tok_s, my_tok);
-    if (lead && my_un) atomicAdd(&unserved, my_un);
+    if (lead) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const unsigned int s = __reduce_add_sync(0xffffffffu, mine[i]);
+            if (lane == 0 && s) atomicAdd(&tally[i], s);
+        }
+    }
     __syncthreads();
     if (lead && tid < 4 && store_ok(tid, 4, a.err))
         a.counts[tid] = tid == 0   ? start[a.B]
-                        : tid == 1 ? static_cast<int>(tok_s)
-                        : tid == 2 ? static_cast<int>(avail - static_cast<int64_t>(used_s))
-                                   : unserved;
+                        : tid == 1 ? static_cast<int>(tally[1])
+                        : tid == 2 ? static_cast<int>(avail) - static_cast<int>(tally[0])
+                                   : static_cast<int>(tally[2]);
 
     // the requests' new table entries, requests dealt over the grid's warps
     const int nwarp = gridDim.x * (PLAN_THREADS / 32);

@@ -42,7 +42,7 @@ struct AttnArgs {
     int D, S, blocks, width;
     float scale_log2;  // scale * log2(e): scores in units of log 2
     int window;        // 0: none
-    unsigned int *count;  // arrival counters: two per CTA, or one per warp
+    unsigned int *count;  // arrival counters
     float *part;          // partial results: four per CTA, or two per warp
     int64_t count_len, part_len;  // their extents, for the store checks
     uint64_t wait_ns;
@@ -50,7 +50,7 @@ struct AttnArgs {
     unsigned int *err;
 };
 
-constexpr size_t ATTN_COUNTER_BYTES = 16384;  // room for 8 counters of 512 CTAs
+constexpr size_t ATTN_COUNTER_BYTES = 131072;
 
 struct AttnPlan {
     bool tc;         // tensor-core kernel (many rows per KV head)
