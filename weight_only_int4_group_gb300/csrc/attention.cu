@@ -92,6 +92,45 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Adds n parts, the first at x and the others 2 * stride slots on each (a first
+// piece of an item lies in the odd slot of its worker), to the row halves
+// 0..J - 1 of the empty sums o, m, l; AHEAD parts' loads are in flight.
+template <int J, int AHEAD, int NO>
+__device__ __forceinline__ void add_parts(const float2 *x, int stride, int n, bool odd, int slot, float (&o)[NO][4],
+                                          float (&m)[2], float (&l)[2])
+{
+    const float2 *even = x - (odd ? slot / 2 : 0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+        float2 y[AHEAD][J][NO], ml[AHEAD][J];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const bool in = i0 + i < n;
+            const float2 *p = i0 + i == 0 ? x : even + static_cast<int64_t>(i0 + i) * stride * slot;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                ml[i][j] = in ? __ldcg(p + (NO * 2 + j) * 32) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                for (int k = 0; k < NO; ++k) y[i][j][k] = in ? __ldcg(p + (k * 2 + j) * 32) : make_float2(0.0f, 0.0f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float mn = fmaxf(m[j], ml[i][j].x), ref = mn == -INFINITY ? 0.0f : mn;
+                const float g0 = ex2(m[j] - ref), g1 = ex2(ml[i][j].x - ref);
+                m[j] = mn;
+                l[j] = l[j] * g0 + ml[i][j].y * g1;
+#pragma unroll
+                for (int k = 0; k < NO; ++k) {
+                    o[k][2 * j] = o[k][2 * j] * g0 + y[i][j][k].x * g1;
+                    o[k][2 * j + 1] = o[k][2 * j + 1] * g0 + y[i][j][k].y * g1;
+                }
+            }
+    }
+}
+
 template <bool F16, int DP>
 __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
 {
@@ -296,27 +335,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
                 l[0] = l[1] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-#pragma unroll 2
-                for (int i = 0; i < n_parts; ++i) {
-                    const float2 *x = part(at + i * stride);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (j == 1 && !two) break;
-                        float2 y[NO];
-#pragma unroll
-                        for (int n = 0; n < NO; ++n) y[n] = __ldcg(x + (n * 2 + j) * 32);
-                        const float2 ml = __ldcg(x + (NO * 2 + j) * 32);
-                        const float mn = fmaxf(m[j], ml.x), ref = mn == -INFINITY ? 0.0f : mn;
-                        const float g0 = ex2(m[j] - ref), g1 = ex2(ml.x - ref);
-                        m[j] = mn;
-                        l[j] = l[j] * g0 + ml.y * g1;
-#pragma unroll
-                        for (int n = 0; n < NO; ++n) {
-                            o[n][2 * j] = o[n][2 * j] * g0 + y[n].x * g1;
-                            o[n][2 * j + 1] = o[n][2 * j + 1] * g0 + y[n].y * g1;
-                        }
-                    }
-                }
+                if (two)
+                    add_parts<2, 2, NO>(part(at), stride, n_parts, w0 == at, Z::SLOT, o, m, l);
+                else
+                    add_parts<1, 4, NO>(part(at), stride, n_parts, w0 == at, Z::SLOT, o, m, l);
                 idx = first / MERGE;
                 nodes = (nodes + MERGE - 1) / MERGE;
                 stride *= MERGE;

@@ -122,10 +122,12 @@ __device__ __forceinline__ int64_t request_units(const AttnArgs &a, int b, bool 
     return sum;
 }
 
-// Sums of slabs of requests, one per warp; a barrier.
+// Sums of slabs of requests, one per warp; a barrier.  Nothing for up to 32
+// requests, which one warp sees at once.
 template <int R, int TK, int NW, int PAD>
 __device__ __forceinline__ void sum_slabs(const AttnArgs &a, LocateScratch &ls)
 {
+    if (a.B <= 32) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b0 = static_cast<int>(static_cast<int64_t>(a.B) * warp / NW),
               b1 = static_cast<int>(static_cast<int64_t>(a.B) * (warp + 1) / NW);
@@ -155,11 +157,18 @@ template <int R, int TK, int NW, int MIN_UNITS, int PAD>
 __device__ Range find_share(const AttnArgs &a, const LocateScratch &ls, int worker, int workers)
 {
     const int lane = threadIdx.x & 31;
-    int64_t all = 0;
+    const bool few = a.B <= 32;
+    int64_t all = 0, mine = 0, incl = 0;
+    if (few) {
+        mine = request_units<R, TK, PAD>(a, lane, lane < a.B) * a.Hkv;
+        incl = inclusive_sum(mine);
+        all = __shfl_sync(0xffffffffu, incl, 31);
+    } else {
 #pragma unroll
-    for (int w = 0; w < NW; ++w) all += ls.slab[w];
+        for (int w = 0; w < NW; ++w) all += ls.slab[w] * a.Hkv;
+    }
     Range r = {};
-    r.total = all * a.Hkv;
+    r.total = all;
     r.G = static_cast<int>(min(static_cast<int64_t>(workers), (r.total + MIN_UNITS - 1) / MIN_UNITS));
     if (worker >= r.G) return r;
     r.u0 = worker * r.total / r.G;
@@ -167,13 +176,18 @@ __device__ Range find_share(const AttnArgs &a, const LocateScratch &ls, int work
     if (r.u0 >= r.u1) return r;
     // the slab, then the request, then the row tile that holds place u0
     int64_t left = r.u0;
-    int slab = 0;
-    while (left >= ls.slab[slab] * a.Hkv) left -= ls.slab[slab++] * a.Hkv;
-    const int b0 = static_cast<int>(static_cast<int64_t>(a.B) * slab / NW),
-              b1 = static_cast<int>(static_cast<int64_t>(a.B) * (slab + 1) / NW);
+    int b0 = 0, b1 = a.B;
+    if (!few) {
+        int slab = 0;
+        while (left >= ls.slab[slab] * a.Hkv) left -= ls.slab[slab++] * a.Hkv;
+        b0 = static_cast<int>(static_cast<int64_t>(a.B) * slab / NW);
+        b1 = static_cast<int>(static_cast<int64_t>(a.B) * (slab + 1) / NW);
+    }
     for (int b = b0; b < b1; b += 32) {
-        const int64_t mine = request_units<R, TK, PAD>(a, b + lane, b + lane < b1) * a.Hkv;
-        const int64_t incl = inclusive_sum(mine);
+        if (!few) {
+            mine = request_units<R, TK, PAD>(a, b + lane, b + lane < b1) * a.Hkv;
+            incl = inclusive_sum(mine);
+        }
         const unsigned past = __ballot_sync(0xffffffffu, incl > left);
         if (!past) {
             left -= __shfl_sync(0xffffffffu, incl, 31);

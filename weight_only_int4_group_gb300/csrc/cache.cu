@@ -182,6 +182,10 @@ cudaError_t cache_plan_launch(const PlanArgs &a, cudaStream_t s)
 namespace {
 
 constexpr int ROPE_THREADS = 256;
+#ifndef ROPE_TOK
+#define ROPE_TOK 1
+#define ROPE_SPLIT 1
+#endif
 
 template <bool F16>
 __device__ __forceinline__ float to_f32(uint16_t b)
@@ -304,8 +308,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope_append(const RopeArgs a, 
 template <bool F16, bool INTER>
 cudaError_t rope_launch(const RopeArgs &a, cudaStream_t s)
 {
-    const int tok = 1;
-    const int split = 1;
+    const int tok = ROPE_TOK;
+    const int split = ROPE_SPLIT;
     const dim3 grid((a.T + tok - 1) / tok, split);
     const size_t smem = static_cast<size_t>(tok) * (a.rot / 2) * sizeof(float2);
     // the widest vector that divides the pair layout and both parts of the head
