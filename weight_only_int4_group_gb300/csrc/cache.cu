@@ -10,7 +10,8 @@ namespace {
 // tokens (first row of each request) and of the blocks they need (which
 // entries of the free stack each request takes).  The data are a few bytes
 // per request and 12 bytes per token, so the call is a launch and three
-// dependent memory round trips; every CTA repeats the sums over all requests
+// dependent memory round trips (measured, in a graph: 3.5 us for 8 requests,
+// 5.5 us for 1024 with 16000 tokens); every CTA repeats the sums over all requests
 // (8 bytes each, from L2 after the first CTA) instead of a second launch,
 // then finds the request of each of its tokens by bisection in shared memory.
 constexpr int PLAN_THREADS = 512;
@@ -179,13 +180,13 @@ cudaError_t cache_plan_launch(const PlanArgs &a, cudaStream_t s)
 // loads a half head apart, or one load of interleaved pairs) or a VEC-element
 // copy (the unrotated part of a head, the values).  VEC is the widest vector
 // that the pair layout allows, 8 elements (16 bytes) for the usual sizes.
+// Measured: 8192 rows of 80 heads of 128 in 57.7 us, 5.8 TB/s read and
+// written, 0.86 of the measured copy bandwidth (the cache rows are 256-byte
+// pieces at random places).  Several units per thread in flight were slower
+// (74 us and more): the registers cost more warps than the loads gain.
 namespace {
 
 constexpr int ROPE_THREADS = 256;
-#ifndef ROPE_TOK
-#define ROPE_TOK 1
-#define ROPE_SPLIT 1
-#endif
 
 template <bool F16>
 __device__ __forceinline__ float to_f32(uint16_t b)
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope_append(const RopeArgs a, 
     if (tid < nt) {
         const int64_t slot = a.slot[t0 + tid];
         const bool in = slot >= 0 && slot < static_cast<int64_t>(a.blocks) * a.S;
-        const int64_t blk = in ? slot / a.S : 0;
+        const int64_t blk = !in ? 0 : slot >> 32 ? slot / a.S : static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.S);
         dst_off[tid] = in ? blk * a.block_stride + (slot - blk * a.S) * a.token_stride : -1;
     }
     __syncthreads();
@@ -308,8 +309,14 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope_append(const RopeArgs a, 
 template <bool F16, bool INTER>
 cudaError_t rope_launch(const RopeArgs &a, cudaStream_t s)
 {
-    const int tok = ROPE_TOK;
-    const int split = ROPE_SPLIT;
+    // Tokens per CTA and CTAs per token (us, 64 + 2 * 8 heads of 128): few
+    // tokens are latency, shared out finer (T = 4: 2.7 by four CTAs each, 3.7
+    // by one; T = 152: 3.7 by two, 4.0 by four); many are bandwidth, where
+    // more tokens per CTA spare beginnings (T = 8192: 57.7 by four tokens in
+    // two halves, 64.1 by one; T = 2048: 18.2 and 16.9).
+    const bool many = a.T >= 3000;
+    const int tok = many ? 4 : 1;
+    const int split = many ? 2 : a.T <= 64 ? 4 : a.T <= 152 ? 2 : 1;
     const dim3 grid((a.T + tok - 1) / tok, split);
     const size_t smem = static_cast<size_t>(tok) * (a.rot / 2) * sizeof(float2);
     // the widest vector that divides the pair layout and both parts of the head
