@@ -144,6 +144,12 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y)
     return r;
 }
 
+// A value that all lanes hold (at least 0), by an instruction whose result the
+// compiler knows to be the same in all lanes: what only depends on such values
+// stays in uniform registers, where the MMA instructions take their operands
+// from, instead of being moved there for each of them.
+__device__ __forceinline__ int uniform(int x) { return static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(x))); }
+
 // The call's tensor maps and how the producers use them.
 struct Maps {
     CUtensorMap k, v;  // (dim, token, head, block), boxes of 64 x kb x 1 x 1
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         const uint64_t dq = sw128_desc(smem_u32(smem + Z::OFF_Q));
         const uint64_t dk = sw128_desc(smem_u32(smem + Z::OFF_R));
         const uint64_t dv = sw128_desc(smem_u32(smem + Z::OFF_R), Z::CHUNK);
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t tm = uniform(tmem);
         // scores of subtile w with the keys in slot s; output of subtile w
         // with the values in slot s
         auto qk = [&](auto w_, int s) {
@@ -404,15 +410,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         // rows finish an item, the other's, and its own next scores, go on.
         int nu = 0, a0 = 0, b0 = 0, a1 = 0, b1 = 0, follows = 0;  // the piece
         int j = 0, pc = 0;
-        bool more = Pieces(a, rng).more(rng);  // there is a next unit
+        bool more = __any_sync(0xffffffffu, Pieces(a, rng).more(rng));  // there is a next unit
         auto read_note = [&]() {
             const volatile int *x = note + (pc & 1) * 6;
-            nu = x[0];
-            a0 = x[1];
-            b0 = x[2];
-            a1 = x[3];
-            b1 = x[4];
-            follows = x[5];
+            nu = uniform(x[0]);
+            a0 = uniform(x[1]);
+            b0 = uniform(x[2]);
+            a1 = uniform(x[3]);
+            b1 = uniform(x[4]);
+            follows = uniform(x[5]);
         };
         if (more) {
             ok = warp_wait(&qfull[0], 0) && warp_wait(&qfull[1], 0) && warp_wait(&kfull[0], 0);
