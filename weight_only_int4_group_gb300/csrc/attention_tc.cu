@@ -112,6 +112,20 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
                  : "memory");
 }
 
+// One probe that may wait for the hardware's own time: reacts sooner than
+// one with a long time given, and takes no issue slots as polling does (whole
+// tiles of 256 rows: 4% and 7% of the time).
+__device__ __forceinline__ bool mbar_ready(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // This lane's arrival on bar after its copies so far have landed, in order
 // with the tensor cores' reads.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
@@ -224,7 +238,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return mbar_wait_bounded(bar, parity, abort_flag, a.wait_ns, a.err);
+        if (mbar_ready(bar, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (;;) {
+            if (mbar_ready(bar, parity)) return true;
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > a.wait_ns) {
+                *abort_flag = 1;
+                atomicOr(a.err, ERR_TIMEOUT);
+                return false;
+            }
+        }
     };
     // by whole warps: the lanes get one answer, also when a wait runs out
     auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
@@ -383,23 +407,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         // with the values in slot s
         auto qk = [&](auto w_, int s) {
             constexpr int w = decltype(w_)::value;
-            const uint64_t k0 = dk + ((s * Z::TILE) >> 4);
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                const int o = (k / 4) * Z::CHUNK + (k % 4) * 32;
-                mma_ss(tm + Z::S_COL + w * 128, dq + ((w * Z::TILE + o) >> 4), k0 + (o >> 4), id_qk, k > 0);
-            }
-            mma_commit_elected(&sfull[w]);
+            mma_rows_ss<DP / 16>(tm + Z::S_COL + w * 128, dq + ((w * Z::TILE) >> 4), dk + ((s * Z::TILE) >> 4), id_qk,
+                                 &sfull[w]);
         };
         auto pv = [&](auto w_, int s, bool acc, uint32_t parity) {
             constexpr int w = decltype(w_)::value;
             if (!warp_wait(&pfull[w], parity)) return false;
             tc_fence_after();
-            const uint64_t v0 = dv + (((2 + s) * Z::TILE) >> 4);
-#pragma unroll
-            for (int k = 0; k < TK / 16; ++k)
-                mma_ts(tm + Z::O_COL + w * DP, tm + Z::S_COL + w * 128 + k * 8, v0 + ((k * 16 * 128) >> 4), id_pv,
-                       acc || k > 0);
+            mma_rows_ts(tm + Z::O_COL + w * DP, tm + Z::S_COL + w * 128, dv + (((2 + s) * Z::TILE) >> 4), id_pv, acc);
             return true;
         };
         int g = 0;                  // units so far
@@ -593,59 +608,55 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
             const bool rows = k.row0 + w * SR < k.row1;
             const int64_t t_row = k.t0 + (in ? a.by_GQ.div(r) : 0);
             const int h_row = k.it.head * a.GQ + (in ? r - a.by_GQ.div(r) * a.GQ : 0);
+            // 64 dims of the subtile from c on: they turn through shared memory,
+            // so that 8 lanes store 128 bytes of one row
+            auto put = [&](int c, const float (&o)[64]) {
+                if (a.ot == Q4_F32) {
+                    if (in) store_dims<F16, 64>(a, t_row, h_row, c, o);
+                    return;
+                }
+                uint8_t *st = smem + Z::OFF_O + warp * 4096;
+                const int q = lane & 7;
+                const int64_t o_len = static_cast<int64_t>(a.T - 1) * a.o_stride + static_cast<int64_t>(a.Hq) * a.D;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 64; i += 8)
+                    *reinterpret_cast<uint4 *>(st + lane * 128 + (((i / 8) ^ (lane & 7)) << 4)) =
+                        make_uint4(pack2<F16>(o[i], o[i + 1]), pack2<F16>(o[i + 2], o[i + 3]),
+                                   pack2<F16>(o[i + 4], o[i + 5]), pack2<F16>(o[i + 6], o[i + 7]));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int x = i * 4 + lane / 8, gr = k.row0 + w * SR + (warp & 3) * 32 + x;
+                    const uint4 y = *reinterpret_cast<const uint4 *>(st + x * 128 + ((q ^ (x & 7)) << 4));
+                    const int t = a.by_GQ.div(gr);
+                    const int64_t at = (k.t0 + t) * a.o_stride +
+                                       static_cast<int64_t>(k.it.head * a.GQ + gr - t * a.GQ) * a.D + c + q * 8;
+                    if (gr < k.row1 && c + q * 8 < a.D && store_ok(at + 7, o_len, a.err))
+                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + at) = y;
+                }
+            };
+            // 64 dims of the output in tensor memory
+            auto sums = [&](int c, float (&o)[64]) {
+                uint32_t v[2][32] = {};
+                __syncwarp();
+                if (any) {
+                    tmem_ld32x(to + c, v[0]);
+                    tmem_ld32x(to + c + 32, v[1]);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int i = 0; i < 64; ++i) o[i] = __uint_as_float(v[i / 32][i % 32]);
+            };
             if (k.whole()) {
                 const float inv = any ? inverse(l) : 0.0f;
-                if (a.ot == Q4_F32) {
 #pragma unroll 1
-                    for (int c = 0; c < DP; c += 32) {
-                        uint32_t v[32] = {};
-                        __syncwarp();
-                        if (any) {
-                            tmem_ld32x(to + c, v);
-                            tmem_wait_ld();
-                        }
-                        float o[32];
+                for (int c = 0; c < DP; c += 64) {
+                    float o[64];
+                    sums(c, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * inv;
-                        if (in) store_dims<F16, 32>(a, t_row, h_row, c, o);
-                    }
-                } else {
-                    // 64 dims of the warp's 32 rows turn through shared
-                    // memory, so that 8 lanes store 128 bytes of one row
-                    uint8_t *st = smem + Z::OFF_O + warp * 4096;
-                    const int q = lane & 7;
-                    const int64_t o_len = static_cast<int64_t>(a.T - 1) * a.o_stride + static_cast<int64_t>(a.Hq) * a.D;
-#pragma unroll 1
-                    for (int c = 0; c < DP; c += 64) {
-                        uint32_t v[2][32] = {};
-                        __syncwarp();
-                        if (any) {
-                            tmem_ld32x(to + c, v[0]);
-                            tmem_ld32x(to + c + 32, v[1]);
-                            tmem_wait_ld();
-                        }
-#pragma unroll
-                        for (int i = 0; i < 64; i += 8) {
-                            uint4 x;
-                            uint32_t *y = reinterpret_cast<uint32_t *>(&x);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                y[e] = pack2<F16>(__uint_as_float(v[i / 32][i % 32 + 2 * e]) * inv,
-                                                  __uint_as_float(v[i / 32][i % 32 + 2 * e + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(st + lane * 128 + (((i / 8) ^ (lane & 7)) << 4)) = x;
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int x = i * 4 + lane / 8, gr = k.row0 + w * SR + (warp & 3) * 32 + x;
-                            const uint4 y = *reinterpret_cast<const uint4 *>(st + x * 128 + ((q ^ (x & 7)) << 4));
-                            const int t = a.by_GQ.div(gr);
-                            const int64_t at = (k.t0 + t) * a.o_stride +
-                                               static_cast<int64_t>(k.it.head * a.GQ + gr - t * a.GQ) * a.D + c + q * 8;
-                            if (gr < k.row1 && c + q * 8 < a.D && store_ok(at + 7, o_len, a.err))
-                                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + at) = y;
-                        }
-                    }
+                    for (int i = 0; i < 64; ++i) o[i] *= inv;
+                    put(c, o);
                 }
                 if (in) store_lse(a, t_row, h_row, m, l);
                 __syncwarp();
@@ -653,17 +664,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 // [dim][row], so that a warp's stores and loads are whole lines
                 float *ps = a.part + ((2 * static_cast<int64_t>(blockIdx.x) + (k.kt == 0)) * 2 + w) * Z::PART;
                 const bool fits = store_ok(ps + Z::PART - 1 - a.part, a.part_len, a.err);
-                uint32_t v[32];
-#pragma unroll
-                for (int c = 0; c < DP / 32; ++c) {
-                    if (any) {
-                        tmem_ld32x(to + c * 32, v);
-                        tmem_wait_ld();
-                    }
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 64) {
+                    float o[64];
+                    sums(c, o);
                     if (fits)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            ps[(c * 32 + i) * SR + rr] = any ? __uint_as_float(v[i]) : 0.0f;
+                        for (int i = 0; i < 64; ++i) ps[(c + i) * SR + rr] = o[i];
                 }
                 if (fits) {
                     ps[DP * SR + rr] = m;
@@ -684,22 +691,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                     auto slot = [&](int f) {
                         return a.part + ((2 * static_cast<int64_t>(f) + (f == f0)) * 2 + w) * Z::PART + rr;
                     };
-                    // each part's weight once, kept in shared memory while
-                    // there are few parts
-                    constexpr int KEPT = 32;
-                    float *kept = reinterpret_cast<float *>(smem + Z::OFF_O + warp * 4096) + lane;  // [part][lane]
-                    float top = -INFINITY, sum = 0.0f;
-#pragma unroll 4
-                    for (int f = f0; f <= f1; ++f) top = fmaxf(top, __ldcg(slot(f) + DP * SR));
-                    const float ref = top == -INFINITY ? 0.0f : top;
-                    auto weight = [&](int f) { return ex2(__ldcg(slot(f) + DP * SR) - ref); };
+                    // the first parts' references stay in registers
+                    float top = -INFINITY, sum = 0.0f, m4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m4[i] = f0 + i <= f1 ? __ldcg(slot(f0 + i) + DP * SR) : -INFINITY;
+                    auto reference = [&](int f) {
+                        const int i = f - f0;
+                        return i == 0 ? m4[0] : i == 1 ? m4[1] : i == 2 ? m4[2] : i == 3 ? m4[3] : __ldcg(slot(f) + DP * SR);
+                    };
 #pragma unroll 4
                     for (int f = f0; f <= f1; ++f) {
-                        const float g = weight(f);
-                        sum += g * __ldcg(slot(f) + (DP + 1) * SR);
-                        if (f - f0 < KEPT) kept[(f - f0) * 32] = g;
+                        const float mf = reference(f), lf = __ldcg(slot(f) + (DP + 1) * SR);
+                        const float mn = fmaxf(top, mf), ref = mn == -INFINITY ? 0.0f : mn;
+                        sum = sum * ex2(top - ref) + lf * ex2(mf - ref);
+                        top = mn;
                     }
-                    const float inv = inverse(sum);
+                    const float ref = top == -INFINITY ? 0.0f : top, inv = inverse(sum);
                     // the CTA's own part is still in tensor memory
                     const int mine = static_cast<int>(blockIdx.x);
 #pragma unroll 1
@@ -709,30 +716,21 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                         for (int i = 0; i < 64; ++i) o[i] = 0.0f;
 #pragma unroll 1
                         for (int f = f0; f <= f1; ++f) {
-                            const float *x = slot(f);
-                            uint32_t y[64];
+                            const float *x = slot(f) + d * SR;
+                            float y[64];
                             if (f != mine) {
 #pragma unroll
-                                for (int i = 0; i < 64; ++i) y[i] = __float_as_uint(__ldcg(x + (d + i) * SR));
+                                for (int i = 0; i < 64; ++i) y[i] = __ldcg(x + i * SR);
                             } else {
-#pragma unroll
-                                for (int i = 0; i < 64; i += 32) {
-                                    uint32_t z[32] = {};
-                                    if (any) {
-                                        tmem_ld32x(to + d + i, z);
-                                        tmem_wait_ld();
-                                    }
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) y[i + e] = z[e];
-                                }
+                                sums(d, y);
                             }
-                            const float g = f - f0 < KEPT ? kept[(f - f0) * 32] : weight(f);
+                            const float g = ex2(reference(f) - ref);
 #pragma unroll
-                            for (int i = 0; i < 64; ++i) o[i] = fmaf(g, __uint_as_float(y[i]), o[i]);
+                            for (int i = 0; i < 64; ++i) o[i] = fmaf(g, y[i], o[i]);
                         }
 #pragma unroll
                         for (int i = 0; i < 64; ++i) o[i] *= inv;
-                        if (in) store_dims<F16, 64>(a, t_row, h_row, d, o);
+                        put(d, o);
                     }
                     if (in) store_lse(a, t_row, h_row, top, sum);
                 }

@@ -54,23 +54,81 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t ab, uint32_t n)
     return (1u << 4) | (ab << 7) | (ab << 10) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Called by whole warps, one elected lane issues.
-// d (tensor memory) = a * b^T, plus d when acc: a and b in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+// Products of a 128-row tile in groups of MMAs under one election, called by a
+// whole warp (one lane, always the same, issues), with a commit behind them.
+// d (tensor memory) = a * b^T over K = 16 * N of 64-element chunks 16 KB
+// apart, K-major in shared memory (descriptors of their first bytes).
+template <int N>
+__device__ __forceinline__ void mma_rows_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint64_t *bar)
 {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
-        : "memory");
+    static_assert(N == 4 || N == 8, "64 or 128 wide");
+    const uint32_t al = static_cast<uint32_t>(a), ah = static_cast<uint32_t>(a >> 32);
+    const uint32_t bl = static_cast<uint32_t>(b), bh = static_cast<uint32_t>(b >> 32);
+    if constexpr (N == 8)
+        asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 x;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %6, %6;\n\t"
+        "add.u32 x, %1, 0;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 0;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+        "add.u32 x, %1, 2;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 2;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 4;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 4;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 6;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 6;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 1024;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 1024;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 1026;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 1026;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 1028;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 1028;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 1030;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 1030;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t}" ::"r"(d),
+            "r"(al), "r"(bl), "r"(ah), "r"(bh), "r"(idesc), "r"(0u), "r"(smem_u32(bar))
+            : "memory");
+    else
+        asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 x;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %6, %6;\n\t"
+        "add.u32 x, %1, 0;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 0;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+        "add.u32 x, %1, 2;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 2;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 4;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 4;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 6;\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, 6;\n\tmov.b64 b, {x, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t}" ::"r"(d),
+            "r"(al), "r"(bl), "r"(ah), "r"(bh), "r"(idesc), "r"(0u), "r"(smem_u32(bar))
+            : "memory");
 }
-// The same with a in tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc)
+// d += a * b over K = 128 (d = when !acc): a in tensor memory, b MN-major in
+// shared memory, 128 bytes a row.
+__device__ __forceinline__ void mma_rows_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc)
 {
+    const uint32_t bl = static_cast<uint32_t>(b), bh = static_cast<uint32_t>(b >> 32);
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 x;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %6, %6;\n\t"
+        "add.u32 x, %2, 0;\n\tmov.b64 b, {x, %4};\n\tadd.u32 x, %1, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %5, p;\n\t"
+        "add.u32 x, %2, 128;\n\tmov.b64 b, {x, %4};\n\tadd.u32 x, %1, 8;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %5, t;\n\t"
+        "add.u32 x, %2, 256;\n\tmov.b64 b, {x, %4};\n\tadd.u32 x, %1, 16;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %5, t;\n\t"
+        "add.u32 x, %2, 384;\n\tmov.b64 b, {x, %4};\n\tadd.u32 x, %1, 24;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %5, t;\n\t"
+        "add.u32 x, %2, 512;\n\tmov.b64 b, {x, %4};\n\tadd.u32 x, %1, 32;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %5, t;\n\t"
+        "add.u32 x, %2, 640;\n\tmov.b64 b, {x, %4};\n\tadd.u32 x, %1, 40;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %5, t;\n\t"
+        "add.u32 x, %2, 768;\n\tmov.b64 b, {x, %4};\n\tadd.u32 x, %1, 48;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %5, t;\n\t"
+        "add.u32 x, %2, 896;\n\tmov.b64 b, {x, %4};\n\tadd.u32 x, %1, 56;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %5, t;\n\t"
+        "}" ::"r"(d),
+        "r"(a), "r"(bl), "r"(0u), "r"(bh), "r"(idesc), "r"(static_cast<uint32_t>(acc))
         : "memory");
 }
 
