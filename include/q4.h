@@ -448,7 +448,8 @@ q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t
  * once; every completed call leaves its counters zero, so it serves any
  * sequence of q4_attention calls on one stream, whatever their sizes, up to
  * the bytes it holds.  It is not shared with the products' workspace (whose
- * rule is stricter) nor with calls on other streams.
+ * rule is stricter) nor with calls on other streams; after a call whose
+ * bounded wait ran out (Q4_ERR_TIMEOUT) zero it again.
  * INVALID_ARG for NULL pointers, sizes < 1, Hq not a multiple of heads, a
  * non-finite scale, a negative window, a short workspace; UNSUPPORTED for
  * types, T * Hq or B beyond 2^31 - 1, width * block_size beyond 2^30 - 1, or a

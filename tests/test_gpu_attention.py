@@ -276,3 +276,37 @@ def test_bounded_waits_report_a_timeout():
     with pytest.raises(m.Q4Error):
         m.attention_timeout_selftest(one.q, m.KVCache(one.k, one.v), one.table, one.q_start, one.kv_len, 1,
                                         torch.empty_like(one.q), ws)
+
+
+@pytest.mark.parametrize("lengths", [[(20000, 1)], [(20000, 2)], [(20000, 3)], [(12000, 7)], [(9000, 13), (9000, 40)]],
+                         ids=str)
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_chains_of_parts(lengths, D):
+    """One KV head, so that many workers share an item: the tree of the
+    streaming kernel (three levels) and the joins of the tensor-core kernel
+    with at most 32, 64 and 128 rows."""
+    m = q4()
+    r = Requests(lengths, 8, 1, D, 32, torch.bfloat16, seed=16)
+    ws = m.attention_workspace(r.max_fresh, 8, 1, D)
+    o, lse = check(r, ws=ws)
+    for _ in range(3):
+        o2, lse2 = run(r, ws=ws)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_hundreds_of_requests(many):
+    """More than 32 requests take the other way of finding a worker's share."""
+    lengths = [(i * 53 % 400, (1 + i * 7 % 30 if many else 1) if i % 5 else 0) for i in range(333)]
+    check(Requests(lengths, 4, 2, 64, 16, torch.float16, seed=17))
+
+
+def test_an_empty_batch_writes_nothing():
+    m = q4()
+    for hint in (1, 100):
+        r = Requests([(5, 1), (7, 1)], 8, 2, 64, 16, torch.bfloat16, seed=18)
+        r.q_start.zero_()
+        out = torch.full_like(r.q, 9.0)
+        run(r, out=out, max_fresh=hint)
+        assert (out == 9.0).all()
+        assert m.check() == m.OK

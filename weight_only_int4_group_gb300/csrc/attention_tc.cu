@@ -61,6 +61,7 @@ constexpr int MIN_UNITS = 4;  // per CTA: a piece that is joined costs about as 
 constexpr int W_K = 8, W_V = 9, W_Q = 10;  // producers
 constexpr int W_M = 11;         // MMA issue
 constexpr int NW = 12, THREADS = NW * 32;  // 168 registers per thread; a 13th warp would cost 40 of them
+constexpr int MANY_PARTS = 3;  // more parts behind the first are added four at a time
 // Registers move from the copying and issuing warpgroup to the softmax ones,
 // which keep a row's 128 scores in registers.
 constexpr int REG_HI = 208, REG_LO = 80;
@@ -661,16 +662,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 if (in) store_lse(a, t_row, h_row, m, l);
                 __syncwarp();
             } else if (rows) {
-                // [dim][row], so that a warp's stores and loads are whole lines
+                // [dim / 4][row][4], so that a warp stores and loads whole lines,
+                // 16 bytes a lane
                 float *ps = a.part + ((2 * static_cast<int64_t>(blockIdx.x) + (k.kt == 0)) * 2 + w) * Z::PART;
                 const bool fits = store_ok(ps + Z::PART - 1 - a.part, a.part_len, a.err);
 #pragma unroll 1
                 for (int c = 0; c < DP; c += 64) {
                     float o[64];
                     sums(c, o);
-                    if (fits)
+                    if (fits && in)
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) ps[(c + i) * SR + rr] = o[i];
+                        for (int i = 0; i < 64; i += 4)
+                            *reinterpret_cast<float4 *>(ps + (c + i) * SR + rr * 4) =
+                                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
                 if (fits) {
                     ps[DP * SR + rr] = m;
@@ -689,50 +693,101 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 named_barrier_sync(1 + w, SR);
                 if (last_s[w]) {  // whole warps: they read tensor memory
                     auto slot = [&](int f) {
-                        return a.part + ((2 * static_cast<int64_t>(f) + (f == f0)) * 2 + w) * Z::PART + rr;
+                        return a.part + ((2 * static_cast<int64_t>(f) + (f == f0)) * 2 + w) * Z::PART;
                     };
-                    // the first parts' references stay in registers
-                    float top = -INFINITY, sum = 0.0f, m4[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) m4[i] = f0 + i <= f1 ? __ldcg(slot(f0 + i) + DP * SR) : -INFINITY;
-                    auto reference = [&](int f) {
+                    // The row's reference and sum over the parts; the first
+                    // parts' references stay in registers.
+                    float m4[4];
+                    auto reference = [&](int f, int row) {
                         const int i = f - f0;
-                        return i == 0 ? m4[0] : i == 1 ? m4[1] : i == 2 ? m4[2] : i == 3 ? m4[3] : __ldcg(slot(f) + DP * SR);
+                        return i == 0   ? m4[0]
+                               : i == 1 ? m4[1]
+                               : i == 2 ? m4[2]
+                               : i == 3 ? m4[3]
+                                        : __ldcg(slot(f) + DP * SR + row);
                     };
+                    auto total = [&](int row, float &top, float &sum) {
+                        top = -INFINITY;
+                        sum = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            m4[i] = f0 + i <= f1 ? __ldcg(slot(f0 + i) + DP * SR + row) : -INFINITY;
 #pragma unroll 4
-                    for (int f = f0; f <= f1; ++f) {
-                        const float mf = reference(f), lf = __ldcg(slot(f) + (DP + 1) * SR);
-                        const float mn = fmaxf(top, mf), ref = mn == -INFINITY ? 0.0f : mn;
-                        sum = sum * ex2(top - ref) + lf * ex2(mf - ref);
-                        top = mn;
-                    }
-                    const float ref = top == -INFINITY ? 0.0f : top, inv = inverse(sum);
-                    // the CTA's own part is still in tensor memory
-                    const int mine = static_cast<int>(blockIdx.x);
-#pragma unroll 1
-                    for (int d = 0; d < DP; d += 64) {
-                        float o[64];
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) o[i] = 0.0f;
-#pragma unroll 1
                         for (int f = f0; f <= f1; ++f) {
-                            const float *x = slot(f) + d * SR;
-                            float y[64];
-                            if (f != mine) {
-#pragma unroll
-                                for (int i = 0; i < 64; ++i) y[i] = __ldcg(x + i * SR);
-                            } else {
-                                sums(d, y);
-                            }
-                            const float g = ex2(reference(f) - ref);
-#pragma unroll
-                            for (int i = 0; i < 64; ++i) o[i] = fmaf(g, y[i], o[i]);
+                            const float mf = reference(f, row), lf = __ldcg(slot(f) + (DP + 1) * SR + row);
+                            const float mn = fmaxf(top, mf), ref = mn == -INFINITY ? 0.0f : mn;
+                            sum = sum * ex2(top - ref) + lf * ex2(mf - ref);
+                            top = mn;
                         }
+                    };
+                    float top, sum;
+                    if (f1 - f0 >= MANY_PARTS) {
+                        // Long chains of parts come with few rows: the threads
+                        // share out a row's dims when there are at most 64 or
+                        // 32 rows, and four parts' loads are in flight.
+                        const int nr = min(SR, k.row1 - (k.row0 + w * SR));
+                        const int rp = nr <= 32 ? 32 : nr <= 64 ? 64 : 128, row = rr & (rp - 1);
+                        const int dims = DP * rp / SR, d0 = rr / rp * dims;  // at least 16
+                        const int gr = k.row0 + w * SR + row, t = a.by_GQ.div(gr);
+                        total(row, top, sum);
+                        const float ref = top == -INFINITY ? 0.0f : top, inv = inverse(sum);
+                        for (int d = d0; row < nr && d < d0 + dims; d += 16) {
+                            float o[16];
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) o[i] *= inv;
-                        put(d, o);
+                            for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+#pragma unroll 1
+                            for (int f = f0; f <= f1; f += 4) {
+                                alignas(16) float y[4][16];
+                                float g[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float4 *x = reinterpret_cast<const float4 *>(slot(min(f + e, f1)) + d * SR) + row;
+                                    g[e] = f + e <= f1 ? reference(f + e, row) : -INFINITY;
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) reinterpret_cast<float4 *>(y[e])[i] = __ldcg(x + i * SR);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float ge = ex2(g[e] - ref);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = fmaf(ge, y[e][i], o[i]);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= inv;
+                            store_dims<F16, 16>(a, k.t0 + t, k.it.head * a.GQ + gr - t * a.GQ, d, o);
+                        }
+                        if (row < nr && d0 == 0) store_lse(a, k.t0 + t, k.it.head * a.GQ + gr - t * a.GQ, top, sum);
+                    } else {
+                        total(rr, top, sum);
+                        const float ref = top == -INFINITY ? 0.0f : top, inv = inverse(sum);
+                        // the CTA's own part is still in tensor memory
+                        const int mine = static_cast<int>(blockIdx.x);
+#pragma unroll 1
+                        for (int d = 0; d < DP; d += 64) {
+                            float o[64];
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) o[i] = 0.0f;
+#pragma unroll 1
+                            for (int f = f0; f <= f1; ++f) {
+                                const float4 *x = reinterpret_cast<const float4 *>(slot(f) + d * SR) + rr;
+                                alignas(16) float y[64];
+                                if (f != mine) {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) reinterpret_cast<float4 *>(y)[i] = __ldcg(x + i * SR);
+                                } else {
+                                    sums(d, y);
+                                }
+                                const float g = ex2(reference(f, rr) - ref);
+#pragma unroll
+                                for (int i = 0; i < 64; ++i) o[i] = fmaf(g, y[i], o[i]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) o[i] *= inv;
+                            put(d, o);
+                        }
+                        if (in) store_lse(a, t_row, h_row, top, sum);
                     }
-                    if (in) store_lse(a, t_row, h_row, top, sum);
                 }
                 __syncwarp();
             }
