@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_cache_plan(const PlanArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool lead = blockIdx.x == 0;
 
-    grid_dep_launch_dependents();
     grid_dep_wait();
+    grid_dep_launch_dependents();
     if (tid < 3) tally[tid] = 0;
     const int64_t avail = max(0, min(*a.free_count, a.free_capacity));
 
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope_append(const RopeArgs a, 
     const int t0 = blockIdx.x * tok, nt = min(tok, a.T - t0);
     const int half = a.rot / 2;
 
-    grid_dep_launch_dependents();
     grid_dep_wait();
+    grid_dep_launch_dependents();
     for (int i = tid; i < nt * half; i += ROPE_THREADS) {
         const int t = i / half;
         // whole turns drop out in 64 bits; what is left fits f32

@@ -96,7 +96,9 @@ cudaError_t rope_append_launch(const RopeArgs &a, bool f16, bool interleaved, cu
 
 // Launch with programmatic stream serialization: the kernel may become
 // resident while the previous one drains, and waits (grid_dep_wait) before it
-// touches memory.
+// touches memory.  It lets its own dependents go only behind that wait, so
+// that whatever they read early (a product its weights) was complete before
+// this kernel began to work.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem,
                              cudaStream_t s, A... args)
