@@ -178,8 +178,10 @@ __device__ __forceinline__ int uniform(int x) { return static_cast<int>(__reduce
 struct Maps {
     CUtensorMap k, v;  // (dim, token, head, block), boxes of 64 x kb x 1 x 1
     CUtensorMap q;     // (dim, query head, row), boxes of 64 x GQ x 128 / GQ
+    CUtensorMap o;     // the same of a 16-bit output, boxes of 64 x GQ x 32 / GQ
     int kb;            // keys per box: the largest power of two up to 128 that divides block_size
     int q_boxes;       // GQ divides 128: queries by tensor copies
+    int o_boxes;       // GQ divides 32: a warp's output rows, when all exist, by one tensor copy
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar)
@@ -198,6 +200,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
         : "memory");
+}
+
+// A warp's output rows to global memory, by one lane.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int c0, int c1, int c2, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 template <bool F16, int DP>
@@ -626,18 +638,27 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                     return;
                 }
                 uint8_t *st = smem + Z::OFF_O + warp * 4096;
-                const int q = lane & 7;
+                const int q = lane & 7, first = k.row0 + w * SR + (warp & 3) * 32;
                 const int64_t o_len = static_cast<int64_t>(a.T - 1) * a.o_stride + static_cast<int64_t>(a.Hq) * a.D;
+                // the last tensor copy has read the staging
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 64; i += 8)
                     *reinterpret_cast<uint4 *>(st + lane * 128 + (((i / 8) ^ (lane & 7)) << 4)) =
                         make_uint4(pack2<F16>(o[i], o[i + 1]), pack2<F16>(o[i + 2], o[i + 3]),
                                    pack2<F16>(o[i + 4], o[i + 5]), pack2<F16>(o[i + 6], o[i + 7]));
+                if (maps.o_boxes && first + 32 <= k.row1) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        tma_store_3d(&maps.o, c, k.it.head * a.GQ, k.t0 + a.by_GQ.div(first), smem_u32(st));
+                    return;
+                }
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int x = i * 4 + lane / 8, gr = k.row0 + w * SR + (warp & 3) * 32 + x;
+                    const int x = i * 4 + lane / 8, gr = first + x;
                     const uint4 y = *reinterpret_cast<const uint4 *>(st + x * 128 + ((q ^ (x & 7)) << 4));
                     const int t = a.by_GQ.div(gr);
                     const int64_t at = (k.t0 + t) * a.o_stride +
@@ -802,6 +823,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
             }
             tc_fence_before();  // this piece's tensor-memory reads end before the next one's products
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -848,6 +871,14 @@ cudaError_t launch(int grid, const AttnArgs &a, cudaStream_t s)
         const int64_t str[3] = {1, a.D, a.q_stride};
         const uint32_t box[3] = {64, static_cast<uint32_t>(a.GQ), static_cast<uint32_t>(SR / a.GQ)};
         ok = encode(&m.q, a.q, F16, 3, ext, str, box);
+    }
+    // debug builds check every store, which a tensor copy's cannot be
+    m.o_boxes = !kDebugBounds && a.ot != Q4_F32 && 32 % a.GQ == 0;
+    if (ok && m.o_boxes) {
+        const uint64_t ext[3] = {u(a.D), u(a.Hq), u(a.T)};
+        const int64_t str[3] = {1, a.D, a.o_stride};
+        const uint32_t box[3] = {64, static_cast<uint32_t>(a.GQ), static_cast<uint32_t>(32 / a.GQ)};
+        ok = encode(&m.o, a.o, F16, 3, ext, str, box);
     }
     if (!ok) return cudaErrorInvalidValue;
     return launch_dependent(kern, dim3(grid), THREADS, Sizes<DP>::SMEM, s, m, a);
