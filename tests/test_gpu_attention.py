@@ -310,3 +310,19 @@ def test_an_empty_batch_writes_nothing():
         run(r, out=out, max_fresh=hint)
         assert (out == 9.0).all()
         assert m.check() == m.OK
+
+
+@pytest.mark.parametrize("step", [0.5, 1.0, 3.0, 7.9, 8.1, 30.0])
+@pytest.mark.parametrize("dtype", DT)
+def test_scores_that_rise_by_tiles(step, dtype):
+    """Every tile of 128 keys scores `step` (in powers of two) above the one
+    before: weights under a stale reference grow to the limits of the type."""
+    r = Requests([(1500, 200), (0, 700)], 4, 2, 64, 16, dtype, seed=19)
+    r.q.fill_(1.0)
+    S = r.k.shape[2]
+    for b, L in enumerate(r.total):
+        for j in range(L):
+            r.k[r.table[b, j // S].item(), :, j % S] = 0.0
+            r.k[r.table[b, j // S].item(), :, j % S, 0] = round(step * (j // 128) * 8) / 8 * 0.6875
+    check(r, scale=1.0)
+    check(r, scale=1.0, window=300)

@@ -220,9 +220,9 @@ __device__ Range find_share(const AttnArgs &a, const LocateScratch &ls, int work
     return r;
 }
 
-// The share of one worker per CTA, by one warp for all; barriers.
+// The share of one worker per CTA, by one warp for all, in ls.r; barriers.
 template <int R, int TK, int NW, int MIN_UNITS, int PAD>
-__device__ Range share(const AttnArgs &a, LocateScratch &ls, int worker, int workers)
+__device__ void share(const AttnArgs &a, LocateScratch &ls, int worker, int workers)
 {
     sum_slabs<R, TK, NW, PAD>(a, ls);
     if (threadIdx.x < 32) {
@@ -230,7 +230,6 @@ __device__ Range share(const AttnArgs &a, LocateScratch &ls, int worker, int wor
         if (threadIdx.x == 0) ls.r = r;
     }
     __syncthreads();
-    return ls.r;
 }
 
 // A worker's pieces of items.

@@ -32,9 +32,8 @@
 // right behind the product that reads the weights they overwrite, and scores
 // being complete implies that every earlier product is.
 //
-// The running maximum is a reference that only moves when a row's maximum
-// passes it by more than 2^8 (weights then stay below 256, well inside
-// binary16): the output is rarely rescaled and the final division removes the
+// The running maximum is a reference that only moves when weights of more than
+// 2^8 show (binary16 holds up to 2^16): the output is rarely rescaled and the final division removes the
 // reference, so the result is the same formula.  Keys that a tile's rows all
 // see need no mask; only tiles on the diagonal or a window's edge do.
 //
@@ -45,12 +44,13 @@
 // tensor memory is freed and the kernel returns.
 //
 // Measured (bf16, 64 query / 8 KV heads of 128): 512 new tokens after 16384 in
-// 190 us, 1.47 PFLOP/s (0.76 of the measured peak; 200 us with inputs from
-// HBM); a prompt of 4096 tokens, 32 heads, f16, in 121 us, 1.13 PFLOP/s; 12
-// requests with 1..160 new tokens after 50..4000 in 84 us.  A unit of 256 rows
-// takes some 3000 cycles, 1550 of them in the tensor pipe: the MMA thread's
-// waits and commits come one after the other with its MMAs, which queue only
-// a few deep.
+// 180 us, 1.55 PFLOP/s (0.81 of the measured peak; 188 us with inputs from
+// HBM); a prompt of 4096 tokens, 32 heads, f16, in 114 us, 1.21 PFLOP/s (118);
+// 12 requests with 1..160 new tokens after 50..4000 in 79 us.  A unit of 256
+// rows takes some 2800 cycles, 1550 of them in the tensor pipe: the MMA
+// thread's waits and commits come one after the other with its MMAs, which
+// queue only a few deep.  The CTA's range stays in shared memory: held in
+// registers it made the softmax warps spill (188 us against 186).
 #include <type_traits>
 
 #include "attention.cuh"
@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
     grid_dep_wait();
     grid_dep_launch_dependents();
     tc_fence_before();
-    const Range rng = share<R, TK, NW, MIN_UNITS, PAD>(a, ls, blockIdx.x, gridDim.x);  // barriers inside
+    share<R, TK, NW, MIN_UNITS, PAD>(a, ls, blockIdx.x, gridDim.x);  // barriers inside
+    const Range &rng = ls.r;  // read where it is: a piece's end is rare, registers are not
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -539,75 +540,109 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 const bool part = key0 + TK - 1 > p.lo || (a.window > 0 && key0 <= p.hi - a.window) || p.lo < 0;
                 const int c1 = place - key0;
                 const int c0 = a.window > 0 && place - a.window + 1 > key0 ? place - a.window + 1 - key0 : 0;
-                uint32_t v[4][32];
+                uint32_t pk[TK / 2];
+                float2 s2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                // The reference seldom moves: weights are taken under the one
+                // there is, and again when their sum shows that one of them may
+                // be above 2^8 (the sum is needed anyway, their maximum is not:
+                // 181 us against 186 for 512 tokens after 16384).  Masked
+                // tiles and an item's first know beforehand.
+                bool again = true;
+                float slack = 8.0f;  // how far the maximum may pass the reference
+                if (!part && !neg && j > p.a) {
+                    const float ref = m == -INFINITY ? 0.0f : m;
+                    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), rf2 = make_float2(-ref, -ref);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32x(ts + c * 32, v[c]);
-                tmem_wait_ld();
-                if (neg) {  // the maximum is taken of scaled scores (hidden ones are -inf, not -inf * 0)
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[2][32];
+                        tmem_ld32x(ts + h * 64, v[0]);
+                        tmem_ld32x(ts + h * 64 + 32, v[1]);
+                        tmem_wait_ld_of(v[0]);
+                        tmem_wait_ld_of(v[1]);
 #pragma unroll
-                    for (int i = 0; i < TK; ++i)
-                        v[i / 32][i % 32] = __float_as_uint(__uint_as_float(v[i / 32][i % 32]) * a.scale_log2);
+                        for (int i = 0; i < 64; i += 2) {
+                            float2 x = make_float2(__uint_as_float(v[i / 32][i % 32]), __uint_as_float(v[i / 32][i % 32 + 1]));
+                            x = fma2(x, sc2, rf2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            s2[(i / 2) & 1] = add2(s2[(i / 2) & 1], x);
+                            pk[h * 32 + i / 2] = pack2<F16>(x.x, x.y);
+                        }
+                    }
+                    const float sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+                    again = __any_sync(0xffffffffu, in && (!(sum <= 256.0f) || m == -INFINITY));
+                    slack = 0.0f;  // many weights above 1 would bring it here each time
                 }
-                if (part) {
-                    constexpr uint32_t HIDDEN = 0xFF800000u;  // -inf
+                if (again) {
+                    uint32_t v[4][32];
+                    s2[0] = s2[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int i = 0; i < TK; ++i)
-                        if (i > c1) v[i / 32][i % 32] = HIDDEN;
-                    if (a.window > 0) {
+                    for (int c = 0; c < 4; ++c) tmem_ld32x(ts + c * 32, v[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_wait_ld_of(v[c]);
+                    if (neg) {  // the maximum is taken of scaled scores (hidden ones are -inf, not -inf * 0)
 #pragma unroll
                         for (int i = 0; i < TK; ++i)
-                            if (i < c0) v[i / 32][i % 32] = HIDDEN;
+                            v[i / 32][i % 32] = __float_as_uint(__uint_as_float(v[i / 32][i % 32]) * a.scale_log2);
                     }
-                }
-                const float sc = neg ? 1.0f : a.scale_log2;
-                float m4[4];
+                    if (part) {
+                        constexpr uint32_t HIDDEN = 0xFF800000u;  // -inf
 #pragma unroll
-                for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(v[c][0]);
+                        for (int i = 0; i < TK; ++i)
+                            if (i > c1) v[i / 32][i % 32] = HIDDEN;
+                        if (a.window > 0) {
 #pragma unroll
-                for (int i = 1; i < 31; i += 2)
+                            for (int i = 0; i < TK; ++i)
+                                if (i < c0) v[i / 32][i % 32] = HIDDEN;
+                        }
+                    }
+                    const float sc = neg ? 1.0f : a.scale_log2;
+                    float m4[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
+                    for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(v[c][0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(v[c][31]));
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
-                bool move = false;
-                float f = 1.0f;
-                if (m == -INFINITY) {
-                    m = mx;
-                } else if (mx > m + 8.0f) {
-                    f = ex2(m - mx);
-                    m = mx;
-                    l *= f;
-                    move = true;
-                }
-                if (__any_sync(0xffffffffu, move) && j > p.a) {
+                    for (int i = 1; i < 31; i += 2)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(v[c][31]));
+                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+                    float f = 1.0f;
+                    if (mx > m + slack) {
+                        f = m == -INFINITY ? 1.0f : ex2(m - mx);  // nothing is summed under -inf
+                        m = mx;
+                        l *= f;
+                    }
+                    if (j > p.a && __any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-                    for (int c = 0; c < DP; c += 16) {
-                        uint32_t x[16];
-                        tmem_ld16x(to + c, x);
-                        tmem_wait_ld();
+                        for (int c = 0; c < DP; c += 16) {
+                            uint32_t x[16];
+                            tmem_ld16x(to + c, x);
+                            tmem_wait_ld_of(x);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                        tmem_st16(to + c, x);
+                            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                            tmem_st16(to + c, x);
+                        }
                     }
-                }
-                const float ref = m == -INFINITY ? 0.0f : m;
-                const float2 sc2 = make_float2(sc, sc), rf2 = make_float2(-ref, -ref);
-                float2 s2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    const float ref = m == -INFINITY ? 0.0f : m;
+                    const float2 sc2 = make_float2(sc, sc), rf2 = make_float2(-ref, -ref);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float2 x = make_float2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+                    for (int i = 0; i < TK; i += 2) {
+                        float2 x = make_float2(__uint_as_float(v[i / 32][i % 32]), __uint_as_float(v[i / 32][i % 32 + 1]));
                         x = fma2(x, sc2, rf2);
                         x.x = ex2(x.x);
                         x.y = ex2(x.y);
                         s2[(i / 2) & 1] = add2(s2[(i / 2) & 1], x);
                         pk[i / 2] = pack2<F16>(x.x, x.y);
                     }
-                    tmem_st16(ts + c * 16, pk);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = pk[c * 32 + i];
+                    tmem_st32(ts + c * 32, x);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -674,7 +709,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 if (any) {
                     tmem_ld32x(to + c, v[0]);
                     tmem_ld32x(to + c + 32, v[1]);
-                    tmem_wait_ld();
+                    tmem_wait_ld_of(v[0]);
+                    tmem_wait_ld_of(v[1]);
                 }
 #pragma unroll
                 for (int i = 0; i < 64; ++i) o[i] = __uint_as_float(v[i / 32][i % 32]);

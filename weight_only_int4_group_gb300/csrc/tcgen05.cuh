@@ -193,6 +193,22 @@ __device__ __forceinline__ void tmem_ld32x(uint32_t taddr, uint32_t (&v)[32])
         : "r"(taddr)
         : "memory");
 }
+// Waits for this warp's tensor-memory loads; tied to the registers they fill,
+// so that no use of v can be moved before it.
+#define Q4_RW8(a, o) "+r"(a[o + 0]), "+r"(a[o + 1]), "+r"(a[o + 2]), "+r"(a[o + 3]), \
+    "+r"(a[o + 4]), "+r"(a[o + 5]), "+r"(a[o + 6]), "+r"(a[o + 7])
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : Q4_RW8(v, 0), Q4_RW8(v, 8) : : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : Q4_RW8(v, 0), Q4_RW8(v, 8), Q4_RW8(v, 16), Q4_RW8(v, 24)
+                 :
+                 : "memory");
+}
+#undef Q4_RW8
 #undef Q4_R8
 #undef Q4_W8
 
