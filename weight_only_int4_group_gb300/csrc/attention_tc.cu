@@ -33,9 +33,10 @@
 // being complete implies that every earlier product is.
 //
 // The running maximum is a reference that only moves when weights of more than
-// 2^8 show (binary16 holds up to 2^16): the output is rarely rescaled and the final division removes the
-// reference, so the result is the same formula.  Keys that a tile's rows all
-// see need no mask; only tiles on the diagonal or a window's edge do.
+// 2^8 show (binary16 holds up to 2^16): the output is rarely rescaled and the
+// final division removes the reference, so the result is the same formula.
+// Keys that a tile's rows all see need no mask; only tiles on the diagonal or
+// a window's edge do.
 //
 // Items cut by a range boundary leave their unscaled outputs, references and
 // sums in the workspace; the subtile's last CTA to arrive adds them in CTA
