@@ -326,3 +326,22 @@ def test_scores_that_rise_by_tiles(step, dtype):
             r.k[r.table[b, j // S].item(), :, j % S, 0] = round(step * (j // 128) * 8) / 8 * 0.6875
     check(r, scale=1.0)
     check(r, scale=1.0, window=300)
+
+
+@pytest.mark.parametrize("lengths", [[(3000, 1)], [(12000, 2)], [(700, 1), (5000, 1), (90, 2)]], ids=str)
+def test_joins_add_this_calls_parts(lengths):
+    """Call after call through one workspace, each with other queries: a join
+    that took a part of the call before, or one not yet there, would show."""
+    m = q4()
+    r = Requests(lengths, 8, 1, 64, 16, torch.bfloat16, seed=21)
+    cache, ws = m.KVCache(r.k, r.v), m.attention_workspace(r.max_fresh, 8, 1, 64)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    qs = [torch.randn(r.q.shape, generator=g, device="cuda").bfloat16() for _ in range(40)]
+    outs = [m.attention(q, cache, r.table, r.q_start, r.kv_len, r.max_fresh, ws=ws) for q in qs]
+    assert m.check() == m.OK
+    for i in (0, 1, 20, 39):
+        r.q = qs[i]
+        assert_attention(outs[i], None, r.reference(), f"call {i}")
+    for q, o in zip(qs, outs):
+        alone = m.attention(q, cache, r.table, r.q_start, r.kv_len, r.max_fresh, ws=ws)
+        assert m.check() == m.OK and torch.equal(alone, o)

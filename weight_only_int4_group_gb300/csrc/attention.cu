@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
                     if (last) *c = 0u;
                 }
                 if (!__shfl_sync(0xffffffffu, last, 0)) break;
+                __syncwarp();  // lane 0's acquire holds for the other lanes' reads too: a shuffle orders no memory
                 m[0] = m[1] = -INFINITY;
                 l[0] = l[1] = 0.0f;
 #pragma unroll
