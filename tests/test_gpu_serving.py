@@ -12,7 +12,7 @@ import sys
 import pytest
 import torch
 
-from serving_ref import Requests, attention_reference, rope_reference
+from serving_ref import Requests, assert_attention, attention_reference, rope_reference
 from test_gpu_canaries import DEBUG_LIB, UNDER_DEBUG, Guarded
 
 pytestmark = pytest.mark.gpu
@@ -86,6 +86,55 @@ def test_example_runs():
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
     assert "lengths [703, 36, 4, 259]" in r.stdout
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_attention_right_behind_its_plan(many):
+    """Nothing between the plan and the attention that reads its lengths and
+    table; the lengths change from step to step, in a graph."""
+    m = q4()
+    B, heads, kv, D, S, W = 40, 8, 2, 64, 16, 8
+    n = 9 if many else 2
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(31)
+    k, v = (torch.randn((B * W, kv, S, D), generator=g, device="cuda").half() for _ in range(2))
+    cache, ws = m.KVCache(k, v), m.attention_workspace(n, heads, kv, D)
+    cached, fresh = torch.zeros(B, **i32), torch.zeros(B, **i32)
+    table, count = torch.full((B, W), -1, **i32), torch.full((1,), B * W, **i32)
+    free = torch.randperm(B * W, generator=g, device="cuda").int()
+    T = B * n
+    q = torch.randn((T, heads, D), generator=g, device="cuda").half()
+    plan, o = m.CachePlan.empty(B, T), torch.empty_like(q)
+
+    def step():
+        m.cache_plan(cached, fresh, table, free, count, S, T, out=plan)
+        m.attention(q, cache, table, plan.q_start, plan.kv_len, n, out=o, ws=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(12):
+        cached.copy_(torch.randint(0, W * S - n, (B,), generator=g, device="cuda"))
+        fresh.copy_(torch.randint(0, n + 1, (B,), generator=g, device="cuda"))
+        # the blocks that the requests hold, and the pool of the others
+        held = ((cached + S - 1) // S).tolist()
+        pool, at = torch.randperm(B * W, generator=g, device="cuda").int(), 0
+        table.fill_(-1)
+        for b, h in enumerate(held):
+            table[b, :h] = pool[at:at + h]
+            at += h
+        free[:B * W - at] = pool[at:]
+        count.fill_(B * W - at)
+        torch.cuda.synchronize()
+        graph.replay()
+        assert m.check() == m.OK
+        start, total = plan.q_start.tolist(), plan.kv_len.tolist()
+        assert total == (cached + fresh).tolist()
+        ref = attention_reference(q, k, v, table, start, total, D ** -0.5, 0)
+        used = start[-1]
+        assert_attention(o[:used], None, [t[:used] for t in ref], f"step {i}")
 
 
 # ------------------------------------------------------------------ guards

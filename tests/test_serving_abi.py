@@ -2,6 +2,7 @@
 host, before any CUDA call (CPU only; the pointers are never dereferenced)."""
 import ctypes
 import os
+import re
 import subprocess
 import sys
 
@@ -153,3 +154,13 @@ def test_debug_library_exports_the_same(lib):
         pytest.skip("the bounds-checked build is not there")
     code = f"import ctypes; l = ctypes.CDLL({other!r}); l.q4_cache_plan; l.q4_rope_append; l.q4_attention"
     subprocess.run([sys.executable, "-c", code], check=True)
+
+
+@pytest.mark.parametrize("source", ["serve.cuh", "attention.cuh", "attention.cu", "attention_tc.cu", "cache.cu"])
+def test_kernels_that_start_early_load_coherently(source):
+    """They are resident while the kernel that writes their inputs may still
+    run: no load of the non-coherent path, which asks for data that nothing
+    writes as long as the kernel lives."""
+    text = open(os.path.join(ROOT, "weight_only_int4_group_gb300", "csrc", source)).read()
+    code = re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+    assert not re.search(r"__ldg\b|ld\.global\.nc|__restrict__", code)

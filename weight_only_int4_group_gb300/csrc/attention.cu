@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
     int ld_i = 0, ld_slot = 0;  // unit of ld, ring slot
     auto block_of = [&]() {  // table entry of the unit to load
         const int key = (ld.kt0 + ld.kt + ld_i) * TK;
-        return ld.more(rng) && key < ld.kv ? __ldg(a.table + ld.it.b * a.table_stride + a.by_S.div(key)) : -1;
+        return ld.more(rng) && key < ld.kv ? a.table[ld.it.b * a.table_stride + a.by_S.div(key)] : -1;
     };
     int blk = block_of();
     auto issue = [&]() {

@@ -9,12 +9,14 @@ namespace q4 {
 
 // A request's new tokens and length as the kernels use them: cut to the token
 // rows and to the table's width, so that no index leaves its buffer whatever
-// the device arrays hold.
+// the device arrays hold.  Plain loads, here and of the table: this kernel is
+// resident while the one that wrote them may still run, and the non-coherent
+// path asks for data that nothing writes as long as a kernel lives.
 __device__ __forceinline__ void request(const AttnArgs &a, int b, int &t0, int &n, int &kv)
 {
-    t0 = min(max(__ldg(a.q_start + b), 0), a.T);
-    n = max(0, min(max(__ldg(a.q_start + b + 1), 0), a.T) - t0);
-    kv = static_cast<int>(min(static_cast<int64_t>(max(__ldg(a.kv_len + b), 0)),
+    t0 = min(max(a.q_start[b], 0), a.T);
+    n = max(0, min(max(a.q_start[b + 1], 0), a.T) - t0);
+    kv = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)),
                               static_cast<int64_t>(a.width) * a.S));
 }
 

@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         int g = 0;  // units loaded
         for (; ok && k.more(rng) && !a.debug_no_copy; k.next(a, rng)) {
             const int *trow = a.table + k.it.b * a.table_stride;
-            auto block_of = [&](int key) { return key < k.kv ? __ldg(trow + a.by_S.div(key)) : -1; };
+            auto block_of = [&](int key) { return key < k.kv ? trow[a.by_S.div(key)] : -1; };
             const int first = (k.kt0 + k.kt) * TK;
             int blk = boxed ? block_of(first + bk) : -1;
             for (int j = 0; j < k.nu; ++j, ++g) {
