@@ -428,10 +428,11 @@ q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t
  *     o = sum_j exp(s_j - lse) v_j,  s_j = scale * q . k_j,  lse = log sum_j exp(s_j)
  * with f32 sums.  Query head h reads KV head h / (Hq / heads).  A row that
  * sees no key (p < 0) gets o = 0 and lse = -inf.  The request's last keys
- * are its new ones: append first.  Only keys j < kv_len[b] are read; what
- * lies behind them in a block never matters, NaN included.  (A NaN or
- * infinity in a key or value that some row of the request does see may
- * reach its other rows too.)
+ * are its new ones: append first.  What no row of the request sees never
+ * matters, NaN included: keys and values behind kv_len[b] in a block, and
+ * those before every row's window, whose blocks may serve other requests by
+ * then.  (A NaN or infinity in a key or value that some row of the request
+ * does see may reach its other rows too.)
  * q, o: T rows of Hq * head_dim elements (strides q_stride, o_stride), q of
  * the cache's type, o of type ot (the cache's type or F32); rows that belong
  * to no request are left alone.  lse: f32 [T][Hq] or NULL.

@@ -345,3 +345,26 @@ def test_joins_add_this_calls_parts(lengths):
     for q, o in zip(qs, outs):
         alone = m.attention(q, cache, r.table, r.q_start, r.kv_len, r.max_fresh, ws=ws)
         assert m.check() == m.OK and torch.equal(alone, o)
+
+
+@pytest.mark.parametrize("recycled", [False, True])
+@pytest.mark.parametrize("window", [1, 5, 16, 33, 100, 128, 200, 1000])
+@pytest.mark.parametrize("lengths", [[(500, 1), (20, 3), (1300, 1)], [(500, 140), (90, 33), (0, 400)], [(3000, 20)]],
+                         ids=["few", "many", "split"])
+def test_nothing_before_a_window_reaches_the_output(lengths, window, recycled):
+    """Keys and values that have left every row's window are NaN; ``recycled``:
+    the blocks that hold nothing else are other requests' or gone."""
+    for dtype, hint in ((torch.bfloat16, None), (torch.float16, 1), (torch.float16, 1000)):
+        r = Requests(lengths, 8, 2, 64 if hint else 128, 16, dtype, seed=20)
+        ref = r.reference(window=window)
+        S = r.k.shape[2]
+        for b, (cached, _) in enumerate(lengths):
+            out = max(0, cached - window + 1)  # keys that no row sees any more
+            for j in range(-(-out // S)):
+                blk, m = r.table[b, j].item(), min(S, out - j * S)
+                r.k[blk, :, :m] = math.nan
+                r.v[blk, :, :m] = math.nan
+                if recycled and m == S:
+                    r.table[b, j] = (-1, 2 ** 31 - 1, r.table[b, 0].item())[j % 3]
+        o, lse = run(r, window, max_fresh=hint)
+        assert_attention(o, lse, ref, f"{lengths} window {window}")

@@ -14,9 +14,10 @@
 // lengths on the device (no host plan, no second launch), and shares nothing
 // with its neighbours, so that one that finishes an item does not hold up the
 // others' loads.  Each warp has a ring of STAGES units in shared memory filled
-// by cp.async (16 bytes per lane; keys past the request's end, blocks outside
-// the cache and the padding of head_dim are filled with zeros, so nothing
-// stale is ever multiplied); the loads run ahead through the ends of items.
+// by cp.async (16 bytes per lane; keys past the request's end or before every
+// row's window, blocks outside the cache and the padding of head_dim are
+// filled with zeros, so nothing stale is ever multiplied); the loads run ahead
+// through the ends of items.
 // An item cut by range boundaries leaves its pieces in the workspace, in the
 // lanes' own order; the last warp to arrive adds them (eight at a time, in a
 // tree, when there are many), always in sequence order, so results do not
@@ -176,10 +177,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
                                   ld.it.head * a.head_stride + c * 8
                             : 0;
             const int rows = in && c * 8 < a.D ? ld.kv - key : 0;  // keys that exist
+            // and those that the window leaves to some row
+            const int row0 = a.window > 0 && ld.kt + ld_i == 0 ? ld.first_key(a) - key : 0;
 #pragma unroll
             for (int l = 0; l < LPT; ++l) {
                 const int row = l * RPI + hi;
-                const bool ok = row < rows;
+                const bool ok = row >= row0 && row < rows;
                 const uint32_t d = dst + row * Z::ROW + ((c ^ (row & 7)) << 4);
                 cp_async16(d, a.k + (ok ? at : 0), ok);
                 cp_async16(d + Z::TILE, a.v + (ok ? at : 0), ok);

@@ -25,6 +25,14 @@ __device__ __forceinline__ int row_tiles(int n, int GQ, int R)
     return static_cast<int>((static_cast<int64_t>(n) * GQ + R - 1) / R);
 }
 
+// The first key that the window leaves to the row in place p (and with it to
+// the rows behind it).
+__device__ __forceinline__ int window_start(const AttnArgs &a, int p)
+{
+    const int64_t first = static_cast<int64_t>(p) - a.window + 1;
+    return a.window > 0 && first > 0 ? static_cast<int>(first) : 0;
+}
+
 // Rows [row0, row1) of a request's n * GQ rows and the units of TK keys they
 // see: units [kt0, kt0 + units) of the request's keys; one (all masked) when
 // they see none, so that their empty results are written.
@@ -50,8 +58,7 @@ private:
         row1 = static_cast<int>(min(static_cast<int64_t>(n) * a.GQ, static_cast<int64_t>(row0) + R));
         const int lo_t = a.by_GQ.div(row0), hi_t = a.by_GQ.div(row1 - 1);
         const int hi = base + hi_t + 1;
-        const int64_t first = static_cast<int64_t>(base) + lo_t - a.window + 1;
-        const int lo = a.window > 0 && first > 0 ? static_cast<int>(first) : 0;
+        const int lo = window_start(a, base + lo_t);
         kt0 = lo / TK;
         units = hi > lo ? (hi - 1) / TK - kt0 + 1 : 1;
     }
@@ -301,6 +308,12 @@ private:
     }
 
 public:
+    // The first key that any of the piece's rows sees; only the item's first
+    // unit can hold keys before it.
+    __device__ __forceinline__ int first_key(const AttnArgs &a) const
+    {
+        return window_start(a, base + a.by_GQ.div(row0));
+    }
     // First and last worker that hold units of the item.
     __device__ __forceinline__ void holders(const Range &r, int &first, int &last) const
     {

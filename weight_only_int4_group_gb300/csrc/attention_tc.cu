@@ -19,10 +19,11 @@
 //                   keys that lies in one block of the cache for certain (16
 //                   keys at least) and 64 dims, each lane issuing one; two
 //                   slots of 32 KB each for keys and values.  Only the value
-//                   tile that holds the request's end goes by cp.async, which
-//                   puts zeros behind it (0 times a stale NaN would reach the
-//                   sums; stale keys only make scores that are masked), and
-//                   queries whose group of heads does not divide 128;
+//                   tiles that hold the request's end or the window's
+//                   beginning go by cp.async, which puts zeros outside (0
+//                   times a stale NaN would reach the sums; stale keys only
+//                   make scores that are masked), and queries whose group of
+//                   heads does not divide 128;
 //   warp 11         allocates tensor memory; one thread issues the MMAs.
 // Tensor memory (512 columns): the two subtiles' scores (128 columns each)
 // and outputs (head_dim each).  While one subtile's softmax runs, the other's
@@ -108,8 +109,7 @@ __device__ __forceinline__ Seen seen(const AttnArgs &a, const Pieces &k, int w)
     s.lo = k.base + a.by_GQ.div(r0);
     s.hi = k.base + a.by_GQ.div(r1 - 1);
     if (s.hi < 0) return s;
-    const int64_t first = static_cast<int64_t>(s.lo) - a.window + 1;
-    const int u0 = (a.window > 0 && first > 0 ? static_cast<int>(first) : 0) / TK - k.kt0 - k.kt;
+    const int u0 = window_start(a, s.lo) / TK - k.kt0 - k.kt;
     const int u1 = s.hi / TK + 1 - k.kt0 - k.kt;
     s.a = min(max(u0, 0), k.nu);
     s.b = max(s.a, min(u1, k.nu));
@@ -298,12 +298,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
             const int *trow = a.table + k.it.b * a.table_stride;
             auto block_of = [&](int key) { return key < k.kv ? trow[a.by_S.div(key)] : -1; };
             const int first = (k.kt0 + k.kt) * TK;
+            const int lo = a.window > 0 ? k.first_key(a) : 0;
             int blk = boxed ? block_of(first + bk) : -1;
             for (int j = 0; j < k.nu; ++j, ++g) {
                 const int s = g & 1, key0 = first + j * TK;
                 if (g >= 2 && !(ok = warp_wait(&empty[s], ((g >> 1) - 1) & 1))) break;
                 const uint32_t dst = ring + s * Z::TILE;
-                if (!vals || key0 + TK <= k.kv) {
+                if (!vals || (key0 + TK <= k.kv && key0 >= lo)) {
                     if (boxed) {
                         // a block outside the cache reads as zeros
                         mbar_arrive_expect_tx(&full[s], maps.kb * 128);
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                     }
                     __syncwarp();
                 } else {
+                    if (boxed) blk = j + 1 < k.nu ? block_of(key0 + TK + bk) : -1;
                     // groups of 16 keys, each within one block of the cache
                     constexpr int RPI = 32 / C8;
                     const int c = lane % C8, hi = lane / C8;
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
 #pragma unroll
                         for (int l = 0; l < 16 / RPI; ++l) {
                             const int row = l * RPI + hi;
-                            const bool ok16 = in && key + row < k.kv && c * 8 < a.D;
+                            const bool ok16 = in && key + row < k.kv && key + row >= lo && c * 8 < a.D;
                             cp_async16(dc + (r0 + l * RPI) * 128 + (((c & 7) ^ (row & 7)) << 4),
                                        ok16 ? base + row * a.token_stride : vh, ok16);
                         }
