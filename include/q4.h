@@ -426,7 +426,12 @@ q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t
  * at place p = kv_len[b] - n + i and sees the keys j <= p (j > p - window
  * too, when window > 0) of the request:
  *     o = sum_j exp(s_j - lse) v_j,  s_j = scale * q . k_j,  lse = log sum_j exp(s_j)
- * with f32 sums.  Query head h reads KV head h / (Hq / heads).  A row that
+ * Products are summed in f32 by the tensor cores; the weights exp(s_j - max)
+ * are rounded to the cache's type for the second product (relative 2^-9 bf16,
+ * 2^-12 binary16, or 2^-32 of the largest where binary16 ends), also with f32
+ * output, and their sum is f32 of the unrounded ones.  As in any f32 sum, terms
+ * under 2^-24 of what is summed already add nothing.
+ * Query head h reads KV head h / (Hq / heads).  A row that
  * sees no key (p < 0) gets o = 0 and lse = -inf.  The request's last keys
  * are its new ones: append first.  What no row of the request sees never
  * matters, NaN included: keys and values behind kv_len[b] in a block, and

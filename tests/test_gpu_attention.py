@@ -368,3 +368,38 @@ def test_nothing_before_a_window_reaches_the_output(lengths, window, recycled):
                     r.table[b, j] = (-1, 2 ** 31 - 1, r.table[b, 0].item())[j % 3]
         o, lse = run(r, window, max_fresh=hint)
         assert_attention(o, lse, ref, f"{lengths} window {window}")
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("dtype", DT)
+def test_many_small_weights_beside_a_large_one(dtype, many):
+    """65536 keys of weight e^-17.5 (2^-25.2) and value 1 beside one of weight 1
+    and value 0: the output is the small ones' share, 0.0016, and nothing if
+    their weights round to nothing.  Allowed: each weight off by u of itself,
+    or in binary16 by half its smallest number, 2^-25, under a reference of
+    2^7 at least; f32 sums of 4096 steps, each off by 2^-24 of the row's sum
+    (near 1 throughout) and 2^-23 of the output's, 2^-10 in all."""
+    m = q4()
+    S, L, D = 64, 65537, 64
+    B, heads, n = (160, 8, 32) if many else (1300, 1, 1)
+    blocks = -(-L // S)
+    k = torch.zeros((blocks, 1, S, D), dtype=dtype, device="cuda")
+    v = torch.ones_like(k)
+    k[0, 0, 0, 0], v[0, 0, 0] = 17.5, 0.0
+    q = torch.zeros((B * n, heads, D), dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    i32 = dict(dtype=torch.int32, device="cuda")
+    # every request reads the same blocks
+    table = torch.arange(blocks, **i32).expand(B, blocks).contiguous()
+    start, kv = torch.arange(B + 1, **i32) * n, torch.full((B,), L, **i32)
+    o, lse = m.attention(q, m.KVCache(k, v), table, start, kv, n, scale=1.0, out_dtype=torch.float32, return_lse=True)
+    assert m.check() == m.OK
+    seen = (L - n + torch.arange(n, device="cuda", dtype=torch.float64)).view(1, n, 1)
+    small = seen * math.exp(-17.5)
+    exact = (small / (1 + small))[..., None]
+    u = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -11
+    allow = (u + 2.0 ** -10) * exact + (L * 2.0 ** -32 if dtype == torch.float16 else 0.0)
+    err = (o.view(B, n, heads, D).double() - exact).abs()
+    assert (err <= allow).all(), float((err / exact).max())
+    err = (lse.view(B, n, heads).double() - 17.5 - torch.log1p(small)).abs()
+    assert (err <= 2.0 ** -12 + 36 * 2.0 ** -18).all(), float(err.max())

@@ -42,6 +42,13 @@ constexpr int THREADS = NW * 32;
 // least that a warp gets (one request of 777 keys: 14.1 us by 4 and 14.7 by 8;
 // 16 with drafted tokens: 16.3 and 18.0).
 constexpr int PAD = 4, MIN_UNITS = 4;
+// Weights are taken under a reference this many powers of two below the row's
+// maximum: they are rounded to the cache's type for the second product, and
+// binary16 ends at 2^16 and 2^-25 (under the maximum itself, 65536 keys of
+// weight 2^-25 beside a large one would vanish from the output while their
+// row's sum counts them).  bf16 has the exponents of f32.
+template <bool F16>
+constexpr float LIFT = F16 ? 15.0f : 0.0f;
 // Parts that are added at a time where an item is split (4 levels hold 4096
 // workers, the most there are).
 constexpr int MERGE = 8, LEVELS = 4, MOST_CTAS = 256;
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
                 f[j] = ex2(m[j] - ref);
                 m[j] = mn;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = ex2(v[e] - ref);
+                for (int e = 0; e < 4; ++e) v[e] = ex2((v[e] - ref) + LIFT<F16>);  // no rounding of a large ref
                 l[j] = l[j] * f[j] + ((v[0] + v[1]) + (v[2] + v[3]));
                 // A fragment of the second product: keys are its k
                 p[j] = pack2<F16>(v[0], v[1]);
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_stream(const AttnArgs a)
                     else
                         *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.o) + at + n * 8) = pack2<F16>(x, y);
                 }
-                if ((lane & 3) == 0) store_lse(a, trow[j], hrow[j], m[j], l[j]);
+                if ((lane & 3) == 0) store_lse(a, trow[j], hrow[j], m[j] - LIFT<F16>, l[j]);
             }
         }
         __syncwarp();

@@ -33,9 +33,12 @@
 // right behind the product that reads the weights they overwrite, and scores
 // being complete implies that every earlier product is.
 //
-// The running maximum is a reference that only moves when weights of more than
-// 2^8 show (binary16 holds up to 2^16): the output is rarely rescaled and the
-// final division removes the reference, so the result is the same formula.
+// The weights' reference follows the running maximum, but only moves when it
+// is passed by more than 2^8: the output is rarely rescaled and the final
+// division removes the reference, so the result is the same formula.  In
+// binary16, which ends at 2^16 and 2^-25, the reference lies 2^7 below the
+// maximum, so that weights reach 2^15 and many small ones beside a large one
+// do not vanish.
 // Keys that a tile's rows all see need no mask; only tiles on the diagonal or
 // a window's edge do.
 //
@@ -76,6 +79,18 @@ constexpr int MANY_PARTS = 3;  // more parts behind the first are added four at 
 // which keep a row's 128 scores in registers.
 constexpr int REG_HI = 208, REG_LO = 80;
 static_assert(2 * REG_HI + REG_LO <= 3 * 168, "within the registers of the launch");
+
+// Powers of two that a weight's reference lies below the maximum it follows,
+// and that the maximum may pass it by before it moves.
+template <bool F16>
+constexpr float LIFT = F16 ? 7.0f : 0.0f;
+constexpr float SLACK = 8.0f;
+// Scores from here on leave f32 no exact place for the lift: their maximum is
+// the reference itself.
+constexpr float LARGE = 1048576.0f;
+// A tile's sum of weights below which none of them is past the slack.
+template <bool F16>
+constexpr float MOST_SUM = F16 ? 32768.0f : 256.0f;
 
 template <int DP>
 struct Sizes {
@@ -547,11 +562,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 float2 s2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 // The reference seldom moves: weights are taken under the one
                 // there is, and again when their sum shows that one of them may
-                // be above 2^8 (the sum is needed anyway, their maximum is not:
-                // 181 us against 186 for 512 tokens after 16384).  Masked
+                // be past the slack (the sum is needed anyway, their maximum is
+                // not: 181 us against 186 for 512 tokens after 16384).  Masked
                 // tiles and an item's first know beforehand.
                 bool again = true;
-                float slack = 8.0f;  // how far the maximum may pass the reference
+                float slack = SLACK;
                 if (!part && !neg && j > p.a) {
                     const float ref = m == -INFINITY ? 0.0f : m;
                     const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), rf2 = make_float2(-ref, -ref);
@@ -573,7 +588,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                         }
                     }
                     const float sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-                    again = __any_sync(0xffffffffu, in && (!(sum <= 256.0f) || m == -INFINITY));
+                    again = __any_sync(0xffffffffu, in && (!(sum <= MOST_SUM<F16>) || m == -INFINITY));
                     slack = 0.0f;  // many weights above 1 would bring it here each time
                 }
                 if (again) {
@@ -611,10 +626,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
 #pragma unroll
                     for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(v[c][31]));
                     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+                    const float mr = fabsf(mx) < LARGE ? mx - LIFT<F16> : mx;
                     float f = 1.0f;
-                    if (mx > m + slack) {
-                        f = m == -INFINITY ? 1.0f : ex2(m - mx);  // nothing is summed under -inf
-                        m = mx;
+                    if (mr > m + slack) {
+                        f = m == -INFINITY ? 1.0f : ex2(m - mr);  // nothing is summed under -inf
+                        m = mr;
                         l *= f;
                     }
                     if (j > p.a && __any_sync(0xffffffffu, f != 1.0f)) {
