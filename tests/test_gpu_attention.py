@@ -403,3 +403,45 @@ def test_many_small_weights_beside_a_large_one(dtype, many):
     assert (err <= allow).all(), float((err / exact).max())
     err = (lse.view(B, n, heads).double() - 17.5 - torch.log1p(small)).abs()
     assert (err <= 2.0 ** -12 + 36 * 2.0 ** -18).all(), float(err.max())
+
+
+@pytest.mark.parametrize("top", [2.0 ** 12, 2.0 ** 20, 2.0 ** 24, 2.0 ** 28, 2.0 ** 32])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("dtype", DT)
+def test_large_scores_pick_their_key(dtype, many, top):
+    """Scores up to `top`, each a power of two away from the next: the largest
+    one a row sees takes all, its value comes out (one weight, rounded once)."""
+    n = 200 if many else 2
+    r = Requests([(300, n), (0, n)], 4, 2, 64, 16, dtype, seed=23)
+    g = torch.Generator().manual_seed(24)
+    S = r.k.shape[2]
+    r.q.zero_()
+    r.q[..., 0] = 2.0 ** 15
+    for sign in (1.0, -1.0):
+        for b, L in enumerate(r.total):
+            # 2^15 * key: top * (1 - i / 64), in any order; every 64th key is as large as another
+            level = torch.arange(L)[torch.randperm(L, generator=g)] % 64
+            for j in range(L):
+                row = r.k[r.table[b, j // S].item(), :, j % S]
+                row.zero_()
+                row[:, 0] = sign * (1.0 - level[j].item() / 64) * 2.0
+        scale = top / 2.0 ** 16
+        o, lse = run(r, scale=scale, out_dtype=torch.float32)
+        for b, L in enumerate(r.total):
+            t0, t1 = r.start[b], r.start[b + 1]
+            ids = r.table[b, :-(-L // S)].long()
+            for c in range(2):
+                k = r.k[ids, c].reshape(-1, 64)[:L, 0].double()
+                v = r.v[ids, c].reshape(-1, 64)[:L].double()
+                s = (2.0 ** 15 * scale) * k.expand(t1 - t0, L)
+                place = torch.arange(L - (t1 - t0), L, device="cuda")[:, None]
+                s = torch.where(torch.arange(L, device="cuda") <= place, s, -math.inf)
+                best = (s == s.amax(1, keepdim=True)).double()  # the next one is e^-64 away at least
+                want = best @ v / best.sum(1, keepdim=True)
+                size = best @ v.abs() / best.sum(1, keepdim=True)
+                u = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -11
+                for h in (2 * c, 2 * c + 1):
+                    err = (o[t0:t1, h].double() - want).abs()
+                    assert (err <= (u + 2.0 ** -16) * size).all(), (sign, b, float(err.max()))
+                    exact = s.amax(1) + torch.log(best.sum(1))
+                    assert ((lse[t0:t1, h].double() - exact).abs() <= 2.0 ** -22 * (1 + exact.abs())).all()

@@ -85,9 +85,13 @@ static_assert(2 * REG_HI + REG_LO <= 3 * 168, "within the registers of the launc
 template <bool F16>
 constexpr float LIFT = F16 ? 7.0f : 0.0f;
 constexpr float SLACK = 8.0f;
-// Scores from here on leave f32 no exact place for the lift: their maximum is
-// the reference itself.
-constexpr float LARGE = 1048576.0f;
+// f32 rounds a row's largest score, as the reference, by up to 2^-24 of it, and
+// the fused multiply-adds of the weights bring that back as a factor on all of
+// them, which would leave the range of the types.  So for their weights a row's
+// scores are scaled to this size (2^24) at most: larger ones that still come
+// close differ by a few of f32's own steps.  (Scores taken from the reference
+// before they are scaled need no such bound; prompts took 2% longer.)
+constexpr float LARGE = 16777216.0f;
 // A tile's sum of weights below which none of them is past the slack.
 template <bool F16>
 constexpr float MOST_SUM = F16 ? 32768.0f : 256.0f;
@@ -538,6 +542,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field: 32 * (warp % 4) << 16
         const uint32_t ts = tmem + lanes + Z::S_COL + w * 128, to = tmem + lanes + Z::O_COL + w * DP;
         const bool neg = a.scale_log2 <= 0.0f;
+        const float sc = neg ? 1.0f : a.scale_log2;  // what is left to scale behind the maximum
         uint32_t ns = 0, no = 0;
         Seen p;
         int r, place;
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 in = r < k.row1;
                 place = in ? k.base + a.by_GQ.div(r) : -1;
             }
-            float m = -INFINITY, l = 0.0f;
+            float peak = -INFINITY, l = 0.0f;  // the score that the reference follows
             for (int j = p.a; ok && j < p.b; ++j, ++ns) {
                 if (!(ok = warp_wait(&sfull[w], ns & 1))) break;
                 tc_fence_after();
@@ -568,8 +573,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 bool again = true;
                 float slack = SLACK;
                 if (!part && !neg && j > p.a) {
-                    const float ref = m == -INFINITY ? 0.0f : m;
-                    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), rf2 = make_float2(-ref, -ref);
+                    const float ref = peak * sc - LIFT<F16>;
+                    const float2 sc2 = make_float2(sc, sc), rf2 = make_float2(-ref, -ref);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t v[2][32];
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                         }
                     }
                     const float sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-                    again = __any_sync(0xffffffffu, in && (!(sum <= MOST_SUM<F16>) || m == -INFINITY));
+                    again = __any_sync(0xffffffffu, in && (!(sum <= MOST_SUM<F16>) || !(fabsf(ref) < LARGE)));
                     slack = 0.0f;  // many weights above 1 would bring it here each time
                 }
                 if (again) {
@@ -614,7 +619,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                                 if (i < c0) v[i / 32][i % 32] = HIDDEN;
                         }
                     }
-                    const float sc = neg ? 1.0f : a.scale_log2;
                     float m4[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(v[c][0]);
@@ -625,12 +629,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                             m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
 #pragma unroll
                     for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(v[c][31]));
-                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
-                    const float mr = fabsf(mx) < LARGE ? mx - LIFT<F16> : mx;
+                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     float f = 1.0f;
-                    if (mr > m + slack) {
-                        f = m == -INFINITY ? 1.0f : ex2(m - mr);  // nothing is summed under -inf
-                        m = mr;
+                    if ((mx - peak) * sc > slack) {
+                        f = peak == -INFINITY ? 1.0f : ex2((peak - mx) * sc);  // nothing is summed under -inf
+                        peak = mx;
                         l *= f;
                     }
                     if (j > p.a && __any_sync(0xffffffffu, f != 1.0f)) {
@@ -644,8 +647,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                             tmem_st16(to + c, x);
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.0f : m;
-                    const float2 sc2 = make_float2(sc, sc), rf2 = make_float2(-ref, -ref);
+                    // (the quick quotient is 0 from 2^126 on)
+                    const float sw = fabsf(peak * sc) > LARGE && peak != -INFINITY
+                                         ? __fdividef(LARGE, fminf(fabsf(peak), 4.0e37f))
+                                         : sc;
+                    const float ref = peak == -INFINITY ? 0.0f : peak * sw - LIFT<F16>;
+                    const float2 sc2 = make_float2(sw, sw), rf2 = make_float2(-ref, -ref);
 #pragma unroll
                     for (int i = 0; i < TK; i += 2) {
                         float2 x = make_float2(__uint_as_float(v[i / 32][i % 32]), __uint_as_float(v[i / 32][i % 32 + 1]));
@@ -670,6 +677,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn_tc(const __grid_constant__ 
                 s2[0] = add2(s2[0], s2[1]);
                 l += s2[0].x + s2[0].y;
             }
+            const float m = peak * sc - LIFT<F16>;  // the reference, in powers of two
             const bool any = p.b > p.a;
             if (ok && any) {
                 ok = warp_wait(&ofull[w], no & 1);
