@@ -23,7 +23,8 @@ import weight_only_int4_group_gb300 as q4  # noqa: E402
 
 
 class Server:
-    """The requests' state on the device: lengths, block table, free blocks."""
+    """The requests' state on the device: lengths, block table, free blocks,
+    and how many requests the last step could not serve."""
 
     def __init__(self, requests: int, blocks: int, block_size: int, width: int):
         i32 = dict(dtype=torch.int32, device="cuda")
@@ -32,13 +33,18 @@ class Server:
         self.table = torch.full((requests, width), -1, **i32)
         self.free_blocks = torch.arange(blocks, **i32)
         self.free_count = torch.full((1,), blocks, **i32)
+        self.refused = torch.zeros(1, **i32)
 
     def plan(self, fresh: torch.Tensor, T: int, out: q4.CachePlan | None = None) -> q4.CachePlan:
-        """The step's plan; the state moves on to the lengths after the step."""
+        """The step's plan; the state moves on to the lengths after the step.
+        A request that was not served (kv_len 0: no blocks left, or no room in
+        the table or among the T rows) keeps its length, and its blocks, and
+        goes on from there in a later step."""
         p = q4.cache_plan(self.length, fresh, self.table, self.free_blocks, self.free_count,
                           self.block_size, T, out=out)
-        self.length.copy_(p.kv_len)
+        self.length.copy_(torch.where(p.kv_len > 0, p.kv_len, self.length))
         self.free_count.copy_(p.counts[2:3])
+        self.refused.copy_(p.counts[3:4])
         return p
 
 
@@ -90,9 +96,10 @@ def main():
     block.max_fresh = 1
     x, one = x[:B].clone(), torch.ones(B, dtype=torch.int32, device="cuda")
     out = q4.CachePlan.empty(B, B)
-    saved = [t.clone() for t in (server.length, server.free_count)]
+    state = (server.length, server.free_count, server.refused)
+    saved = [t.clone() for t in state]
     y = block(x, server, server.plan(one, B, out))  # first use outside the graph: workspaces
-    for t, s in zip((server.length, server.free_count), saved):
+    for t, s in zip(state, saved):
         t.copy_(s)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -105,6 +112,7 @@ def main():
     t1.record()
     assert q4.check() == q4.OK and torch.isfinite(y).all()
     print(f"lengths {server.length.tolist()}, free blocks {server.free_count.item()}, "
+          f"not served in the last step {server.refused.item()}, "
           f"{t0.elapsed_time(t1) / steps * 1e3:.1f} us per decode step of {B} requests")
 
 

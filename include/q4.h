@@ -378,6 +378,8 @@ typedef struct {
  * when the running total of new blocks passes *free_count (a request that
  * needs no block is still served then): its kv_len is 0 and its tokens get
  * position 0 and slot -1, so the append skips them and their attention is 0.
+ * Such a request keeps its length, its blocks and its table row: the next
+ * step's cached[b] is kv_len[b], or what it was where kv_len[b] is 0.
  * Token rows past the last request get the same (padding, for graphs of a
  * fixed T).  A slot whose table entry is negative is -1.  Nothing that is
  * read is written (free_count and free_blocks are left alone; take

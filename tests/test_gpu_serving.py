@@ -137,6 +137,38 @@ def test_attention_right_behind_its_plan(many):
         assert_attention(o[:used], None, [t[:used] for t in ref], f"step {i}")
 
 
+def test_a_refused_request_keeps_its_history():
+    """Two blocks for two requests: the step in which the first needs another
+    one refuses it, and when a block comes back it goes on from its length."""
+    from attention_block import AttentionBlock, Server
+    heads, kv, D, hidden = 4, 2, 64, 256
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def fresh(*n):
+        return torch.tensor(n, **i32)
+
+    x = torch.randn(64, hidden, device="cuda").half()
+    ys = {}
+    for short in (False, True):
+        server = Server(2, 2 if short else 4, 16, 4)
+        block = AttentionBlock(hidden, heads, kv, D, 16, 4, dtype=torch.float16)
+        block(x[:26], server, server.plan(fresh(16, 10), 26))
+        assert server.length.tolist() == [16, 10] and server.refused.item() == 0
+        y1 = block(x[26:28], server, server.plan(fresh(1, 1), 2))
+        if short:
+            assert server.length.tolist() == [16, 11] and server.refused.item() == 1
+            assert (y1[0] == 0).all()
+            server.free_blocks[0], server.free_count[0] = 3, 1  # a block comes back
+            y1[:1] = block(x[26:27], server, server.plan(fresh(1, 0), 1))
+        assert server.length.tolist() == [17, 11]
+        y2 = block(x[28:30], server, server.plan(fresh(1, 1), 2))
+        assert server.length.tolist() == [18, 12] and server.refused.item() == 0
+        assert q4().check() == q4().OK
+        ys[short] = torch.cat([y1, y2])
+    # one row at a time or two: the products may round differently, twice, to f16
+    assert (ys[True].double() - ys[False].double()).norm() <= 4 * 2.0 ** -11 * ys[False].double().norm()
+
+
 # ------------------------------------------------------------------ guards
 @pytest.mark.parametrize("lengths", [[(700, 1), (40, 1), (0, 1)], [(700, 60), (40, 133), (0, 1)]], ids=["few", "many"])
 @pytest.mark.parametrize("D", [64, 80, 128])

@@ -384,7 +384,7 @@ class KVCache:
 class CachePlan:
     """What q4_cache_plan writes for one step."""
     q_start: torch.Tensor   # int32 [B + 1]
-    kv_len: torch.Tensor    # int32 [B]
+    kv_len: torch.Tensor    # int32 [B]; 0: not served, the request keeps the length it had
     position: torch.Tensor  # int32 [T]
     slot: torch.Tensor      # int64 [T]
     counts: torch.Tensor    # int32 [4]: rows used, tokens served, free blocks left, requests not served
