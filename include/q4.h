@@ -460,9 +460,9 @@ q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t
  * bounded wait ran out (Q4_ERR_TIMEOUT) zero it again.
  * INVALID_ARG for NULL pointers, sizes < 1, Hq not a multiple of heads, a
  * non-finite scale, a negative window, a short workspace; UNSUPPORTED for
- * types, T * Hq or B beyond 2^31 - 1, width * block_size beyond 2^30 - 1, or a
- * cache beyond q4_kv_cache's limits; MISALIGNED unless q, o, k, v, workspace are 16-byte aligned and
- * strides multiples of 8.
+ * types, T * Hq beyond 2^31 - 1024, B beyond 2^31 - 1, width * block_size
+ * beyond 2^30 - 1, or a cache beyond q4_kv_cache's limits; MISALIGNED unless
+ * q, o, k, v, workspace are 16-byte aligned and strides multiples of 8.
  */
 q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
                        const q4_kv_cache *cache, const int32_t *table, int64_t table_stride,

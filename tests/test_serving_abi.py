@@ -164,3 +164,11 @@ def test_kernels_that_start_early_load_coherently(source):
     text = open(os.path.join(ROOT, "weight_only_int4_group_gb300", "csrc", source)).read()
     code = re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
     assert not re.search(r"__ldg\b|ld\.global\.nc|__restrict__", code)
+
+
+@pytest.mark.parametrize("Hq,heads", [(1, 1), (4, 2), (64, 1), (1000, 2)])
+def test_attention_refuses_rows_whose_tiles_pass_32_bits(lib, Hq, heads):
+    """Row indices run on to the end of a tile of 256 rows."""
+    good = dict(ATTN, Hq=Hq, q_stride=Hq * 64, o_stride=Hq * 64, cache=dict(CACHE, heads=heads))
+    for rows in (2 ** 31 - 1, 2 ** 31 - 256, 2 ** 31 - 513):
+        assert call(lib.q4_attention, good, list(ATTN), T=rows // Hq if Hq < 1000 else 2147483) == UNSUP

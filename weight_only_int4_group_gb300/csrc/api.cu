@@ -451,6 +451,10 @@ q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t
     return e == cudaSuccess ? Q4_OK : cuda_fail(e);
 }
 
+// Rows (tokens times heads) of a call: their indices run on to the end of a
+// tile of 256 rows, in 32 bits.
+constexpr int64_t ATTN_MOST_ROWS = INT_MOST - 1023;
+
 static bool attention_sizes_ok(int64_t max_fresh, int64_t Hq, int64_t heads, int64_t head_dim)
 {
     return max_fresh >= 1 && max_fresh <= INT_MOST && heads >= 1 && Hq >= heads && Hq % heads == 0 &&
@@ -480,7 +484,7 @@ static q4_status attention_common(const void *q, int64_t q_stride, int64_t T, in
         table_stride < width || window < 0 || !std::isfinite(scale))
         return Q4_ERR_INVALID_ARG;
     if (ot != Q4_F32 && ot != cache->type) return Q4_ERR_UNSUPPORTED;
-    if (!attention_sizes_ok(max_fresh, Hq, cache->heads, cache->head_dim) || T > INT_MOST / Hq ||
+    if (!attention_sizes_ok(max_fresh, Hq, cache->heads, cache->head_dim) || T > ATTN_MOST_ROWS / Hq ||
         B > INT_MOST || table_stride > (1LL << 40) || width > (INT_MOST >> 1) / cache->block_size)
         return Q4_ERR_UNSUPPORTED;
     const int64_t row = Hq * cache->head_dim;
