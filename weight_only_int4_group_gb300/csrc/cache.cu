@@ -168,7 +168,7 @@ cudaError_t cache_plan_launch(const PlanArgs &a, cudaStream_t s)
     const cudaError_t e = allow_smem(k_cache_plan, most, done);
     if (e != cudaSuccess) return e;
     const size_t smem = (2 * static_cast<size_t>(a.B) + 1) * sizeof(int);
-    const int grid = std::max(1, std::min(128, (a.T + PLAN_THREADS - 1) / PLAN_THREADS));
+    const int grid = std::min(128, ctas_for(a.T, PLAN_THREADS));
     return launch_dependent(k_cache_plan, dim3(grid), PLAN_THREADS, smem, s, a);
 }
 
@@ -317,7 +317,7 @@ cudaError_t rope_launch(const RopeArgs &a, cudaStream_t s)
     const bool many = a.T >= 3000;
     const int tok = many ? 4 : 1;
     const int split = many ? 2 : a.T <= 64 ? 4 : a.T <= 152 ? 2 : 1;
-    const dim3 grid((a.T + tok - 1) / tok, split);
+    const dim3 grid(ctas_for(a.T, tok), split);
     const size_t smem = static_cast<size_t>(tok) * (a.rot / 2) * sizeof(float2);
     // the widest vector that divides the pair layout and both parts of the head
     const int m = (INTER ? a.rot : a.rot / 2) | (a.D - a.rot);

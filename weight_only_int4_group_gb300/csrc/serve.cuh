@@ -20,11 +20,14 @@ struct FastDiv {
         shift = 31 + l;
         mul = static_cast<uint32_t>((1ull << shift) / static_cast<unsigned>(divisor) + 1);
     }
-    __device__ __forceinline__ int div(int n) const
+    __host__ __device__ __forceinline__ int div(int n) const
     {
         return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
     }
 };
+
+// CTAs that take n (up to 2^31 - 1) things, `per` each.
+inline int ctas_for(int64_t n, int per) { return static_cast<int>((n + per - 1) / per); }
 
 // One q4_attention call as its kernels see it.
 struct AttnArgs {
