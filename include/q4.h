@@ -383,9 +383,10 @@ typedef struct {
  * Token rows past the last request get the same (padding, for graphs of a
  * fixed T).  A slot whose table entry is negative is -1.  Nothing that is
  * read is written (free_count and free_blocks are left alone; take
- * counts[2] as the next count), so a repeated call gives the same result.
+ * counts[2] as the next count), so a repeated call gives the same result;
+ * what is written may not overlap any other of the arrays.
  * INVALID_ARG for NULL pointers, T, B, width, block_size or free_capacity
- * < 1 or a table_stride below width; UNSUPPORTED above
+ * < 1, a table_stride below width or overlapping arrays; UNSUPPORTED above
  * Q4_PLAN_MAX_REQUESTS requests, or T, width * block_size, free_capacity
  * beyond 2^31 - 1.
  */

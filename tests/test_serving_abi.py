@@ -172,3 +172,28 @@ def test_attention_refuses_rows_whose_tiles_pass_32_bits(lib, Hq, heads):
     good = dict(ATTN, Hq=Hq, q_stride=Hq * 64, o_stride=Hq * 64, cache=dict(CACHE, heads=heads))
     for rows in (2 ** 31 - 1, 2 ** 31 - 256, 2 ** 31 - 513):
         assert call(lib.q4_attention, good, list(ATTN), T=rows // Hq if Hq < 1000 else 2147483) == UNSUP
+
+
+PLAN_APART = dict(PLAN, **{n: P * i for i, n in enumerate(("cached", "fresh", "table", "free", "count", "q_start", "kv_len",
+                                                           "position", "slot", "counts"), 1)})
+
+
+@pytest.mark.parametrize("out", ["table", "q_start", "kv_len", "position", "slot", "counts"])
+@pytest.mark.parametrize("other", ["cached", "fresh", "table", "free", "count", "q_start", "kv_len", "position", "slot", "counts"])
+def test_plan_refuses_outputs_over_other_arrays(lib, out, other):
+    """kv_len over cached would be the tempting one: CTAs read the lengths
+    again after some of them have been written."""
+    if out == other:
+        return
+    size = dict(table=(3 * 8 + 8) * 4, q_start=20, kv_len=16, position=20, slot=40, counts=16)[out]
+    for at in (PLAN_APART[out], PLAN_APART[out] + size - 4):
+        assert call(lib.q4_cache_plan, PLAN_APART, list(PLAN), **{other: at}) == BAD
+
+
+def test_plan_checks_the_tables_rows_only(lib):
+    """A wide table whose second row lies over a length array is refused."""
+    wide = dict(PLAN_APART, table=P * 100, stride=P // 4)
+    for at, name in ((P * 101 + 28, "cached"), (P * 101 - 4, "kv_len"), (P * 103 + 31 - 3, "fresh")):
+        assert call(lib.q4_cache_plan, wide, list(PLAN), **{name: at}) == BAD
+    # between the rows nothing is refused for that; a bad size still is, first
+    assert call(lib.q4_cache_plan, wide, list(PLAN), kv_len=P * 101 + 64, T=0) == BAD

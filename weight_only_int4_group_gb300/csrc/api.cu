@@ -385,6 +385,22 @@ q4_status q4_cache_plan(const int32_t *cached, const int32_t *fresh, int64_t B, 
     if (B > Q4_PLAN_MAX_REQUESTS || T > INT_MOST || free_capacity > INT_MOST ||
         table_stride > (1LL << 40) || width > INT_MOST / block_size)
         return Q4_ERR_UNSUPPORTED;
+    // What is written (the first six) may lie over nothing else: every CTA
+    // reads the lengths, some after others have written.
+    const struct {
+        const void *p;
+        int64_t bytes;
+    } arrays[] = {{table, ((B - 1) * table_stride + width) * 4}, {q_start, (B + 1) * 4}, {kv_len, B * 4},
+                  {position, T * 4}, {slot, T * 8}, {counts, 16}, {cached, B * 4}, {fresh, B * 4},
+                  {free_blocks, free_capacity * 4}, {free_count, 4}};
+    for (int i = 0; i < 6; ++i)
+        for (int j = i + 1; j < 10; ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(arrays[i].p), y = reinterpret_cast<uintptr_t>(arrays[j].p);
+            if (x >= y + arrays[j].bytes || y >= x + arrays[i].bytes) continue;
+            // between the table's rows there is room
+            const int64_t step = table_stride * 4, at = static_cast<int64_t>(y - x);
+            if (i > 0 || y < x || at % step < width * 4 || at % step + arrays[j].bytes > step) return Q4_ERR_INVALID_ARG;
+        }
     PlanArgs a{};
     a.cached = cached;
     a.fresh = fresh;
