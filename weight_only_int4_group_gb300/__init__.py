@@ -128,9 +128,21 @@ def _ok(status: int, where: str):
         raise Q4Error(status, where)
 
 
+# The library launches on the thread's current device, which addresses of
+# another one must not reach: every tensor's device is compared with it.
+_current_device = torch._C._cuda_getDevice
+
+
+def _elsewhere(name: str, index: int, dev: int):
+    """Refuses a tensor of device `index` (-1: the host), which is not `dev`."""
+    raise ValueError(f"{name} must be a CUDA tensor" if index < 0 else
+                     f"{name} is on CUDA device {index}, the current device is {dev}")
+
+
 def _cuda(t: torch.Tensor, name: str):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    on = t.get_device()
+    if on < 0 or on != _current_device():
+        _elsewhere(name, on, -1 if on < 0 else _current_device())
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
@@ -185,6 +197,7 @@ def repack(packed: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor, N: int
         raise ValueError(f"invalid shape {N}x{K}")
     if out is None:
         out = torch.empty(nb, dtype=torch.uint8, device=packed.device)
+    _cuda(out, "out")
     _ok(_lib.q4_repack(packed.data_ptr(), scale.data_ptr(), zero.data_ptr(), N, K,
                        out.data_ptr(), _stream(stream)), "q4_repack")
     return out
@@ -210,6 +223,7 @@ def repack_compact(packed: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor
         raise ValueError(f"invalid shape {N}x{K}")
     if out is None:
         out = torch.empty(nb, dtype=torch.uint8, device=packed.device)
+    _cuda(out, "out")
     _ok(_lib.q4_repack_compact(packed.data_ptr(), scale.data_ptr(), zero.data_ptr(), N, K,
                                out.data_ptr(), _stream(stream)), "q4_repack_compact")
     return out
@@ -279,7 +293,12 @@ def gemm_workspace(M: int, N: int, K: int, device=None) -> torch.Tensor | None:
 
 
 def _ws(ws):
-    return (0, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    if ws is None:
+        return 0, 0
+    on = ws.get_device()
+    if on < 0 or on != _current_device():
+        _elsewhere("ws", on, -1 if on < 0 else _current_device())
+    return ws.data_ptr(), ws.numel()
 
 
 def _product_args(x: torch.Tensor, qw: QWeight, out_dtype, out):
@@ -287,8 +306,13 @@ def _product_args(x: torch.Tensor, qw: QWeight, out_dtype, out):
     M, K = x.shape
     if K != qw.K:
         raise ValueError(f"x has K={K}, weight has K={qw.K}")
+    dev = x.get_device()
+    if qw.data.get_device() != dev:
+        _elsewhere("qw", qw.data.get_device(), dev)
     if out is None:
         out = torch.empty((M, qw.N), dtype=out_dtype or x.dtype, device=x.device)
+    elif out.get_device() != dev:
+        _elsewhere("out", out.get_device(), dev)
     return M, K, out
 
 
@@ -366,7 +390,7 @@ class KVCache:
             raise ValueError("k and v must have the same shape, strides, type and device")
         if k.shape[3] > 1 and k.stride(3) != 1:
             raise ValueError("the last dimension must be contiguous")
-        self.k, self.v = k, v
+        self.k, self.v, self._on = k, v, k.get_device()
         self.dtype, (_, self.heads, self.block_size, self.head_dim) = k.dtype, k.shape
         self._arg = _KVCacheArg(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], *k.shape, *k.stride()[:3])
         self._ref = ctypes.byref(self._arg)
@@ -400,8 +424,8 @@ class CachePlan:
 
 # The checks below are a call's whole host cost beside the launch: a few tenths
 # of a microsecond each, where a decode step's kernels take several.
-def _raw_stream(stream, device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _on(stream):
@@ -417,17 +441,21 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _array(t: torch.Tensor, name: str, dtype, n: int | None = None) -> int:
-    """Address of a contiguous CUDA array of n elements."""
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and (n is None or t.numel() == n)):
+def _array(t: torch.Tensor, name: str, dtype, dev: int, n: int | None = None) -> int:
+    """Address of a contiguous array of n elements on device dev."""
+    if t.get_device() != dev:
+        _elsewhere(name, t.get_device(), dev)
+    if not (t.dtype == dtype and t.is_contiguous() and (n is None or t.numel() == n)):
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor" +
                          ("" if n is None else f" of {n} elements") + f", is {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _table(table: torch.Tensor, B: int):
+def _table(table: torch.Tensor, B: int, dev: int):
     """Address, row stride and width of a block table."""
-    if not (table.is_cuda and table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B):
+    if table.get_device() != dev:
+        _elsewhere("table", table.get_device(), dev)
+    if not (table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == B):
         raise ValueError(f"table must be an int32 CUDA tensor of {B} rows")
     width = table.shape[1]
     stride, one = table.stride()
@@ -437,9 +465,11 @@ def _table(table: torch.Tensor, B: int):
     return table.data_ptr(), stride if B > 1 else max(stride, width), width
 
 
-def _rows(t: torch.Tensor, name: str, dtype):
+def _rows(t: torch.Tensor, name: str, dtype, dev: int):
     """Token rows, 2-D or 3-D, contiguous but for the stride between rows:
     their address, number, elements and stride."""
+    if t.get_device() != dev:
+        _elsewhere(name, t.get_device(), dev)
     shape, stride = t.shape, t.stride()
     if len(shape) == 3:
         n = shape[1] * shape[2]
@@ -447,7 +477,7 @@ def _rows(t: torch.Tensor, name: str, dtype):
     else:
         n = shape[-1] if len(shape) == 2 else 0
         dense = len(shape) == 2 and (stride[1] == 1 or n == 1)
-    if not (dense and t.is_cuda and t.dtype == dtype and shape[0] >= 1):
+    if not (dense and t.dtype == dtype and shape[0] >= 1):
         raise ValueError(f"{name} must be {dtype} CUDA rows of contiguous elements, is {t.dtype} {tuple(shape)}")
     return t.data_ptr(), shape[0], n, stride[0] if shape[0] > 1 else max(stride[0], n)
 
@@ -459,8 +489,8 @@ def cache_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor,
     and ``fresh`` [B]; ``table`` int32 [B][W] gets the blocks of the new tokens,
     taken from the end of ``free_blocks`` int32, of which the first
     ``free_count`` (int32 [1]) are free.  T token rows."""
-    B = cached.numel()
-    tp, ts, width = _table(table, B)
+    B, dev = cached.numel(), _current_device()
+    tp, ts, width = _table(table, B, dev)
     if out is None:
         if stream is None:
             out = CachePlan.empty(B, T, cached.device)
@@ -468,12 +498,12 @@ def cache_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor,
             with _on(stream):
                 out = CachePlan.empty(B, T, cached.device)
     i32 = torch.int32
-    _ok(_lib.q4_cache_plan(_array(cached, "cached", i32), _array(fresh, "fresh", i32, B), B, block_size, tp, ts,
-                           width, _array(free_blocks, "free_blocks", i32), _array(free_count, "free_count", i32, 1),
-                           free_blocks.numel(), T, _array(out.q_start, "q_start", i32, B + 1),
-                           _array(out.kv_len, "kv_len", i32, B), _array(out.position, "position", i32, T),
-                           _array(out.slot, "slot", torch.int64, T), _array(out.counts, "counts", i32, 4),
-                           _raw_stream(stream, cached.device)), "q4_cache_plan")
+    _ok(_lib.q4_cache_plan(_array(cached, "cached", i32, dev), _array(fresh, "fresh", i32, dev, B), B, block_size, tp, ts,
+                           width, _array(free_blocks, "free_blocks", i32, dev), _array(free_count, "free_count", i32, dev, 1),
+                           free_blocks.numel(), T, _array(out.q_start, "q_start", i32, dev, B + 1),
+                           _array(out.kv_len, "kv_len", i32, dev, B), _array(out.position, "position", i32, dev, T),
+                           _array(out.slot, "slot", torch.int64, dev, T), _array(out.counts, "counts", i32, dev, 4),
+                           _raw_stream(stream, dev)), "q4_cache_plan")
     return out
 
 
@@ -507,18 +537,21 @@ def rope_append(qkv: torch.Tensor, cache: KVCache, position: torch.Tensor, slot:
     head_dim] and append keys and values to the cache (q4_rope_append).
     2 * len(freq) elements of each head turn.  Returns the queries
     [T][heads][head_dim] (``out`` may be the query part of qkv itself)."""
-    qp, T, n, stride = _rows(qkv, "qkv", cache.dtype)
+    dev = _current_device()
+    if cache._on != dev:
+        _elsewhere("cache", cache._on, dev)
+    qp, T, n, stride = _rows(qkv, "qkv", cache.dtype, dev)
     if n != (heads + 2 * cache.heads) * cache.head_dim:
         raise ValueError(f"qkv rows have {n} elements, not (heads + 2 * cache heads) * head_dim")
     if out is None:
         out = _empty((T, heads, cache.head_dim), cache.dtype, qkv.device, stream)
-    op, To, no, ostride = _rows(out, "out", cache.dtype)
+    op, To, no, ostride = _rows(out, "out", cache.dtype, dev)
     if To != T or no != heads * cache.head_dim:
         raise ValueError("out must be T rows of heads * head_dim")
     _ok(_lib.q4_rope_append(qp, stride, T, heads, 2 * freq.numel(), ROPE_INTERLEAVED if interleaved else ROPE_HALF,
-                            _array(freq, "freq", torch.float64), factor, _array(position, "position", torch.int32, T),
-                            _array(slot, "slot", torch.int64, T), op, ostride, cache._ref,
-                            _raw_stream(stream, qkv.device)), "q4_rope_append")
+                            _array(freq, "freq", torch.float64, dev), factor, _array(position, "position", torch.int32, dev, T),
+                            _array(slot, "slot", torch.int64, dev, T), op, ostride, cache._ref,
+                            _raw_stream(stream, dev)), "q4_rope_append")
     return out
 
 
@@ -544,16 +577,19 @@ def attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: tor
     ``window`` > 0: each token sees that many keys, itself included.  Returns
     o [T][heads][head_dim] (q's type, or float32), with ``return_lse`` also the
     f32 log-sum-exp [T][heads]."""
-    qp, T, n, stride = _rows(q, "q", cache.dtype)
+    dev = _current_device()
+    if cache._on != dev:
+        _elsewhere("cache", cache._on, dev)
+    qp, T, n, stride = _rows(q, "q", cache.dtype, dev)
     D = cache.head_dim
     if q.dim() != 3 or q.shape[2] != D:
         raise ValueError(f"q must be [T][heads][{D}]")
     heads = q.shape[1]
     B = kv_len.numel()
-    tp, ts, width = _table(table, B)
+    tp, ts, width = _table(table, B, dev)
     if out is None:
         out = _empty((T, heads, D), out_dtype or cache.dtype, q.device, stream)
-    op, To, no, ostride = _rows(out, "out", out.dtype)
+    op, To, no, ostride = _rows(out, "out", out.dtype, dev)
     if To != T or no != n:
         raise ValueError("out must be T rows of heads * head_dim")
     if return_lse and lse is None:
@@ -561,11 +597,11 @@ def attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: tor
     if ws is None:
         with _on(stream if stream is not None else torch.cuda.current_stream()):
             ws = attention_workspace(max_fresh, heads, cache.heads, D, q.device)
-    _ok(_call(qp, stride, T, heads, cache._ref, tp, ts, width, _array(q_start, "q_start", torch.int32, B + 1),
-              _array(kv_len, "kv_len", torch.int32, B), B, max_fresh, D ** -0.5 if scale is None else scale, window,
+    _ok(_call(qp, stride, T, heads, cache._ref, tp, ts, width, _array(q_start, "q_start", torch.int32, dev, B + 1),
+              _array(kv_len, "kv_len", torch.int32, dev, B), B, max_fresh, D ** -0.5 if scale is None else scale, window,
               op, _DTYPE.get(out.dtype, -1), ostride,
-              0 if lse is None else _array(lse, "lse", torch.float32, T * heads),
-              *_ws(ws), _raw_stream(stream, q.device)), "q4_attention")
+              0 if lse is None else _array(lse, "lse", torch.float32, dev, T * heads),
+              *_ws(ws), _raw_stream(stream, dev)), "q4_attention")
     return (out, lse) if lse is not None else out
 
 
