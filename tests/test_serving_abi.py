@@ -156,7 +156,7 @@ def test_debug_library_exports_the_same(lib):
     subprocess.run([sys.executable, "-c", code], check=True)
 
 
-@pytest.mark.parametrize("source", ["serve.cuh", "attention.cuh", "attention.cu", "attention_tc.cu", "cache.cu"])
+@pytest.mark.parametrize("source", ["serve.cuh", "attention.cuh", "attention.cu", "attention_tc.cu", "cache.cu", "gemv.cu"])
 def test_kernels_that_start_early_load_coherently(source):
     """They are resident while the kernel that writes their inputs may still
     run: no load of the non-coherent path, which asks for data that nothing

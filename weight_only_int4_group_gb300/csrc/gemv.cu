@@ -772,13 +772,13 @@ __global__ void __launch_bounds__(THREADS, MIN_BLOCKS) k_gemv(const GemvArgs a)
                     if (act && m < M) {
                         const int64_t idx = static_cast<int64_t>(m) * a.K + k + 8 * h;
                         if (XSPLIT) {
-                            const float2 xv = __ldg(reinterpret_cast<const float2 *>(
-                                static_cast<const float *>(a.x) + idx));
+                            // coherent loads: the kernel that writes x may have run beside this one
+                            const float2 xv =
+                                *reinterpret_cast<const float2 *>(static_cast<const float *>(a.x) + idx);
                             vh = pack_bf16x2(xv.x, xv.y);
                             vl = pack_bf16x2(xv.x - bf16_lo_f32(vh), xv.y - bf16_hi_f32(vh));
                         } else {
-                            vh = __ldg(reinterpret_cast<const unsigned int *>(
-                                static_cast<const uint16_t *>(a.x) + idx));
+                            vh = *reinterpret_cast<const unsigned int *>(static_cast<const uint16_t *>(a.x) + idx);
                         }
                     }
                     bh[n][j][h] = vh;
