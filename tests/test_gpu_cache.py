@@ -219,3 +219,32 @@ def test_rope_frequencies():
     assert abs(factor - (0.1 * math.log(16) + 1)) < 1e-12
     g, factor = m.rope_frequencies(64, stretch=4.0)
     assert factor == 1.0 and np.allclose((g / f).cpu().numpy(), 0.25)
+
+
+@pytest.mark.parametrize("T", [2999, 3000, 3001, 3003])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_of_many_tokens(T, inter):
+    """Several tokens per CTA, with a last CTA of fewer; in place too."""
+    rope_case(T, 3, 2, 64, 32, 16, torch.bfloat16, inter, seed=T)
+    rope_case(T, 4, 1, 80, 80, 48, torch.float16, inter, seed=T, in_place=True, token_major=True)
+
+
+@pytest.mark.parametrize("T", [2999, 3001, 3003])
+def test_rope_of_many_tokens_stays_inside(T):
+    from test_gpu_canaries import Guarded
+    m = q4()
+    H, KV, D, S = 3, 2, 80, 16
+    blocks = -(-T // S)
+    nb = blocks * KV * S * D * 2
+    k, v, q = Guarded(nb), Guarded(nb), Guarded(T * H * D * 2)
+    cache = m.KVCache(*(t.view(torch.float16, (blocks, KV, S, D)) for t in (k, v)))
+    qkv = torch.randn(T, (H + 2 * KV) * D, device="cuda").half()
+    freq, _ = m.rope_frequencies(D)
+    slot = torch.arange(blocks * S - 1, blocks * S - 1 - T, -1, device="cuda")
+    slot[5::7] = blocks * S  # one past the cache
+    for inter in (False, True):
+        m.rope_append(qkv, cache, torch.arange(T, dtype=torch.int32, device="cuda"), slot, freq, H,
+                      interleaved=inter, out=q.view(torch.float16, (T, H, D)))
+        assert m.check() == m.OK
+        for g, n in ((k, "k"), (v, "v"), (q, "q")):
+            g.assert_guards(n)
