@@ -236,3 +236,31 @@ def test_suites_with_the_bounds_checked_library():
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider", *files],
                        cwd=ROOT, env=env, capture_output=True, text=True, timeout=1200)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-1000:]
+
+
+@pytest.mark.parametrize("pad", [0, 8, 72])
+@pytest.mark.parametrize("heads,kv", [(3, 3), (8, 2), (16, 2), (32, 1), (40, 1)])
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_attention_stores_end_at_the_rows(heads, kv, D, pad):
+    """Groups of 1, 4, 8, 32 and 40 query heads, requests of rows on both sides
+    of multiples of 32 and 128, outputs inside wider rows: whole rows of the
+    first four leave by tensor copies of 32.  Padding between the rows, rows of
+    no request and the bytes around the buffer stay as they were."""
+    m = q4()
+    g = heads // kv
+    news = [max(1, x // g) for x in (31, 32, 33, 64, 127, 128, 129, 256, 257)] + [1, 2, 40]
+    r = Requests([(i * 29 % 90, n) for i, n in enumerate(news)], heads, kv, D, 16, torch.float16, seed=D + heads)
+    T, row, tail = r.T, heads * D, 5
+    q = torch.cat([r.q, torch.randn_like(r.q[:1]).expand(tail, -1, -1)])
+    o = Guarded((T + tail) * (row + pad) * 2)
+    wide = o.view(torch.float16, (T + tail, row + pad))
+    before = wide.view(torch.int16).clone()
+    lse = Guarded((T + tail) * heads * 4)
+    m.attention(q, m.KVCache(r.k, r.v), r.table, r.q_start, r.kv_len, r.max_fresh,
+                out=wide[:, :row].unflatten(1, (heads, D)), lse=lse.view(torch.float32, (T + tail, heads)))
+    assert m.check() == m.OK
+    o.assert_guards("o")
+    lse.assert_guards("lse")
+    after = wide.view(torch.int16)
+    assert torch.equal(after[:, row:], before[:, row:]) and torch.equal(after[T:], before[T:])
+    assert_attention(wide[:T, :row].unflatten(1, (heads, D)), None, r.reference(), f"{heads}/{kv} {D}")
