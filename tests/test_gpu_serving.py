@@ -264,3 +264,17 @@ def test_attention_stores_end_at_the_rows(heads, kv, D, pad):
     after = wide.view(torch.int16)
     assert torch.equal(after[:, row:], before[:, row:]) and torch.equal(after[T:], before[T:])
     assert_attention(wide[:T, :row].unflatten(1, (heads, D)), None, r.reference(), f"{heads}/{kv} {D}")
+
+
+@pytest.mark.parametrize("lengths", [[(20000, 1)], [(20000, 2)], [(12000, 7)], [(9000, 13), (9000, 40)]], ids=str)
+def test_the_workspace_counters_return_to_zero(lengths):
+    """All of them: those of every level of the streaming kernel's tree too."""
+    m = q4()
+    for kv in (1, 2):
+        r = Requests(lengths, 8, kv, 64, 32, torch.bfloat16, seed=25)
+        ws = m.attention_workspace(r.max_fresh, 8, kv, 64)
+        for _ in range(2):
+            m.attention(r.q, m.KVCache(r.k, r.v), r.table, r.q_start, r.kv_len, r.max_fresh, ws=ws)
+            assert m.check() == m.OK
+            assert not ws[:131072].any()
+        assert ws[131072:].any()  # the items were split
