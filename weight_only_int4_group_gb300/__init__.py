@@ -488,7 +488,8 @@ def cache_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor,
     """The step's plan from request lengths (q4_cache_plan): int32 ``cached``
     and ``fresh`` [B]; ``table`` int32 [B][W] gets the blocks of the new tokens,
     taken from the end of ``free_blocks`` int32, of which the first
-    ``free_count`` (int32 [1]) are free.  T token rows."""
+    ``free_count`` (int32 [1]) are free.  T token rows.  A step's loop keeps
+    one ``out``: allocating its five arrays takes longer than the plan."""
     B, dev = cached.numel(), _current_device()
     tp, ts, width = _table(table, B, dev)
     if out is None:
@@ -576,7 +577,8 @@ def attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: tor
     its keys the kv_len[b] first tokens of table row b, its own new ones last.
     ``window`` > 0: each token sees that many keys, itself included.  Returns
     o [T][heads][head_dim] (q's type, or float32), with ``return_lse`` also the
-    f32 log-sum-exp [T][heads]."""
+    f32 log-sum-exp [T][heads].  Keep one ``ws`` (attention_workspace) per
+    stream: without it each call allocates and zero-fills tens of megabytes."""
     dev = _current_device()
     if cache._on != dev:
         _elsewhere("cache", cache._on, dev)

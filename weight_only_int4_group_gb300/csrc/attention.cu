@@ -24,8 +24,8 @@
 // depend on timing.
 //
 // Measured (64 query / 8 KV heads of 128, bf16): 48 requests of 1001..24576
-// keys 386 us, 6.5 TB/s (0.96 of the measured copy bandwidth); 32 of
-// 101..8192 keys 96 us (0.83); one of 65536 55 us (0.72); one of 777 keys 12 us,
+// keys 384 us, 6.5 TB/s (0.96 of the measured copy bandwidth); 32 of
+// 101..8192 keys 96 us (0.83); one of 65536 55 us (0.72); one of 777 keys 13 us,
 // which is latency.
 #include "serve.cuh"
 #include "attention.cuh"
@@ -49,8 +49,8 @@ constexpr int PAD = 4, MIN_UNITS = 4;
 // row's sum counts them).  bf16 has the exponents of f32.
 template <bool F16>
 constexpr float LIFT = F16 ? 15.0f : 0.0f;
-// Parts that are added at a time where an item is split (4 levels hold 4096
-// workers, the most there are).
+// Parts that are added at a time where an item is split; 4 levels hold 4096
+// workers, of 2048 at most.
 constexpr int MERGE = 8, LEVELS = 4, MOST_CTAS = 256;
 static_assert(MERGE * MERGE * MERGE * MERGE >= NW * MOST_CTAS, "levels");
 static_assert(LEVELS * 2 * NW * MOST_CTAS * sizeof(unsigned int) <= ATTN_COUNTER_BYTES, "counters");
@@ -408,7 +408,9 @@ AttnPlan attention_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count)
     p.grid = std::min<int>(sm_count, MOST_CTAS);
     // One row tile streams the cache once; more tiles would read it again (us,
     // streaming / tensor cores: 8 rows, 2 x 32768 keys 55 / 63; 24 rows, 16
-    // requests of 4000 keys 81 / 62; 32 rows 84 / 62; 64 rows 136 / 63).
+    // requests of 4000 keys 81 / 62; 32 rows 84 / 62; 64 rows 136 / 63).  The
+    // whole call goes by its longest request: 40 decodes of 8000 keys take 206
+    // alone, a chunk of 128 after 2000 takes 40, both in one call 236.
     p.tc = max_fresh > R / GQ;
     const size_t slot = (D > 64 ? Sizes<128>::SLOT : Sizes<64>::SLOT) * sizeof(float);
     const size_t part = p.tc ? attention_tc_part_bytes(D, p.grid) : 2 * static_cast<size_t>(p.grid) * NW * slot;

@@ -48,14 +48,17 @@
 // error word, every role stops, copies and MMAs in flight are waited for,
 // tensor memory is freed and the kernel returns.
 //
-// Measured (bf16, 64 query / 8 KV heads of 128): 512 new tokens after 16384 in
-// 180 us, 1.55 PFLOP/s (0.81 of the measured peak; 188 us with inputs from
-// HBM); a prompt of 4096 tokens, 32 heads, f16, in 114 us, 1.21 PFLOP/s (118);
-// 12 requests with 1..160 new tokens after 50..4000 in 79 us.  A unit of 256
-// rows takes some 2800 cycles, 1550 of them in the tensor pipe: the MMA
-// thread's waits and commits come one after the other with its MMAs, which
-// queue only a few deep.  The CTA's range stays in shared memory: held in
-// registers it made the softmax warps spill (188 us against 186).
+// Measured (bf16, 64 query / 8 KV heads of 128, inputs from HBM): 512 new
+// tokens after 16384 in 188 us, 1.49 PFLOP/s (0.77 of the measured peak; 180 to
+// 182 us with inputs in L2); a prompt of 4096 tokens, 32 heads, f16, in 118 us,
+// 1.17 PFLOP/s; 12 requests with 1..160 new tokens after 50..4000 in 81 us;
+// prompts of 2048 with head sizes of 64, 80, 96 and 128 in 62, 73, 74 and 75
+// us (80 and 96 run as 128), with f32 output 103.  A unit of 256 rows took some
+// 2800 cycles when traced; its operations are 2048 cycles of the tensor pipe
+// (8192 per cycle and SM).  The rest is the MMA thread's waits and commits,
+// which come one after the other with its MMAs, as those queue only a few deep.
+// The CTA's range stays in shared memory: held in registers it made the softmax
+// warps spill (188 us against 186).
 #include <type_traits>
 
 #include "attention.cuh"

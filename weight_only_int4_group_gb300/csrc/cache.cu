@@ -180,8 +180,8 @@ cudaError_t cache_plan_launch(const PlanArgs &a, cudaStream_t s)
 // loads a half head apart, or one load of interleaved pairs) or a VEC-element
 // copy (the unrotated part of a head, the values).  VEC is the widest vector
 // that the pair layout allows, 8 elements (16 bytes) for the usual sizes.
-// Measured: 8192 rows of 80 heads of 128 in 57.7 us, 5.8 TB/s read and
-// written, 0.86 of the measured copy bandwidth (the cache rows are 256-byte
+// Measured: 8192 rows of 80 heads of 128 in 58.3 us, 5.8 TB/s read and
+// written, 0.85 of the measured copy bandwidth (the cache rows are 256-byte
 // pieces at random places).  Several units per thread in flight were slower
 // (74 us and more): the registers cost more warps than the loads gain.
 namespace {
@@ -313,7 +313,9 @@ cudaError_t rope_launch(const RopeArgs &a, cudaStream_t s)
     // tokens are latency, shared out finer (T = 4: 2.7 by four CTAs each, 3.7
     // by one; T = 152: 3.7 by two, 4.0 by four); many are bandwidth, where
     // more tokens per CTA spare beginnings (T = 8192: 57.7 by four tokens in
-    // two halves, 64.1 by one; T = 2048: 18.2 and 16.9).
+    // two halves, 64.1 by one; T = 2048: 18.2 and 16.9).  The rule goes by
+    // tokens alone: with 32 + 2 * 32 heads T = 2999 takes 28.9 and 3000 30.5,
+    // with 8 + 2 8.9 and 7.4.
     const bool many = a.T >= 3000;
     const int tok = many ? 4 : 1;
     const int split = many ? 2 : a.T <= 64 ? 4 : a.T <= 152 ? 2 : 1;
