@@ -118,6 +118,29 @@ def test_plan_in_a_graph_follows_its_inputs():
         count.copy_(out.counts[2:3])
 
 
+def test_plan_arrays_between_the_tables_rows():
+    """The room between a wide table's rows is nobody's: arrays may lie there."""
+    m = q4()
+    c = plan_case([5, 16, 30], [20, 1, 9], 16, 4, 8)
+    ref = plan_reference(**c)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    buf = torch.full((3, 64), -3, **i32)
+    table = buf[:, :4]
+    table.copy_(torch.tensor(c["table"]))
+    out = m.CachePlan.empty(3, c["T"])
+    out.kv_len, cached = buf[0, 4:7], buf[1, 61:64]
+    cached.copy_(torch.tensor(c["cached"]))
+    m.cache_plan(cached, torch.tensor(c["fresh"], **i32), table, torch.tensor(c["free_blocks"], **i32),
+                 torch.tensor([c["free_count"]], **i32), 16, c["T"], out=out)
+    assert m.check() == m.OK
+    assert table.tolist() == ref["table"].tolist() and out.slot.tolist() == list(ref["slot"])
+    assert out.kv_len.tolist() == ref["kv_len"] and cached.tolist() == c["cached"]
+    with pytest.raises(m.Q4Error):
+        out.kv_len = buf[1, 3:6]
+        m.cache_plan(cached, torch.tensor(c["fresh"], **i32), table, torch.tensor(c["free_blocks"], **i32),
+                     torch.tensor([c["free_count"]], **i32), 16, c["T"], out=out)
+
+
 # ------------------------------------------------------------------- rope
 def rope_case(T, heads, kv, D, rot, S, dtype, inter, seed=0, reach=5000, token_major=False, in_place=False,
               skip=False, factor=1.0, freq=None):

@@ -190,10 +190,8 @@ def test_plan_refuses_outputs_over_other_arrays(lib, out, other):
         assert call(lib.q4_cache_plan, PLAN_APART, list(PLAN), **{other: at}) == BAD
 
 
-def test_plan_checks_the_tables_rows_only(lib):
-    """A wide table whose second row lies over a length array is refused."""
+def test_plan_checks_every_row_of_a_wide_table(lib):
+    """Rows of a table whose stride is far above its width."""
     wide = dict(PLAN_APART, table=P * 100, stride=P // 4)
     for at, name in ((P * 101 + 28, "cached"), (P * 101 - 4, "kv_len"), (P * 103 + 31 - 3, "fresh")):
         assert call(lib.q4_cache_plan, wide, list(PLAN), **{name: at}) == BAD
-    # between the rows nothing is refused for that; a bad size still is, first
-    assert call(lib.q4_cache_plan, wide, list(PLAN), kv_len=P * 101 + 64, T=0) == BAD
