@@ -26,7 +26,7 @@ MHA = {"heads": 32, "kv_heads": 32, "dim": 128}  # the 7B-shaped layer
 MOST = {"int8": 127.0, "e4m3": 448.0}  # the largest code
 # the exponents that keep every value a number of the 16-bit type
 RANGE = {("int8", "f16"): (-24, 9), ("e4m3", "f16"): (-15, 7),
-         ("int8", "bf16"): (-64, 64), ("e4m3", "bf16"): (-64, 64)}
+         ("int8", "bf16"): (-48, 48), ("e4m3", "bf16"): (-48, 48)}
 
 
 # ------------------------------------------------------------------ cases
