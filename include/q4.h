@@ -491,6 +491,103 @@ q4_status q4_attention_timeout_selftest(const void *q, int64_t q_stride, int64_t
  * invalid sizes). */
 size_t q4_attention_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads, int64_t head_dim);
 
+/* ------------------------------------------------------------------------
+ * The same with the cache in 8 bits: half the bytes that a decode step reads.
+ * q4_rope_append8 quantises keys and values as it writes them, q4_attention8
+ * runs over the codes, q4_cache_read8 reads tokens back.  The step's plan
+ * (q4_cache_plan) is the same.
+ *
+ * Codes are signed integers (Q4_I8: -127..127) or e4m3 numbers (Q4_E4M3: four
+ * exponent and three mantissa bits, to +-448, no infinity).  All tokens of one
+ * block share one power-of-two scale per head, keys and values apart: a code c
+ * stands for c * 2^e, with e + 127 the byte k_exp[block * heads + head]
+ * (v_exp).  e lies in
+ *     F16   [-24, 9] for Q4_I8, [-15, 7] for Q4_E4M3
+ *     BF16  [-48, 48]
+ * (a byte outside counts as the nearest end), so that every c * 2^e is a number
+ * of the 16-bit type: an 8-bit cache is a 16-bit cache whose values lie on a
+ * grid.  int8 keeps a step of 2^e for all, under 1/63 of the block's largest
+ * magnitude; e4m3 keeps 2^-4 of each value, down to 2^-6 * 2^e.
+ * ---------------------------------------------------------------------- */
+typedef enum { Q4_I8 = 0, Q4_E4M3 = 1 } q4_code;
+
+typedef struct {
+    void *k, *v;             /* device, 16-byte aligned, not the same */
+    uint8_t *k_exp, *v_exp;  /* device, [blocks][heads] each, not overlapping */
+    q4_code code;
+    q4_dtype type;           /* of queries and of values read back: Q4_BF16 or Q4_F16 */
+    int64_t blocks;          /* 1 .. 2^31 - 1 */
+    int64_t heads;           /* KV heads */
+    int64_t block_size;      /* tokens per block, a multiple of 16 */
+    int64_t head_dim;        /* a multiple of 16, at most 128 */
+    /* strides of k and v alike, in codes (bytes), multiples of 16 below 2^39;
+     * the head_dim codes of a token are contiguous */
+    int64_t block_stride, head_stride, token_stride;
+} q4_kv_cache8;
+
+/*
+ * q4_rope_append into an 8-bit cache: same arguments, queries, angles and
+ * refusals (the angles' fractions of a turn are kept in 64-bit integers).
+ * Keys are rotated in f32 and quantised from there; values as they are.
+ * Consecutive token rows with consecutive slots of one block form a run (as
+ * q4_cache_plan lays them out).  For a run that begins at offset o0 of its
+ * block, and each head:
+ *     need = the least e of the range with max |x| <= M * 2^e over the run's
+ *            finite x (M = 127 or 448); the range's end where none is
+ *     e    = need when o0 = 0, else max(need, the block's e)
+ * The run's codes are x / 2^e to the nearest code (ties to even), beyond +-M the
+ * end; NaN becomes 0.  Where e grows, the codes at offsets 0 .. o0 - 1 are
+ * rounded again, c / 2^(growth) to the nearest: as e grows by whole powers of
+ * two, all roundings of an int8 code together are off by less than one step of
+ * the last scale, and e4m3 numbers change only where they become subnormal.
+ * What lies behind a run in its block is left alone and not looked at.  A
+ * token's offset 0 begins the block anew, whatever it held.  No two runs of a
+ * call may share a block, and a slot outside the cache is skipped.
+ */
+q4_status q4_rope_append8(const void *qkv, int64_t qkv_stride, int64_t T, int64_t Hq, int64_t rot,
+                          q4_rope_style style, const double *freq, float factor,
+                          const int32_t *position, const int64_t *slot, void *q_out,
+                          int64_t q_stride, const q4_kv_cache8 *cache, q4_stream_t stream);
+
+/*
+ * Reads tokens of requests back, c * 2^e.  Rows and places are those of
+ * q4_attention: row t = q_start[b] + i of request b (n rows) stands for the
+ * token at place kv_len[b] - n + i, so that q_start = the running sum of kv_len
+ * reads whole requests and a step's own q_start its new tokens.  k_out, v_out:
+ * T rows of heads * head_dim elements (strides k_stride, v_stride) of type ot:
+ * the cache's type, which holds every value, or F32.  Rows that belong to no
+ * request are left alone; a place before the first token, or in a block outside
+ * the cache, gives zeros.  Lengths are cut to the table's width, as there.
+ * INVALID_ARG for NULL pointers, sizes < 1, strides shorter than a row, a bad
+ * cache; UNSUPPORTED for types and sizes beyond the limits of q4_attention;
+ * MISALIGNED unless k_out and v_out are 16-byte aligned and strides multiples
+ * of 8.
+ */
+q4_status q4_cache_read8(const q4_kv_cache8 *cache, const int32_t *table, int64_t table_stride,
+                         int64_t width, const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                         int64_t T, void *k_out, int64_t k_stride, void *v_out, int64_t v_stride,
+                         q4_dtype ot, q4_stream_t stream);
+
+/*
+ * q4_attention over an 8-bit cache: the same arguments, rows, masks, results,
+ * refusals and workspace rule, with k_j and v_j the values that the codes stand
+ * for.  The codes are widened to 16 bits exactly and products summed in f32 by
+ * the tensor cores.
+ * Workspace: q4_attention8_workspace_bytes; one of the larger size may serve
+ * q4_attention and q4_attention8 calls of one stream in turn.  Codes behind a
+ * request's end and before every row's window never matter; the two e4m3 codes
+ * that are NaN, which the append never writes, are not specified.
+ */
+q4_status q4_attention8(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                        const q4_kv_cache8 *cache, const int32_t *table, int64_t table_stride,
+                        int64_t width, const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                        int64_t max_fresh, float scale, int64_t window, void *o, q4_dtype ot,
+                        int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes,
+                        q4_stream_t stream);
+
+/* Workspace bytes of q4_attention8, as q4_attention_workspace_bytes. */
+size_t q4_attention8_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads, int64_t head_dim);
+
 /* Synchronises `stream` and reports errors raised on the device since the
  * last check: Q4_ERR_BOUNDS when, in a library built with -DQ4_DEBUG, a
  * kernel computed a global store outside the buffer it writes (the store was

@@ -1,0 +1,331 @@
+"""q4_attention8 against the definition in 64 bits over the values that the
+codes stand for: codes, types, head layouts, lengths from one token up, odd
+sizes, both cache layouts, windows, rows that see nothing, garbage in unused
+codes, scales far apart, splits over CTAs, streams, graphs, shared workspaces.
+Tolerances: serving_ref.py (weights are rounded to 16 bits there too)."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from cache8_ref import CODES, Requests8, raw
+from serving_ref import assert_attention
+
+pytestmark = pytest.mark.gpu
+DT = [torch.bfloat16, torch.float16]
+
+
+def q4():
+    import weight_only_int4_group_gb300 as m
+    return m
+
+
+def run(r, window=0, scale=None, out_dtype=None, ws=None, max_fresh=None, **kw):
+    m = q4()
+    o, lse = m.attention(r.q, r.cache(), r.table, r.q_start, r.kv_len, max_fresh or r.max_fresh, scale=scale,
+                         window=window, out_dtype=out_dtype, return_lse=True, ws=ws, **kw)
+    assert m.check() == m.OK
+    return o, lse
+
+
+def check(r, window=0, scale=None, **kw):
+    o, lse = run(r, window, scale, **kw)
+    assert_attention(o, lse, r.reference(scale, window), f"{r.lengths} window {window}")
+    return o, lse
+
+
+FEW = [
+    [(0, 1)],
+    [(15, 1)], [(16, 1)], [(17, 1)],
+    [(127, 1)], [(128, 1)], [(129, 1)],
+    [(776, 1)],
+    [(5000, 1)],
+    [(3, 2), (100, 1), (0, 1), (31, 3)],
+    [(0, 0), (64, 1), (0, 0), (7, 1), (300, 0)],
+    [(i * 37 % 500, 1) for i in range(70)],
+]
+MANY = [
+    [(0, 17)], [(0, 128)], [(0, 129)], [(5, 64)],
+    [(0, 300)], [(777, 100)], [(1000, 257)],
+    [(0, 130), (50, 1), (0, 0), (400, 65), (3, 33)],
+    [(127, 1), (128, 128), (129, 2)],
+]
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("lengths", FEW, ids=lambda x: str(x)[:24])
+@pytest.mark.parametrize("heads,kv", [(8, 1), (4, 4), (14, 2), (16, 1)])
+def test_few_rows(lengths, heads, kv, dtype, code):
+    check(Requests8(lengths, heads, kv, 128, 16, dtype, code, seed=len(lengths)))
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("lengths", MANY, ids=lambda x: str(x)[:24])
+@pytest.mark.parametrize("heads,kv", [(8, 1), (2, 2), (14, 2)])
+def test_many_rows(lengths, heads, kv, dtype, code):
+    check(Requests8(lengths, heads, kv, 128, 16, dtype, code, seed=len(lengths)))
+
+
+@pytest.mark.parametrize("D", [16, 32, 48, 64, 80, 96, 112, 128])
+@pytest.mark.parametrize("lengths", [[(200, 1), (33, 1)], [(200, 40), (0, 150)]], ids=["few", "many"])
+def test_head_dims(D, lengths):
+    for dtype in DT:
+        for code in CODES:
+            check(Requests8(lengths, 6, 2, D, 32, dtype, code, seed=D))
+
+
+@pytest.mark.parametrize("S", [16, 32, 48, 64, 80, 128, 256, 400])
+@pytest.mark.parametrize("token_major", [False, True])
+def test_block_sizes_and_layouts(S, token_major):
+    for code in CODES:
+        for lengths in ([(S, 1), (2 * S + 1, 1), (S - 2, 1)], [(S - 1, 70), (3 * S, 20), (0, 5)]):
+            check(Requests8(lengths, 8, 2, 64, S, torch.float16, code, seed=S, token_major=token_major))
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 128, 129, 1000, 2 ** 31 - 1, 2 ** 40])
+@pytest.mark.parametrize("lengths", [[(500, 1), (20, 1), (0, 1)], [(500, 140), (0, 260), (90, 1)]],
+                         ids=["few", "many"])
+def test_windows(window, lengths):
+    check(Requests8(lengths, 8, 2, 128, 16, torch.bfloat16, torch.int8, seed=3), window)
+    check(Requests8(lengths, 4, 4, 64, 32, torch.float16, torch.float8_e4m3fn, seed=4), window)
+
+
+@pytest.mark.parametrize("heads", [1, 3, 9, 16, 17, 33, 64, 100, 128, 200])
+def test_one_kv_head_for_all(heads):
+    for code in CODES:
+        for lengths in ([(90, 1), (300, 1)], [(90, 5), (0, 9)]):
+            check(Requests8(lengths, heads, 1, 64, 16, torch.bfloat16, code, seed=heads))
+
+
+@pytest.mark.parametrize("lengths", [[(40, 1), (0, 2)], [(40, 30), (0, 200)]], ids=["few", "many"])
+@pytest.mark.parametrize("dtype", DT)
+def test_f32_output_and_scales(lengths, dtype):
+    r = Requests8(lengths, 4, 2, 128, 16, dtype, torch.int8, seed=5)
+    for scale in (0.0, 0.3, -0.2, 1e-6):
+        o, lse = run(r, scale=scale, out_dtype=torch.float32)
+        assert o.dtype == torch.float32
+        assert_attention(o, lse, r.reference(scale), f"scale {scale}")
+
+
+@pytest.mark.parametrize("lengths", [[(400, 1), (70, 1)], [(400, 200), (70, 33)]], ids=["few", "many"])
+@pytest.mark.parametrize("code", CODES)
+def test_peaked_and_growing_scores(lengths, code):
+    """Scores of hundreds whose maximum keeps rising along the keys."""
+    r = Requests8(lengths, 4, 1, 64, 16, torch.float16, code, seed=6, q_scale=8.0)
+    check(r)
+    r.q.fill_(1.0)
+    for b, L in enumerate(r.total):
+        for j in range(L):
+            blk = r.table[b, j // 16].item()
+            e = max(0, (j // 16).bit_length() - 3)
+            r.k_exp[blk] = 127 + e
+            value = torch.tensor(j / 16 / 2 ** e, device="cuda")
+            raw(r.k)[blk, :, j % 16] = raw(value.round().to(torch.int8) if code == torch.int8 else value.to(code)).item()
+    check(r)
+    check(r, scale=-0.125)
+
+
+@pytest.mark.parametrize("lengths", [[(700, 1), (70, 2)], [(700, 100), (70, 33)]], ids=["few", "many"])
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DT)
+def test_scales_far_apart(lengths, dtype, code):
+    """Blocks whose values differ by many powers of two, and keys likewise: a
+    large scale with a negligible weight may not cost the others' precision."""
+    span = (-12, 6) if dtype == torch.float16 else (-30, 20)
+    r = Requests8(lengths, 4, 2, 128, 16, dtype, code, seed=11, exps=span)
+    r.k_exp.copy_(torch.randint(127 - 10, 127 - 3, r.k_exp.shape, device="cuda"))
+    check(r)
+    # the largest values only where the weights are smallest
+    r.q.fill_(1.0)
+    raw(r.k).fill_(raw(torch.ones((), device="cuda").to(code)).item())
+    r.k_exp.fill_(127)
+    r.v_exp.fill_(127 + span[0])
+    for b, L in enumerate(r.total):
+        blk = r.table[b, 1].item()
+        r.v_exp[blk] = 127 + span[1]
+        raw(r.k)[blk] = raw(torch.full((), -1.0, device="cuda").to(code)).item()
+    check(r)
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("code", CODES)
+def test_rows_that_see_nothing(many, code):
+    n = 150 if many else 4
+    r = Requests8([(0, n), (60, n), (0, n)], 4, 2, 64, 16, torch.bfloat16, code, seed=7)
+    short = [n - 3, 60 + n, 0]
+    r.kv_len.copy_(torch.tensor(short, dtype=torch.int32))
+    o, lse = run(r)
+    assert (o[:3] == 0).all() and torch.isinf(lse[:3]).all()
+    assert (o[2 * n:] == 0).all() and torch.isinf(lse[2 * n:]).all()
+    r.total = short
+    assert_attention(o, lse, r.reference(), "short")
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_hint_does_not_change_what_is_computed(many):
+    """Any number of new tokens is right with either kernel."""
+    r = Requests8([(300, 40), (20, 1), (0, 9)], 8, 2, 128, 16, torch.bfloat16, torch.int8, seed=8)
+    ws = q4().attention_workspace(1 if not many else 64, 8, 2, 128, eight_bit=True)
+    check(r, max_fresh=1 if not many else 64, ws=ws)
+
+
+def test_equals_the_16_bit_attention_within_rounding():
+    """The same values in a 16-bit cache."""
+    m = q4()
+    for lengths in ([(900, 1), (33, 2)], [(900, 200), (0, 70)]):
+        for code in CODES:
+            r = Requests8(lengths, 8, 2, 128, 16, torch.bfloat16, code, seed=2)
+            k, v = (x.to(torch.bfloat16) for x in r.values())
+            o8, l8 = run(r, out_dtype=torch.float32)
+            o, l = m.attention(r.q, m.KVCache(k, v), r.table, r.q_start, r.kv_len, r.max_fresh, return_lse=True,
+                               out_dtype=torch.float32)
+            # 2 * 2^-8 on the weights
+            assert ((o8 - o).abs() <= 2 ** -7 * v.double().abs().nan_to_num().max()).all()
+            assert ((l8 - l).abs() <= 1e-4).all()
+
+
+def test_rows_of_no_request_and_strides():
+    m = q4()
+    for lengths, pad in (([(50, 1), (9, 1)], 3), ([(50, 60), (9, 30)], 5)):
+        r = Requests8(lengths, 4, 2, 64, 16, torch.float16, torch.float8_e4m3fn, seed=1)
+        T = r.T + pad
+        qbig = torch.zeros(T, 4 * 64 + 8, dtype=torch.float16, device="cuda")
+        qbig[:r.T, :256] = r.q.flatten(1)
+        obig = torch.full((T, 4 * 64 + 16), 5.0, dtype=torch.float16, device="cuda")
+        m.attention(qbig[:, :256].unflatten(1, (4, 64)), r.cache(), r.table, r.q_start, r.kv_len, r.max_fresh,
+                    out=obig[:, :256].unflatten(1, (4, 64)))
+        want, _ = run(r)
+        assert torch.equal(obig[:r.T, :256].unflatten(1, (4, 64)), want)
+        assert (obig[r.T:] == 5).all() and (obig[:, 256:] == 5).all()
+
+
+def test_bad_device_data():
+    """Table entries outside the cache are keys of score 0 and value 0; lengths and
+    row starts of any kind stay within the buffers."""
+    m = q4()
+    for lengths in ([(60, 1), (40, 2)], [(60, 50), (40, 70)]):
+        r = Requests8(lengths, 4, 2, 64, 16, torch.bfloat16, torch.int8, seed=4)
+        r.table[0, 1] = -3
+        r.table[1, 0] = 2 ** 31 - 1
+        good = r.table.clone()
+        # the reference: a spare block of zeros in their place
+        spare = next(i for i in range(r.k.shape[0]) if i not in set(good[good >= 0].tolist()))
+        raw(r.k)[spare] = 0
+        raw(r.v)[spare] = 0
+        o, lse = run(r)
+        r.table[0, 1] = r.table[1, 0] = spare
+        assert_attention(o, lse, r.reference(), "outside")
+        for lens, starts in (([10 ** 9, -5], r.start), ([2 ** 31 - 1] * 2, [0, 10 ** 9, 2 ** 31 - 1]),
+                             (r.total, [-9, 90, 5]), (r.total, [r.T, 1, 0])):
+            m.attention(r.q, r.cache(), good, torch.tensor(starts, dtype=torch.int32, device="cuda"),
+                        torch.tensor(lens, dtype=torch.int32, device="cuda"), r.max_fresh)
+            assert m.check() == m.OK
+
+
+def test_long_context_split_over_all_workers():
+    for heads, kv in ((1, 1), (8, 1), (16, 1)):
+        check(Requests8([(70000, 1)], heads, kv, 128, 64, torch.bfloat16, torch.int8, seed=heads))
+    check(Requests8([(30000, 3), (5, 1)], 8, 1, 64, 16, torch.float16, torch.float8_e4m3fn, seed=5))
+    check(Requests8([(9000, 300)], 4, 1, 128, 16, torch.bfloat16, torch.float8_e4m3fn, seed=5))
+
+
+def test_one_workspace_for_calls_of_both_kinds_and_repeats():
+    m = q4()
+    sizes = [(1, [(5000, 1)]), (150, [(700, 150), (3, 20)]), (1, [(i * 13, 1) for i in range(40)]), (40, [(2000, 40)])]
+    ws = max((m.attention_workspace(n, 8, 2, 128, eight_bit=e) for n, _ in sizes for e in (False, True)),
+             key=lambda t: t.numel())
+    outs = {}
+    for turn in range(2):
+        for i, (n, lengths) in enumerate(sizes):
+            r = Requests8(lengths, 8, 2, 128, 16, torch.bfloat16, CODES[i % 2], seed=i)
+            o, lse = check(r, ws=ws)
+            k, v = (x.to(torch.bfloat16) for x in r.values())
+            m.attention(r.q, m.KVCache(k, v), r.table, r.q_start, r.kv_len, r.max_fresh, ws=ws)
+            if turn:
+                assert torch.equal(outs[i][0], o) and torch.equal(outs[i][1], lse)
+            outs[i] = (o, lse)
+    torch.cuda.synchronize()
+    assert int(ws[:131072].count_nonzero()) == 0
+
+
+def test_streams_and_graphs():
+    m = q4()
+    for lengths in ([(3000, 1), (100, 1)], [(3000, 90), (100, 33)]):
+        r = Requests8(lengths, 8, 2, 128, 16, torch.bfloat16, torch.int8, seed=9)
+        want, wl = run(r)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        o, l = m.attention(r.q, r.cache(), r.table, r.q_start, r.kv_len, r.max_fresh, return_lse=True, stream=side)
+        side.synchronize()
+        assert torch.equal(o, want) and torch.equal(l, wl)
+        ws = m.attention_workspace(r.max_fresh, 8, 2, 128, eight_bit=True)
+        cache = r.cache()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o, l = m.attention(r.q, cache, r.table, r.q_start, r.kv_len, r.max_fresh, return_lse=True, ws=ws)
+        for _ in range(3):
+            o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, want) and torch.equal(l, wl)
+        # other lengths in the same graph
+        r.kv_len.copy_(torch.tensor([2000 + lengths[0][1], lengths[1][1]], dtype=torch.int32))
+        r.total = r.kv_len.tolist()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_attention(o, l, r.reference(), "replayed")
+    assert m.check() == m.OK
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_a_layer_in_8_bits(code):
+    """Plan, quantising append, attention and read-back together, as a server
+    runs them: a prompt step, then decode steps in a graph."""
+    m = q4()
+    heads, kv, D, S, B = 8, 2, 128, 16, 3
+    prompts = [70, 5, 33]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    length, table = torch.zeros(B, **i32), torch.full((B, 12), -1, **i32)
+    free, count = torch.arange(36, **i32), torch.full((1,), 36, **i32)
+    cache = m.KVCache8.empty(36, kv, S, D, code)
+    freq, factor = m.rope_frequencies(D)
+    ws = m.attention_workspace(max(prompts), heads, kv, D, eight_bit=True)
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def step(x, fresh, T, most, plan=None):
+        p = m.cache_plan(length, fresh, table, free, count, S, T, out=plan)
+        length.copy_(p.kv_len)
+        count.copy_(p.counts[2:3])
+        q = m.rope_append(x, cache, p.position, p.slot, freq, heads, factor=factor)
+        return q, m.attention(q, cache, table, p.q_start, p.kv_len, most, ws=ws), p
+
+    def reference(q, p):
+        from serving_ref import attention_reference
+        start = torch.cumsum(torch.cat([torch.zeros(1, **i32), p.kv_len]), 0).int()
+        k, v = m.cache_read(cache, table, start, p.kv_len, int(start[-1]))
+        # the values read back as requests' own blocks of a 64-bit cache
+        L = p.kv_len.tolist()
+        W = max(L)
+        kk, vv = (torch.zeros(B, kv, W, D, dtype=torch.float64, device="cuda") for _ in "kv")
+        for b in range(B):
+            kk[b, :, :L[b]] = k[start[b]:start[b + 1]].double().transpose(0, 1)
+            vv[b, :, :L[b]] = v[start[b]:start[b + 1]].double().transpose(0, 1)
+        return attention_reference(q, kk, vv, torch.arange(B, device="cuda")[:, None], p.q_start.tolist(), L, D ** -0.5, 0)
+
+    x = torch.randn(sum(prompts), (heads + 2 * kv) * D, generator=g, device="cuda").bfloat16()
+    q, o, p = step(x, torch.tensor(prompts, **i32), len(x), max(prompts))
+    assert_attention(o, None, reference(q, p), "prompt")
+    x, one = x[:B].clone(), torch.ones(B, **i32)
+    plan = m.CachePlan.empty(B, B)
+    step(x, one, B, 1, plan)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, o, p = step(x, one, B, 1, plan)
+    for _ in range(20):
+        x.normal_(generator=g)
+        graph.replay()
+        assert_attention(o, None, reference(q, p), "decode")
+    assert length.tolist() == [n + 21 for n in prompts] and m.check() == m.OK

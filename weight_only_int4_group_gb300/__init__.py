@@ -9,7 +9,8 @@ Names follow include/q4.h: quantize, quantize_sym, repack, unpack, xsum,
 gemv, gemm, check, weight_bytes, gemv_workspace_bytes, gemm_workspace_bytes,
 repack_compact, unpack_compact, gemv_noalloc and the two timeout
 self-tests; the serving operators cache_plan, rope_append and attention over
-a KVCache (rope_frequencies makes their angles).  A QWeight carries its layout (TILED or COMPACT), and every
+a KVCache, or in 8 bits over a KVCache8 with cache_read (rope_frequencies makes
+their angles).  A QWeight carries its layout (TILED or COMPACT), and every
 product call passes that layout and the buffer's byte count to the library,
 which refuses a mismatch.
 """
@@ -38,6 +39,8 @@ LAYOUT_TILED, LAYOUT_COMPACT = 1, 2
 PATH_AUTO, PATH_FMA, PATH_MMA = 0, 1, 2
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+I8, E4M3 = 0, 1
+_CODE = {torch.int8: I8, torch.float8_e4m3fn: E4M3}
 
 
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
@@ -50,6 +53,14 @@ class _KVCacheArg(ctypes.Structure):
                 ("block_size", ctypes.c_int64), ("head_dim", ctypes.c_int64),
                 ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("token_stride", ctypes.c_int64)]
+
+
+class _KVCache8Arg(ctypes.Structure):
+    """q4_kv_cache8."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp")] + [
+        ("code", ctypes.c_int), ("type", ctypes.c_int)] + [
+        (n, ctypes.c_int64) for n in ("blocks", "heads", "block_size", "head_dim", "block_stride",
+                                      "head_stride", "token_stride")]
 
 
 class Q4Error(RuntimeError):
@@ -94,6 +105,12 @@ def _load():
     lib.q4_attention_timeout_selftest.argtypes = lib.q4_attention.argtypes
     lib.q4_attention_workspace_bytes.argtypes = [I, I, I, I]
     lib.q4_attention_workspace_bytes.restype = Z
+    C8 = ctypes.POINTER(_KVCache8Arg)
+    lib.q4_rope_append8.argtypes = [P, I, I, I, I, S, P, F, P, P, P, I, C8, P]
+    lib.q4_cache_read8.argtypes = [C8, P, I, I, P, P, I, I, P, I, P, I, S, P]
+    lib.q4_attention8.argtypes = [P, I, I, I, C8, P, I, I, P, P, I, I, F, I, P, S, I, P, P, Z, P]
+    lib.q4_attention8_workspace_bytes.argtypes = [I, I, I, I]
+    lib.q4_attention8_workspace_bytes.restype = Z
     lib.q4_check.argtypes = [P]
     lib.q4_debug_bounds_selftest.argtypes = [P, P]
     lib.q4_status_str.argtypes = [S]
@@ -103,7 +120,7 @@ def _load():
               "q4_unpack_compact", "q4_xsum", "q4_gemv", "q4_gemv_path", "q4_gemv_timeout_selftest",
               "q4_gemm", "q4_gemm_timeout_selftest", "q4_gemv_noalloc", "q4_check",
               "q4_cache_plan", "q4_rope_append", "q4_attention",
-              "q4_attention_timeout_selftest",
+              "q4_attention_timeout_selftest", "q4_rope_append8", "q4_cache_read8", "q4_attention8",
               "q4_debug_bounds_selftest"):
         getattr(lib, f).restype = S
     return lib
@@ -380,6 +397,9 @@ class KVCache:
     (a [blocks][block_size][heads][head_dim] buffer is passed as
     ``t.transpose(1, 2)``).  The tensors are used where they lie."""
 
+    _append, _append_name = _lib.q4_rope_append, "q4_rope_append"
+    _attend, _attend_name, _eight_bit = _lib.q4_attention, "q4_attention", False
+
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         for t, n in ((k, "k"), (v, "v")):
             if not t.is_cuda:
@@ -402,6 +422,50 @@ class KVCache:
         device = device or torch.cuda.current_device()
         return cls(torch.empty(shape, dtype=dtype, device=device),
                    torch.empty(shape, dtype=dtype, device=device))
+
+
+class KVCache8:
+    """A blocked KV cache in 8 bits (q4_kv_cache8): codes k and v, int8 or
+    float8_e4m3fn [blocks][heads][block_size][head_dim], with the layouts that
+    KVCache takes, and the exponents of their scales, uint8 [blocks][heads]: a
+    code c stands for c * 2 ** (exp - 127).  ``dtype``: of queries and of values
+    read back, bfloat16 or float16.  rope_append quantises into it, attention
+    reads it and cache_read gives its values."""
+
+    _append, _append_name = _lib.q4_rope_append8, "q4_rope_append8"
+    _attend, _attend_name, _eight_bit = _lib.q4_attention8, "q4_attention8", True
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor,
+                 dtype=torch.bfloat16):
+        for t, n in ((k, "k"), (v, "v"), (k_exp, "k_exp"), (v_exp, "v_exp")):
+            if not t.is_cuda:
+                raise ValueError(f"{n} must be a CUDA tensor")
+            if t.device != k.device:
+                raise ValueError("all tensors of a cache must lie on one device")
+        if k.dim() != 4 or k.dtype not in _CODE:
+            raise ValueError("k must be a 4-D int8 or float8_e4m3fn tensor")
+        if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must have the same shape, strides and type")
+        if k.shape[3] > 1 and k.stride(3) != 1:
+            raise ValueError("the last dimension must be contiguous")
+        for t, n in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+            if t.shape != k.shape[:2] or t.dtype != torch.uint8 or not t.is_contiguous():
+                raise ValueError(f"{n} must be a contiguous uint8 tensor [blocks][heads]")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("dtype must be bfloat16 or float16")
+        self.k, self.v, self.k_exp, self.v_exp, self._on = k, v, k_exp, v_exp, k.get_device()
+        self.dtype, (_, self.heads, self.block_size, self.head_dim) = dtype, k.shape
+        self._arg = _KVCache8Arg(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), _CODE[k.dtype],
+                                 _DTYPE[dtype], *k.shape, *k.stride()[:3])
+        self._ref = ctypes.byref(self._arg)
+
+    @classmethod
+    def empty(cls, blocks: int, heads: int, block_size: int, head_dim: int, code=torch.int8,
+              dtype=torch.bfloat16, device=None) -> "KVCache8":
+        shape = (blocks, heads, block_size, head_dim)
+        device = device or torch.cuda.current_device()
+        return cls(*(torch.empty(shape, dtype=code, device=device) for _ in "kv"),
+                   *(torch.zeros(shape[:2], dtype=torch.uint8, device=device) for _ in "kv"), dtype)
 
 
 @dataclass
@@ -531,13 +595,14 @@ def rope_frequencies(rot: int, base: float = 10000.0, stretch: float = 1.0, by_p
     return torch.tensor(f, dtype=torch.float64, device=device), factor
 
 
-def rope_append(qkv: torch.Tensor, cache: KVCache, position: torch.Tensor, slot: torch.Tensor,
+def rope_append(qkv: torch.Tensor, cache: KVCache | KVCache8, position: torch.Tensor, slot: torch.Tensor,
                 freq: torch.Tensor, heads: int, interleaved: bool = False, factor: float = 1.0,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rotate the queries and keys of ``qkv`` [T][(heads + 2 * cache.heads) *
     head_dim] and append keys and values to the cache (q4_rope_append).
     2 * len(freq) elements of each head turn.  Returns the queries
-    [T][heads][head_dim] (``out`` may be the query part of qkv itself)."""
+    [T][heads][head_dim] (``out`` may be the query part of qkv itself).  Into a
+    KVCache8 keys and values go quantised (q4_rope_append8)."""
     dev = _current_device()
     if cache._on != dev:
         _elsewhere("cache", cache._on, dev)
@@ -549,29 +614,56 @@ def rope_append(qkv: torch.Tensor, cache: KVCache, position: torch.Tensor, slot:
     op, To, no, ostride = _rows(out, "out", cache.dtype, dev)
     if To != T or no != heads * cache.head_dim:
         raise ValueError("out must be T rows of heads * head_dim")
-    _ok(_lib.q4_rope_append(qp, stride, T, heads, 2 * freq.numel(), ROPE_INTERLEAVED if interleaved else ROPE_HALF,
-                            _array(freq, "freq", torch.float64, dev), factor, _array(position, "position", torch.int32, dev, T),
-                            _array(slot, "slot", torch.int64, dev, T), op, ostride, cache._ref,
-                            _raw_stream(stream, dev)), "q4_rope_append")
+    _ok(cache._append(qp, stride, T, heads, 2 * freq.numel(), ROPE_INTERLEAVED if interleaved else ROPE_HALF,
+                      _array(freq, "freq", torch.float64, dev), factor, _array(position, "position", torch.int32, dev, T),
+                      _array(slot, "slot", torch.int64, dev, T), op, ostride, cache._ref,
+                      _raw_stream(stream, dev)), cache._append_name)
     return out
 
 
-def attention_workspace_bytes(max_fresh: int, heads: int, kv_heads: int, head_dim: int) -> int:
-    return int(_lib.q4_attention_workspace_bytes(max_fresh, heads, kv_heads, head_dim))
+def cache_read(cache: KVCache8, table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, T: int,
+               out: tuple[torch.Tensor, torch.Tensor] | None = None, out_dtype=None, stream=None):
+    """Reads tokens back from an 8-bit cache (q4_cache_read8): (k, v), T rows
+    [heads][head_dim] each, of the cache's dtype or float32.  Rows q_start[b] ..
+    q_start[b + 1] are request b's last tokens of the kv_len[b] it holds, in
+    order: all of them where q_start is the running sum of kv_len."""
+    if not isinstance(cache, KVCache8):
+        raise TypeError("cache must be a KVCache8: a 16-bit cache holds its values as they are")
+    dev = _current_device()
+    if cache._on != dev:
+        _elsewhere("cache", cache._on, dev)
+    B = kv_len.numel()
+    tp, ts, width = _table(table, B, dev)
+    if out is None:
+        shape = (T, cache.heads, cache.head_dim)
+        out = tuple(_empty(shape, out_dtype or cache.dtype, table.device, stream) for _ in "kv")
+    (kp, Tk, nk, ks), (vp, Tv, nv, vs) = (_rows(t, "out", out[0].dtype, dev) for t in out)
+    if Tk != T or Tv != T or nk != cache.heads * cache.head_dim or nv != nk:
+        raise ValueError("out must be two tensors of T rows of heads * head_dim")
+    _ok(_lib.q4_cache_read8(cache._ref, tp, ts, width, _array(q_start, "q_start", torch.int32, dev, B + 1),
+                            _array(kv_len, "kv_len", torch.int32, dev, B), B, T, kp, ks, vp, vs,
+                            _DTYPE.get(out[0].dtype, -1), _raw_stream(stream, dev)), "q4_cache_read8")
+    return out
+
+
+def attention_workspace_bytes(max_fresh: int, heads: int, kv_heads: int, head_dim: int, eight_bit: bool = False) -> int:
+    fn = _lib.q4_attention8_workspace_bytes if eight_bit else _lib.q4_attention_workspace_bytes
+    return int(fn(max_fresh, heads, kv_heads, head_dim))
 
 
 def attention_workspace(max_fresh: int, heads: int, kv_heads: int, head_dim: int,
-                        device=None) -> torch.Tensor | None:
-    """A zero-filled workspace for attention (not shared with the products')."""
-    return _zeros(attention_workspace_bytes(max_fresh, heads, kv_heads, head_dim), device)
+                        device=None, eight_bit: bool = False) -> torch.Tensor | None:
+    """A zero-filled workspace for attention (not shared with the products'),
+    ``eight_bit``: over a KVCache8."""
+    return _zeros(attention_workspace_bytes(max_fresh, heads, kv_heads, head_dim, eight_bit), device)
 
 
-def attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: torch.Tensor,
+def attention(q: torch.Tensor, cache: KVCache | KVCache8, table: torch.Tensor, q_start: torch.Tensor,
               kv_len: torch.Tensor, max_fresh: int, scale: float | None = None, window: int = 0,
               out: torch.Tensor | None = None, out_dtype=None, return_lse: bool = False,
-              lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None,
-              _call=_lib.q4_attention):
-    """Attention of each request's new tokens over its cache (q4_attention).
+              lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None, _call=None):
+    """Attention of each request's new tokens over its cache (q4_attention;
+    q4_attention8 over a KVCache8).
 
     q [T][heads][head_dim]; request b's rows are q_start[b]..q_start[b + 1],
     its keys the kv_len[b] first tokens of table row b, its own new ones last.
@@ -598,12 +690,12 @@ def attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: tor
         lse = _empty((T, heads), torch.float32, q.device, stream)
     if ws is None:
         with _on(stream if stream is not None else torch.cuda.current_stream()):
-            ws = attention_workspace(max_fresh, heads, cache.heads, D, q.device)
-    _ok(_call(qp, stride, T, heads, cache._ref, tp, ts, width, _array(q_start, "q_start", torch.int32, dev, B + 1),
+            ws = attention_workspace(max_fresh, heads, cache.heads, D, q.device, cache._eight_bit)
+    _ok((_call or cache._attend)(qp, stride, T, heads, cache._ref, tp, ts, width, _array(q_start, "q_start", torch.int32, dev, B + 1),
               _array(kv_len, "kv_len", torch.int32, dev, B), B, max_fresh, D ** -0.5 if scale is None else scale, window,
               op, _DTYPE.get(out.dtype, -1), ostride,
               0 if lse is None else _array(lse, "lse", torch.float32, dev, T * heads),
-              *_ws(ws), _raw_stream(stream, dev)), "q4_attention")
+              *_ws(ws), _raw_stream(stream, dev)), cache._attend_name)
     return (out, lse) if lse is not None else out
 
 

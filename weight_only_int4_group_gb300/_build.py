@@ -39,6 +39,8 @@ SOURCES = {
     "cache.cu": [],
     "attention.cu": [],
     "attention_tc.cu": [],
+    "cache8.cu": [],
+    "attention8.cu": [],
 }
 
 

@@ -159,13 +159,16 @@ static q4_status gemv_common(const void *x, q4_dtype xt, int64_t M, int64_t N, i
 constexpr int64_t INT_MOST = 2147483647;
 
 // The cache's fields, in the order that decides which status is returned.
-static q4_status cache_ok(const q4_kv_cache *c)
+// head_dim and the strides count elements (codes) and are multiples of `unit`:
+// the 16 bytes that the kernels load.
+template <typename Cache>
+static q4_status cache_fields_ok(const Cache *c, int unit)
 {
     if (!c || !c->k || !c->v || c->blocks < 1 || c->heads < 1 || c->block_size < 1 || c->head_dim < 1)
         return Q4_ERR_INVALID_ARG;
     if (c->type != Q4_BF16 && c->type != Q4_F16) return Q4_ERR_UNSUPPORTED;
     if (c->blocks > INT_MOST || c->heads > 65536 || c->block_size > 65536 || c->block_size % 16 ||
-        c->head_dim > 128 || c->head_dim % 8)
+        c->head_dim > 128 || c->head_dim % unit)
         return Q4_ERR_UNSUPPORTED;
     constexpr int64_t most = 1LL << 40;  // elements; keeps every offset far inside 64 bits
     if (c->block_stride < 0 || c->head_stride < 0 || c->token_stride < c->head_dim ||
@@ -184,11 +187,47 @@ static q4_status cache_ok(const q4_kv_cache *c)
         if (x.stride >= (1LL << 39) || x.stride > (1LL << 60) / x.n) return Q4_ERR_UNSUPPORTED;
         extent += (x.n - 1) * x.stride;
     }
-    if (!aligned16(c->k) || !aligned16(c->v) || c->block_stride % 8 || c->head_stride % 8 ||
-        c->token_stride % 8)
+    if (!aligned16(c->k) || !aligned16(c->v) || c->block_stride % unit || c->head_stride % unit ||
+        c->token_stride % unit)
         return Q4_ERR_MISALIGNED;
     return Q4_OK;
 }
+
+static q4_status cache_ok(const q4_kv_cache *c) { return cache_fields_ok(c, 8); }
+
+static q4_status cache_ok(const q4_kv_cache8 *c)
+{
+    if (!c || !c->k_exp || !c->v_exp) return Q4_ERR_INVALID_ARG;
+    const q4_status st = cache_fields_ok(c, 16);
+    if (st != Q4_OK) return st;
+    if (c->code != Q4_I8 && c->code != Q4_E4M3) return Q4_ERR_UNSUPPORTED;
+    const uintptr_t k = reinterpret_cast<uintptr_t>(c->k_exp), v = reinterpret_cast<uintptr_t>(c->v_exp);
+    const uintptr_t n = static_cast<uintptr_t>(c->blocks * c->heads);
+    return c->k == c->v || (k < v + n && v < k + n) ? Q4_ERR_INVALID_ARG : Q4_OK;
+}
+
+// The cache as the kernels see it.
+static Codes codes_of(const q4_kv_cache8 *c)
+{
+    Codes x{};
+    x.k = static_cast<uint8_t *>(c->k);
+    x.v = static_cast<uint8_t *>(c->v);
+    x.k_exp = c->k_exp;
+    x.v_exp = c->v_exp;
+    x.block_stride = c->block_stride;
+    x.head_stride = c->head_stride;
+    x.token_stride = c->token_stride;
+    x.blocks = static_cast<int>(c->blocks);
+    x.heads = static_cast<int>(c->heads);
+    x.S = static_cast<int>(c->block_size);
+    x.D = static_cast<int>(c->head_dim);
+    x.by_S.set(x.S);
+    return x;
+}
+
+// Token rows of a call on an 8-bit cache: chunks of rows and a block behind
+// them are counted in 32 bits.
+constexpr int64_t MOST_ROWS8 = INT_MOST - (1 << 18);
 
 }  // namespace q4
 
@@ -423,10 +462,12 @@ q4_status q4_cache_plan(const int32_t *cached, const int32_t *fresh, int64_t B, 
     return e == cudaSuccess ? Q4_OK : cuda_fail(e);
 }
 
-q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t Hq, int64_t rot,
-                         q4_rope_style style, const double *freq, float factor,
-                         const int32_t *position, const int64_t *slot, void *q_out,
-                         int64_t q_stride, const q4_kv_cache *cache, q4_stream_t stream)
+}  // extern "C"
+
+template <typename Cache>
+static q4_status append_ok(const void *qkv, int64_t qkv_stride, int64_t T, int64_t Hq, int64_t rot, q4_rope_style style,
+                           const double *freq, const int32_t *position, const int64_t *slot, const void *q_out,
+                           int64_t q_stride, const Cache *cache, int64_t most_rows)
 {
     if (!qkv || !position || !slot || !q_out) return Q4_ERR_INVALID_ARG;
     const q4_status st = cache_ok(cache);
@@ -434,12 +475,25 @@ q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t
     if (T < 1 || Hq < 1 || rot < 0 || rot > cache->head_dim || rot % 2 || (rot > 0 && !freq))
         return Q4_ERR_INVALID_ARG;
     if (style != Q4_ROPE_HALF && style != Q4_ROPE_INTERLEAVED) return Q4_ERR_INVALID_ARG;
-    if (T > INT_MOST || Hq > 65536) return Q4_ERR_UNSUPPORTED;
+    if (T > most_rows || Hq > 65536) return Q4_ERR_UNSUPPORTED;
     if (qkv_stride < (Hq + 2 * cache->heads) * cache->head_dim || q_stride < Hq * cache->head_dim)
         return Q4_ERR_INVALID_ARG;
     if (qkv_stride > (1LL << 30) || q_stride > (1LL << 30)) return Q4_ERR_UNSUPPORTED;
     if (!aligned16(qkv) || !aligned16(q_out) || qkv_stride % 8 || q_stride % 8)
         return Q4_ERR_MISALIGNED;
+    return Q4_OK;
+}
+
+extern "C" {
+
+q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t Hq, int64_t rot,
+                         q4_rope_style style, const double *freq, float factor,
+                         const int32_t *position, const int64_t *slot, void *q_out,
+                         int64_t q_stride, const q4_kv_cache *cache, q4_stream_t stream)
+{
+    const q4_status st =
+        append_ok(qkv, qkv_stride, T, Hq, rot, style, freq, position, slot, q_out, q_stride, cache, INT_MOST);
+    if (st != Q4_OK) return st;
     RopeArgs a{};
     a.qkv = static_cast<const uint16_t *>(qkv);
     a.qkv_stride = qkv_stride;
@@ -467,6 +521,69 @@ q4_status q4_rope_append(const void *qkv, int64_t qkv_stride, int64_t T, int64_t
     return e == cudaSuccess ? Q4_OK : cuda_fail(e);
 }
 
+q4_status q4_rope_append8(const void *qkv, int64_t qkv_stride, int64_t T, int64_t Hq, int64_t rot,
+                          q4_rope_style style, const double *freq, float factor,
+                          const int32_t *position, const int64_t *slot, void *q_out,
+                          int64_t q_stride, const q4_kv_cache8 *cache, q4_stream_t stream)
+{
+    const q4_status st =
+        append_ok(qkv, qkv_stride, T, Hq, rot, style, freq, position, slot, q_out, q_stride, cache, MOST_ROWS8);
+    if (st != Q4_OK) return st;
+    const DevInfo *d = dev_info();
+    if (!d) return cuda_fail(cudaGetLastError());
+    Append8Args a{};
+    a.qkv = static_cast<const uint16_t *>(qkv);
+    a.qkv_stride = qkv_stride;
+    a.T = static_cast<int>(T);
+    a.Hq = static_cast<int>(Hq);
+    a.rot = static_cast<int>(rot);
+    a.freq = freq;
+    a.factor = factor;
+    a.position = position;
+    a.slot = slot;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.q_stride = q_stride;
+    a.c = codes_of(cache);
+    a.err = debug_err();
+    const cudaError_t e = append8_launch(a, cache->code, cache->type == Q4_F16, style == Q4_ROPE_INTERLEAVED, d->sm_count,
+                                         reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q4_OK : cuda_fail(e);
+}
+
+q4_status q4_cache_read8(const q4_kv_cache8 *cache, const int32_t *table, int64_t table_stride,
+                         int64_t width, const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                         int64_t T, void *k_out, int64_t k_stride, void *v_out, int64_t v_stride,
+                         q4_dtype ot, q4_stream_t stream)
+{
+    if (!table || !q_start || !kv_len || !k_out || !v_out) return Q4_ERR_INVALID_ARG;
+    const q4_status st = cache_ok(cache);
+    if (st != Q4_OK) return st;
+    if (T < 1 || B < 1 || width < 1 || table_stride < width) return Q4_ERR_INVALID_ARG;
+    if (ot != Q4_F32 && ot != cache->type) return Q4_ERR_UNSUPPORTED;
+    if (T > MOST_ROWS8 || B > MOST_ROWS8 || table_stride > (1LL << 40) || width > (INT_MOST >> 1) / cache->block_size)
+        return Q4_ERR_UNSUPPORTED;
+    const int64_t row = cache->heads * cache->head_dim;
+    if (k_stride < row || v_stride < row) return Q4_ERR_INVALID_ARG;
+    if (k_stride > (1LL << 30) || v_stride > (1LL << 30)) return Q4_ERR_UNSUPPORTED;
+    if (!aligned16(k_out) || !aligned16(v_out) || k_stride % 8 || v_stride % 8) return Q4_ERR_MISALIGNED;
+    Read8Args a{};
+    a.c = codes_of(cache);
+    a.table = table;
+    a.table_stride = table_stride;
+    a.width = static_cast<int>(width);
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.B = static_cast<int>(B);
+    a.T = static_cast<int>(T);
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.err = debug_err();
+    const cudaError_t e = read8_launch(a, cache->code, cache->type == Q4_F16, ot == Q4_F32, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q4_OK : cuda_fail(e);
+}
+
 // Rows (tokens times heads) of a call: their indices run on to the end of a
 // tile of 256 rows, in 32 bits.
 constexpr int64_t ATTN_MOST_ROWS = INT_MOST - 1023;
@@ -485,8 +602,29 @@ size_t q4_attention_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads
     return attention_plan(max_fresh, Hq / heads, head_dim, d->sm_count).workspace;
 }
 
+}  // extern "C"
+
+// What differs between the caches.
+static AttnPlan plan_for(const q4_kv_cache *c, int64_t max_fresh, int64_t Hq, int sm_count)
+{
+    return attention_plan(max_fresh, Hq / c->heads, c->head_dim, sm_count);
+}
+static AttnPlan plan_for(const q4_kv_cache8 *c, int64_t max_fresh, int64_t Hq, int sm_count)
+{
+    return attention8_plan(max_fresh, Hq / c->heads, c->head_dim, sm_count);
+}
+static cudaError_t launch_for(const q4_kv_cache *c, const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
+{
+    return attention_launch(p, a, c->type == Q4_F16, s);
+}
+static cudaError_t launch_for(const q4_kv_cache8 *c, const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
+{
+    return attention8_launch(p, a, codes_of(c), c->code, c->type == Q4_F16, s);
+}
+
+template <typename Cache>
 static q4_status attention_common(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
-                                  const q4_kv_cache *cache, const int32_t *table,
+                                  const Cache *cache, const int32_t *table,
                                   int64_t table_stride, int64_t width, const int32_t *q_start,
                                   const int32_t *kv_len, int64_t B, int64_t max_fresh, float scale,
                                   int64_t window, void *o, q4_dtype ot, int64_t o_stride, float *lse,
@@ -511,12 +649,12 @@ static q4_status attention_common(const void *q, int64_t q_stride, int64_t T, in
         return Q4_ERR_MISALIGNED;
     const DevInfo *d = dev_info();
     if (!d) return cuda_fail(cudaGetLastError());
-    const AttnPlan plan = attention_plan(max_fresh, Hq / cache->heads, cache->head_dim, d->sm_count);
+    const AttnPlan plan = plan_for(cache, max_fresh, Hq, d->sm_count);
     if (debug_no_copy && !plan.tc) return Q4_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < plan.workspace) return Q4_ERR_INVALID_ARG;
     AttnArgs a{};
     a.q = static_cast<const uint16_t *>(q);
-    a.k = static_cast<const uint16_t *>(cache->k);
+    a.k = static_cast<const uint16_t *>(cache->k);  // (bytes, of an 8-bit cache)
     a.v = static_cast<const uint16_t *>(cache->v);
     a.o = o;
     a.ot = ot;
@@ -551,10 +689,11 @@ static q4_status attention_common(const void *q, int64_t q_stride, int64_t T, in
     a.debug_no_copy = debug_no_copy;
     a.part_len = static_cast<int64_t>((plan.workspace - ATTN_COUNTER_BYTES) / sizeof(float));
     a.err = d->err;
-    const cudaError_t e = attention_launch(plan, a, cache->type == Q4_F16,
-                                           reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_for(cache, plan, a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? Q4_OK : cuda_fail(e);
 }
+
+extern "C" {
 
 q4_status q4_attention(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
                        const q4_kv_cache *cache, const int32_t *table, int64_t table_stride,
@@ -579,6 +718,26 @@ q4_status q4_attention_timeout_selftest(const void *q, int64_t q_stride, int64_t
     return attention_common(q, q_stride, T, Hq, cache, table, table_stride, width, q_start, kv_len, B,
                             max_fresh, scale, window, o, ot, o_stride, lse, workspace, workspace_bytes,
                             stream, 1, 20000000ull);
+}
+
+q4_status q4_attention8(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                        const q4_kv_cache8 *cache, const int32_t *table, int64_t table_stride,
+                        int64_t width, const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                        int64_t max_fresh, float scale, int64_t window, void *o, q4_dtype ot,
+                        int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes,
+                        q4_stream_t stream)
+{
+    return attention_common(q, q_stride, T, Hq, cache, table, table_stride, width, q_start, kv_len, B,
+                            max_fresh, scale, window, o, ot, o_stride, lse, workspace, workspace_bytes,
+                            stream, 0, 2000000000ull);
+}
+
+size_t q4_attention8_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads, int64_t head_dim)
+{
+    if (!attention_sizes_ok(max_fresh, Hq, heads, head_dim) || head_dim % 16) return 0;
+    const DevInfo *d = dev_info();
+    if (!d) return 0;
+    return attention8_plan(max_fresh, Hq / heads, head_dim, d->sm_count).workspace;
 }
 
 q4_status q4_check(q4_stream_t stream)

@@ -97,6 +97,47 @@ struct RopeArgs {
 };
 cudaError_t rope_append_launch(const RopeArgs &a, bool f16, bool interleaved, cudaStream_t s);
 
+// ------------------------------------------------------ the cache in 8 bits
+// Codes and exponents of an 8-bit cache as its kernels see them.
+struct Codes {
+    uint8_t *k, *v, *k_exp, *v_exp;
+    int64_t block_stride, head_stride, token_stride;  // bytes
+    int blocks, heads, S, D;
+    FastDiv by_S;
+};
+
+struct Append8Args {
+    const uint16_t *qkv;
+    int64_t qkv_stride;
+    int T, Hq, rot;
+    const double *freq;
+    float factor;
+    const int *position;
+    const int64_t *slot;
+    uint16_t *q_out;
+    int64_t q_stride;
+    Codes c;
+    unsigned int *err;
+};
+cudaError_t append8_launch(const Append8Args &a, q4_code code, bool f16, bool interleaved, int sm_count, cudaStream_t s);
+
+struct Read8Args {
+    Codes c;
+    const int *table;
+    int64_t table_stride;
+    int width;
+    const int *q_start, *kv_len;
+    int B, T;
+    void *k_out, *v_out;
+    int64_t k_stride, v_stride;
+    unsigned int *err;
+};
+cudaError_t read8_launch(const Read8Args &a, q4_code code, bool f16, bool f32_out, cudaStream_t s);
+
+// One q4_attention8 call: of a, the cache's fields are those in c.
+AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count);
+cudaError_t attention8_launch(const AttnPlan &p, const AttnArgs &a, const Codes &c, q4_code code, bool f16, cudaStream_t s);
+
 // Launch with programmatic stream serialization: the kernel may become
 // resident while the previous one drains, and waits (grid_dep_wait) before it
 // touches memory.  It lets its own dependents go only behind that wait, so
