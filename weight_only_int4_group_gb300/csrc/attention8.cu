@@ -1,102 +1,523 @@
-// attention8.cu -- attention over the 8-bit blocked cache.
+// attention8.cu -- attention over the 8-bit blocked cache, few rows per KV
+// head: the decode kernel.
+//
+// Rows.  The n new tokens of a request and the GQ query heads that share a KV
+// head form n * GQ rows that read the same keys, in row tiles of 8 or 16.  Bound:
+// with one tile the codes are read once; HBM bounds the call as long as a
+// byte's work, twice what a byte of a 16-bit cache brings, fits beside its load.
+//
+// Keys are the m of mma.sync m16n8k16 and rows its n: with 8 rows no part of
+// the tile is empty, and codes are A fragments, widened to binary16 in registers
+// on the way from shared memory (exactly: int8 by the bytes of 1024 + 128 + c,
+// e4m3 by its conversion instruction).
+//   scores   S^T[key][row] = K Q^T: the order of the dims in the sum is free, so a
+//            lane takes 16 consecutive bytes of its two keys and the queries are
+//            permuted alike;
+//   outputs  O^T[dim][row] = V^T P^T: a lane takes 16 consecutive dims of four
+//            keys and pairs the keys' bytes; it ends with 16 consecutive dims of
+//            its two rows.  The weights turn by movmatrix in between.
+// Queries in bf16 are scaled by a power of two per row, so that their largest
+// lies in [2^14, 2^15), and go to binary16 without rounding (below 2^-39 of the
+// largest they lose bits; a sum in f32 holds no more).
+//
+// Scales.  A unit is 16 keys, all of one block, so its two scales are uniform:
+// 2^ek goes into the factor of the scores, 2^ev into the weights' exponent: with
+// x_j = s_j + ev the second product sums 2^(x_j - ref) c_j and the row sum
+// 2^(x_j - ref) 2^-ev, both under one running reference that follows x.  So
+// weights in binary16 (which end at 2^16 and 2^-25) are large where their
+// contribution is, whatever the scales of other blocks.  The reference lies 2^7
+// below the x that it was taken from and moves when that is passed by 2^8.
+//
+// Work.  As in the 16-bit kernel (attention.cu): all units of the call form one
+// sequence cut into an equal range per warp; a ring of units per warp filled by
+// cp.async; split items meet in a tree, in sequence order.
 #include "attention.cuh"
 #include "cache8.cuh"
 
 namespace q4 {
 namespace {
 
-// A warp per (token row, query head): 32 keys at a time, a key per lane for the
-// scores, 4 dims per lane for the weighted values; one pass with the running
-// maximum and sum.
-template <int CODE, bool F16>
-__global__ void __launch_bounds__(256) k_attn8(const AttnArgs a, const Codes c)
+constexpr int TK = 16;       // keys per unit
+constexpr int NW = 12;       // warps
+constexpr int THREADS = NW * 32;
+constexpr int PAD = 4, MIN_UNITS = 4;
+constexpr float LIFT = 7.0f, SLACK = 8.0f;
+constexpr int MERGE = 8, LEVELS = 4, MOST_CTAS = 256;
+static_assert(MERGE * MERGE * MERGE * MERGE >= NW * MOST_CTAS, "levels");
+static_assert(LEVELS * 2 * NW * MOST_CTAS * sizeof(unsigned int) <= ATTN_COUNTER_BYTES, "counters");
+
+template <int DP, int NT>
+struct Sizes {
+    static constexpr int STAGES = DP == 128 ? 4 : 6;   // units in flight per warp
+    static constexpr int TILE = TK * DP;               // bytes of a unit's keys
+    static constexpr int RING = STAGES * 2 * TILE;
+    static constexpr int SMEM = NW * RING + NW * STAGES * 2 * 4;
+    static constexpr int SLOT = 128 * NT * (DP / 16 + 1);  // floats of a partial result
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
 {
-    using X = Exponents<CODE, F16>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ float qs[8][128];
-    grid_dep_wait();
-    grid_dep_launch_dependents();
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp;
-    if (w >= static_cast<int64_t>(a.T) * a.Hq) return;
-    const int t = static_cast<int>(w / a.Hq), h = static_cast<int>(w - static_cast<int64_t>(t) * a.Hq), kvh = h / a.GQ;
-    const int b = request_of(a.q_start, a.B, t);
-    int t0, n, kv;
-    request(a, b, t0, n, kv);
-    if (t < t0 || t >= t0 + n) return;
-    const int place = kv - n + (t - t0);
-    for (int d = lane; d < 128; d += 32)
-        qs[warp][d] = d < a.D ? bits_to_f32<F16>(a.q[t * a.q_stride + static_cast<int64_t>(h) * a.D + d]) : 0.0f;
-    __syncwarp();
-    float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j0 = window_start(a, place) & ~15; j0 <= place; j0 += 32) {
-        const int j = j0 + lane;
-        const bool seen = j <= place && (a.window == 0 || j > place - a.window);
-        int64_t at = -1;
-        float fk = 0.0f, fv = 0.0f, s = -INFINITY;
-        if (seen) {
-            s = 0.0f;
-            const int col = a.by_S.div(j), blk = a.table[b * a.table_stride + col];
-            if (static_cast<unsigned>(blk) < static_cast<unsigned>(c.blocks)) {
-                at = blk * c.block_stride + (j - col * a.S) * c.token_stride + kvh * c.head_stride;
-                fk = pow2(X::of(c.k_exp[static_cast<int64_t>(blk) * c.heads + kvh]));
-                fv = pow2(X::of(c.v_exp[static_cast<int64_t>(blk) * c.heads + kvh]));
-                for (int d = 0; d < a.D; d += 4) {
-                    float x[4];
-                    codes_to_f32<CODE>(*reinterpret_cast<const uint32_t *>(c.k + at + d), x);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transposed(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Bytes 0, 1 (lo) and 2, 3 (hi) of a word of codes as pairs of binary16.
+template <int CODE>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    if (CODE == I8) {
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half(0xE480));  // -(1024 + 128)
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 x = __hadd2(*reinterpret_cast<const __half2 *>(&a), off), y = __hadd2(*reinterpret_cast<const __half2 *>(&b), off);
+        lo = *reinterpret_cast<const uint32_t *>(&x);
+        hi = *reinterpret_cast<const uint32_t *>(&y);
+    } else {
+        lo = e4m3_to_f16x2(w);
+        hi = e4m3_to_f16x2(w >> 16);
+    }
+}
+
+template <int NT, int NO>
+__device__ __forceinline__ void add_parts(const float4 *x, int stride, int n, bool odd, int slot, float (&o)[NT][NO][4],
+                                          float (&m)[NT][2], float (&l)[NT][2])
+{
+    constexpr int AHEAD = NT == 1 ? 2 : 1;
+    const float4 *even = x - (odd ? slot / 4 : 0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+        float4 y[AHEAD][NT][NO], ml[AHEAD][NT];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s = fmaf(x[e], qs[warp][d + e], s);
+        for (int i = 0; i < AHEAD; ++i) {
+            const bool in = i0 + i < n;
+            const float4 *p = i0 + i == 0 ? x : even + static_cast<int64_t>(i0 + i) * stride * (slot / 2);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                ml[i][t] = in ? __ldcg(p + (NT * NO + t) * 32) : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+#pragma unroll
+                for (int k = 0; k < NO; ++k) y[i][t][k] = in ? __ldcg(p + (t * NO + k) * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float g0[2], g1[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float mi = j ? ml[i][t].z : ml[i][t].x, li = j ? ml[i][t].w : ml[i][t].y;
+                    const float mn = fmaxf(m[t][j], mi), ref = mn == -INFINITY ? 0.0f : mn;
+                    g0[j] = ex2(m[t][j] - ref);
+                    g1[j] = ex2(mi - ref);
+                    m[t][j] = mn;
+                    l[t][j] = l[t][j] * g0[j] + li * g1[j];
+                }
+#pragma unroll
+                for (int k = 0; k < NO; ++k) {
+                    o[t][k][0] = o[t][k][0] * g0[0] + y[i][t][k].x * g1[0];
+                    o[t][k][1] = o[t][k][1] * g0[1] + y[i][t][k].y * g1[1];
+                    o[t][k][2] = o[t][k][2] * g0[0] + y[i][t][k].z * g1[0];
+                    o[t][k][3] = o[t][k][3] * g0[1] + y[i][t][k].w * g1[1];
                 }
             }
-            s *= fk * a.scale_log2;
+    }
+}
+
+template <int CODE, bool F16, int DP, int NT>
+__global__ void __launch_bounds__(THREADS, 1) k_attn8_stream(const AttnArgs a, const Codes c)
+{
+    using X = Exponents<CODE, F16>;
+    using Z = Sizes<DP, NT>;
+    constexpr int R = 8 * NT, STAGES = Z::STAGES;
+    constexpr int CH = DP / 16, RPI = 32 / CH, LPT = TK / RPI;  // 16-byte pieces of a key; keys per load; loads
+    constexpr int KH = DP / 64;                                 // pieces of a key that a lane takes
+    constexpr int NO = DP / 16;                                 // output m tiles
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ LocateScratch ls;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
+
+    grid_dep_wait();
+    grid_dep_launch_dependents();
+    sum_slabs<R, TK, NW, PAD>(a, ls);
+    // neighbours in the sequence on different SMs: few units use many SMs
+    const int me = warp * gridDim.x + blockIdx.x;
+    const Range rng = find_share<R, TK, NW, MIN_UNITS, PAD>(a, ls, me, NW * gridDim.x);
+    if (rng.u0 >= rng.u1) return;
+
+    using Pieces = Walk<R, TK, PAD>;
+    Pieces k(a, rng), ld = k;  // being summed; being loaded
+    const uint32_t ring = smem_u32(smem) + warp * Z::RING;
+    int *const scales = reinterpret_cast<int *>(smem + NW * Z::RING) + warp * STAGES * 2;  // (ek, ev) per slot
+    int ld_i = 0, ld_slot = 0;  // unit of ld, ring slot
+    int exp_slot = -1;  // exponents on their way (lanes 0-15 keys', 16-31 values'):
+    int exp = 0;        // kept a unit later, so that nothing waits for their loads
+    auto block_of = [&]() {  // table entry of the unit to load
+        const int key = (ld.kt0 + ld.kt + ld_i) * TK;
+        return ld.more(rng) && key < ld.kv ? a.table[ld.it.b * a.table_stride + a.by_S.div(key)] : -1;
+    };
+    int blk = block_of();
+    auto issue = [&]() {
+        if (exp_slot >= 0 && (lane & 15) == 0) scales[exp_slot * 2 + (lane >> 4)] = X::of(exp);
+        exp_slot = -1;
+        if (ld.more(rng)) {
+            const int key = (ld.kt0 + ld.kt + ld_i) * TK;
+            const bool in = static_cast<unsigned>(blk) < static_cast<unsigned>(a.blocks);
+            const uint32_t dst = ring + ld_slot * 2 * Z::TILE;
+            // lane: 16-byte piece p of keys hi, hi + RPI, ..
+            const int p = lane % CH, hi = lane / CH;
+            int64_t at = in ? blk * a.block_stride + (key - a.by_S.div(key) * a.S + hi) * a.token_stride +
+                                  ld.it.head * a.head_stride + p * 16
+                            : 0;
+            exp = in ? (lane < 16 ? c.k_exp : c.v_exp)[static_cast<int64_t>(blk) * a.Hkv + ld.it.head] : 127;
+            exp_slot = ld_slot;
+            const int rows = in && p * 16 < a.D ? ld.kv - key : 0;  // keys that exist
+            // and those that the window leaves to some row
+            const int row0 = a.window > 0 && ld.kt + ld_i == 0 ? ld.first_key(a) - key : 0;
+#pragma unroll
+            for (int l = 0; l < LPT; ++l) {
+                const int row = l * RPI + hi;
+                const bool ok = row >= row0 && row < rows;
+                // no two of the lanes that read together meet in a bank
+                const int pk = DP == 128 ? p ^ ((row & 1) << 2) : p;
+                const int pv = DP == 128 ? p ^ ((row >> 1 & 3) << 1) : p ^ (row >> 1 & 3);
+                cp_async16(dst + row * DP + (pk << 4), c.k + (ok ? at : 0), ok);
+                cp_async16(dst + Z::TILE + row * DP + (pv << 4), c.v + (ok ? at : 0), ok);
+                at += RPI * a.token_stride;
+            }
+            ld_slot = ld_slot + 1 == STAGES ? 0 : ld_slot + 1;
+            if (++ld_i == ld.nu) {
+                ld.next(a, rng);
+                ld_i = 0;
+            }
+            blk = block_of();
         }
-        float mx = s;
-        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float mn = fmaxf(m, mx);
-        const float ref = mn == -INFINITY ? 0.0f : mn, f = ex2(m - ref), p = ex2(s - ref);
-        m = mn;
-        l = l * f + p;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] *= f;
-        for (int i = 0; i < 32; ++i) {
-            const int64_t from = __shfl_sync(0xffffffffu, at, i);
-            const float pv = __shfl_sync(0xffffffffu, p * fv, i);
-            if (from >= 0 && lane * 4 < a.D) {
-                float x[4];
-                codes_to_f32<CODE>(*reinterpret_cast<const uint32_t *>(c.v + from + lane * 4), x);
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+
+    int slot = 0;
+    for (; k.more(rng); k.next(a, rng)) {
+        // ---- queries as B fragments: row lg of a tile, the lane's pieces of it
+        uint32_t qf[NT][KH * 4][2];
+        float cr[NT][2];  // scores' factor of rows 2 lt and 2 lt + 1
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = fmaf(pv, x[e], o[e]);
+        for (int t = 0; t < NT; ++t) {
+            const int r = k.row0 + 8 * t + lg;
+            const bool in = r < k.row1;
+            const int tok = in ? a.by_GQ.div(r) : 0;
+            const uint16_t *q = a.q + (k.t0 + tok) * a.q_stride + static_cast<int64_t>(k.it.head * a.GQ + r - tok * a.GQ) * a.D;
+            uint32_t peak = 0;
+#pragma unroll
+            for (int h = 0; h < KH; ++h) {
+                const int d = (lt + 4 * h) * 16;
+                uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                if (in && d < a.D) {
+                    x = *reinterpret_cast<const uint4 *>(q + d);
+                    y = *reinterpret_cast<const uint4 *>(q + d + 8);
+                }
+                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    qf[t][h * 4 + i / 2][i & 1] = w[i];
+                    if (!F16) peak = max(peak, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
+                }
+            }
+            int ex = 0;
+            if (!F16) {
+                peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+                peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
+                ex = peak ? min(max(static_cast<int>(peak >> 7) - 127 - 14, -126), 126) : 0;
+                const float f = pow2(-ex);
+#pragma unroll
+                for (int i = 0; i < KH * 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t w = qf[t][i][j];
+                        qf[t][i][j] = pack2<true>(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) cr[t][j] = a.scale_log2 * pow2(__shfl_sync(0xffffffffu, ex, 4 * (2 * lt + j)));
+        }
+        int place[NT][2];  // the rows' places in the request (their last visible keys)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = k.row0 + 8 * t + 2 * lt + j;
+                place[t][j] = r < k.row1 ? k.base + a.by_GQ.div(r) : -1;
+            }
+        const int lo_place = k.base + a.by_GQ.div(k.row0), hi_place = k.base + a.by_GQ.div(k.row1 - 1);
+
+        float o[NT][NO][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NO; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
+        }
+
+        for (int i = 0; i < k.nu; ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+            __syncwarp();  // the other lanes' copies too; and all lanes are done with the slot below
+            issue();
+            const uint32_t ks = ring + slot * 2 * Z::TILE, vs = ks + Z::TILE;
+            const int ek = scales[slot * 2], ev = scales[slot * 2 + 1];
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            float sc[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < KH; ++h) {
+                const int p = DP == 128 ? (lt + 4 * h) ^ ((lg & 1) << 2) : lt;
+                const uint4 x = lds16(ks + lg * DP + (p << 4)), y = lds16(ks + (lg + 8) * DP + (p << 4));
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t f[4];
+                    widen<CODE>(xw[w], f[0], f[2]);
+                    widen<CODE>(yw[w], f[1], f[3]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma16816(sc[t], f, qf[t][h * 4 + w][0], qf[t][h * 4 + w][1]);
+                }
+            }
+            // ---- mask and weights in units of log 2
+            const int key0 = (k.kt0 + k.kt + i) * TK;
+            const bool part = key0 + TK - 1 > lo_place || (a.window > 0 && key0 <= hi_place - a.window);
+            const float fk = pow2(ek), fv = static_cast<float>(ev), undo = pow2(-ev);
+            bool past = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = e & 1, key = key0 + lg + (e >> 1) * 8;
+                    float x = fmaf(sc[t][e], cr[t][j] * fk, fv);
+                    if (part && !(key <= place[t][j] && (a.window == 0 || key > place[t][j] - a.window))) x = -INFINITY;
+                    past |= x > m[t][j] + SLACK;
+                    sc[t][e] = x;
+                }
+            if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float f[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float mx = fmaxf(sc[t][j], sc[t][2 + j]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float mn = fmaxf(m[t][j], mx), ref = mn == -INFINITY ? 0.0f : mn;
+                        f[j] = ex2(m[t][j] - ref);
+                        m[t][j] = mn;
+                        l[t][j] *= f[j];
+                    }
+#pragma unroll
+                    for (int n = 0; n < NO; ++n) {
+                        o[t][n][0] *= f[0];
+                        o[t][n][1] *= f[1];
+                        o[t][n][2] *= f[0];
+                        o[t][n][3] *= f[1];
+                    }
+                }
+            }
+            uint32_t p[NT][2];  // B fragments: keys are k, rows n
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float ref = m[t][j] == -INFINITY ? 0.0f : m[t][j];
+                    sc[t][j] = ex2((sc[t][j] - ref) + LIFT);  // no rounding of a large ref
+                    sc[t][2 + j] = ex2((sc[t][2 + j] - ref) + LIFT);
+                    l[t][j] = fmaf(sc[t][j] + sc[t][2 + j], undo, l[t][j]);
+                }
+                p[t][0] = transposed(pack2<true>(sc[t][0], sc[t][1]));
+                p[t][1] = transposed(pack2<true>(sc[t][2], sc[t][3]));
+            }
+            // ---- values: the lane's dims of keys 2 lt, 2 lt + 1, and those + 8
+            uint32_t v[4][NO / 2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = 2 * lt + (e & 1) + (e >> 1) * 8;
+                if (DP == 128) {
+                    const uint4 x = lds16(vs + key * DP + ((lg ^ ((key >> 1 & 3) << 1)) << 4));
+                    v[e][0] = x.x;
+                    v[e][1] = x.y;
+                    v[e][NO / 2 - 2] = x.z;
+                    v[e][NO / 2 - 1] = x.w;
+                } else {
+                    const uint2 x = lds8(vs + key * DP + (((lg >> 1) ^ (key >> 1 & 3)) << 4) + (lg & 1) * 8);
+                    v[e][0] = x.x;
+                    v[e][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < NO / 2; ++w) {
+                uint32_t f[2][4];  // two m tiles: dims 4w, 4w + 1 and 4w + 2, 4w + 3
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    widen<CODE>(__byte_perm(v[2 * b][w], v[2 * b + 1][w], 0x5140), f[0][2 * b], f[0][2 * b + 1]);
+                    widen<CODE>(__byte_perm(v[2 * b][w], v[2 * b + 1][w], 0x7362), f[1][2 * b], f[1][2 * b + 1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma16816(o[t][2 * w + e], f[e], p[t][0], p[t][1]);
             }
         }
-    }
-    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    const float inv = inverse(l);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] *= inv;
-    if (lane * 4 < a.D) store_dims<F16, 4>(a, t, h, lane * 4, o);
-    if (lane == 0) store_lse(a, t, h, m, l);
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], 4);
+                l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], 8);
+                l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], 16);
+            }
+
+        bool store = k.whole();
+        if (!store) {
+            // as in the 16-bit kernel: the item's pieces are the leaves of a tree
+            // of MERGE-fold nodes over the workers that hold them; whoever
+            // completes a node adds its parts in order, leaves the sum in the
+            // first part's place and goes on to the next level.  A node's counter
+            // goes by its first worker, which may also hold the end of another item.
+            int w0, w1;
+            k.holders(rng, w0, w1);
+            // [tile][m tile][lane][4], then [tile][lane](reference, sum) of two rows
+            auto slot_of = [&](int w) {
+                return reinterpret_cast<float4 *>(a.part + (2 * static_cast<int64_t>(w) + (w == w0)) * Z::SLOT) + lane;
+            };
+            int at = me;            // where this warp's sum goes
+            int nodes = w1 - w0 + 1, idx = me - w0, stride = 1;  // of the level
+            unsigned int *count = a.count;
+            for (;;) {
+                float4 *ps = slot_of(at);
+                if (store_ok(reinterpret_cast<float *>(ps - lane) + Z::SLOT - 1 - a.part, a.part_len, a.err)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                        for (int n = 0; n < NO; ++n) ps[(t * NO + n) * 32] = make_float4(o[t][n][0], o[t][n][1], o[t][n][2], o[t][n][3]);
+                        ps[(NT * NO + t) * 32] = make_float4(m[t][0], l[t][0], m[t][1], l[t][1]);
+                    }
+                }
+                __threadfence();
+                __syncwarp();
+                const int first = idx / MERGE * MERGE, n_parts = min(MERGE, nodes - first);
+                at = w0 + first * stride;
+                int last = 0;
+                if (lane == 0) {
+                    unsigned int *cnt = count + 2 * at + (first == 0);
+                    last = store_ok(cnt - a.count, a.count_len, a.err) &&
+                           atomic_add_acq_rel_gpu(cnt, 1u) == static_cast<unsigned>(n_parts - 1);
+                    if (last) *cnt = 0u;
+                }
+                if (!__shfl_sync(0xffffffffu, last, 0)) break;
+                __syncwarp();  // lane 0's acquire holds for the other lanes' reads too: a shuffle orders no memory
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    m[t][0] = m[t][1] = -INFINITY;
+                    l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NO; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
+                }
+                add_parts<NT, NO>(slot_of(at), stride, n_parts, w0 == at, Z::SLOT, o, m, l);
+                idx = first / MERGE;
+                nodes = (nodes + MERGE - 1) / MERGE;
+                stride *= MERGE;
+                count += 2 * NW * gridDim.x;
+                if (nodes == 1) {
+                    store = true;
+                    break;
+                }
+            }
+        }
+        if (store) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = k.row0 + 8 * t + 2 * lt + j;
+                    if (r >= k.row1) continue;
+                    const int tok = a.by_GQ.div(r), h = k.it.head * a.GQ + r - tok * a.GQ;
+                    const float inv = inverse(l[t][j]);
+                    float y[2 * NO];
+#pragma unroll
+                    for (int n = 0; n < NO; ++n) {
+                        y[2 * n] = o[t][n][j] * inv;
+                        y[2 * n + 1] = o[t][n][2 + j] * inv;
+                    }
+                    store_dims<F16, 2 * NO>(a, k.t0 + tok, h, lg * 2 * NO, y);
+                    if (lg == 0) store_lse(a, k.t0 + tok, h, m[t][j] - LIFT, l[t][j]);
+                }
+        }
+        __syncwarp();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <int CODE, bool F16, int DP, int NT>
+cudaError_t launch(const AttnPlan &p, const AttnArgs &a, const Codes &c, cudaStream_t s)
+{
+    static std::atomic<bool> done[64];
+    auto kern = k_attn8_stream<CODE, F16, DP, NT>;
+    const cudaError_t e = allow_smem(kern, Sizes<DP, NT>::SMEM, done);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(p.grid), THREADS, Sizes<DP, NT>::SMEM, s, a, c);
 }
 
 template <int CODE, bool F16>
-cudaError_t launch(const AttnArgs &a, const Codes &c, cudaStream_t s)
+cudaError_t launch_rows(const AttnPlan &p, const AttnArgs &a, const Codes &c, cudaStream_t s)
 {
-    const dim3 grid(ctas_for(static_cast<int64_t>(a.T) * a.Hq, 8));
-    return launch_dependent(k_attn8<CODE, F16>, grid, 256, 0, s, a, c);
+    if (a.D > 64) return p.tiles == 1 ? launch<CODE, F16, 128, 1>(p, a, c, s) : launch<CODE, F16, 128, 2>(p, a, c, s);
+    return p.tiles == 1 ? launch<CODE, F16, 64, 1>(p, a, c, s) : launch<CODE, F16, 64, 2>(p, a, c, s);
 }
 
 }  // namespace
 
-AttnPlan attention8_plan(int64_t, int64_t, int64_t, int sm_count)
+AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count)
 {
     AttnPlan p{};
-    p.grid = sm_count;
-    p.workspace = ATTN_COUNTER_BYTES;
+    p.grid = std::min<int>(sm_count, MOST_CTAS);
+    p.tiles = max_fresh > 8 / GQ ? 2 : 1;
+    const size_t slot = (D > 64 ? Sizes<128, 2>::SLOT : Sizes<64, 2>::SLOT) * sizeof(float) / 2 * p.tiles;
+    p.workspace = ATTN_COUNTER_BYTES + 2 * static_cast<size_t>(p.grid) * NW * slot;
     return p;
 }
 
-cudaError_t attention8_launch(const AttnPlan &, const AttnArgs &a, const Codes &c, q4_code code, bool f16, cudaStream_t s)
+cudaError_t attention8_launch(const AttnPlan &p, const AttnArgs &a, const Codes &c, q4_code code, bool f16, cudaStream_t s)
 {
-    if (code == Q4_I8) return f16 ? launch<I8, true>(a, c, s) : launch<I8, false>(a, c, s);
-    return f16 ? launch<E4M3, true>(a, c, s) : launch<E4M3, false>(a, c, s);
+    if (code == Q4_I8) return f16 ? launch_rows<I8, true>(p, a, c, s) : launch_rows<I8, false>(p, a, c, s);
+    return f16 ? launch_rows<E4M3, true>(p, a, c, s) : launch_rows<E4M3, false>(p, a, c, s);
 }
 
 }  // namespace q4

@@ -16,7 +16,7 @@ template <int CODE, bool F16>
 struct Exponents {
     static constexpr int LO = F16 ? (CODE == I8 ? -24 : -15) : -48;
     static constexpr int HI = F16 ? (CODE == I8 ? 9 : 7) : 48;
-    static __device__ __forceinline__ int of(uint8_t byte) { return min(max(static_cast<int>(byte) - 127, LO), HI); }
+    static __device__ __forceinline__ int of(int byte) { return min(max(byte - 127, LO), HI); }
 };
 
 // 2^e, -126 <= e <= 127

@@ -58,6 +58,7 @@ constexpr size_t ATTN_COUNTER_BYTES = 131072;
 struct AttnPlan {
     bool tc;         // tensor-core kernel (many rows per KV head)
     int grid;
+    int tiles;       // of 8 rows in a row tile (streaming, 8-bit cache)
     size_t workspace;
 };
 AttnPlan attention_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count);
