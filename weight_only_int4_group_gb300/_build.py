@@ -41,6 +41,7 @@ SOURCES = {
     "attention_tc.cu": [],
     "cache8.cu": [],
     "attention8.cu": [],
+    "attention8_tc.cu": [],
 }
 
 

@@ -619,7 +619,10 @@ static cudaError_t launch_for(const q4_kv_cache *c, const AttnPlan &p, const Att
 }
 static cudaError_t launch_for(const q4_kv_cache8 *c, const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 {
-    return attention8_launch(p, a, codes_of(c), c->code, c->type == Q4_F16, s);
+    AttnArgs a8 = a;
+    a8.k_exp = c->k_exp;
+    a8.v_exp = c->v_exp;
+    return attention8_launch(p, a8, c->code, c->type == Q4_F16, s);
 }
 
 template <typename Cache>

@@ -153,7 +153,7 @@ __device__ __forceinline__ void add_parts(const float4 *x, int stride, int n, bo
 }
 
 template <int CODE, bool F16, int DP, int NT>
-__global__ void __launch_bounds__(THREADS, 1) k_attn8_stream(const AttnArgs a, const Codes c)
+__global__ void __launch_bounds__(THREADS, 1) k_attn8_stream(const AttnArgs a)
 {
     using X = Exponents<CODE, F16>;
     using Z = Sizes<DP, NT>;
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn8_stream(const AttnArgs a, c
     Pieces k(a, rng), ld = k;  // being summed; being loaded
     const uint32_t ring = smem_u32(smem) + warp * Z::RING;
     int *const scales = reinterpret_cast<int *>(smem + NW * Z::RING) + warp * STAGES * 2;  // (ek, ev) per slot
+    const uint8_t *const kb = reinterpret_cast<const uint8_t *>(a.k), *const vb = reinterpret_cast<const uint8_t *>(a.v);
     int ld_i = 0, ld_slot = 0;  // unit of ld, ring slot
     int exp_slot = -1;  // exponents on their way (lanes 0-15 keys', 16-31 values'):
     int exp = 0;        // kept a unit later, so that nothing waits for their loads
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn8_stream(const AttnArgs a, c
             int64_t at = in ? blk * a.block_stride + (key - a.by_S.div(key) * a.S + hi) * a.token_stride +
                                   ld.it.head * a.head_stride + p * 16
                             : 0;
-            exp = in ? (lane < 16 ? c.k_exp : c.v_exp)[static_cast<int64_t>(blk) * a.Hkv + ld.it.head] : 127;
+            exp = in ? (lane < 16 ? a.k_exp : a.v_exp)[static_cast<int64_t>(blk) * a.Hkv + ld.it.head] : 127;
             exp_slot = ld_slot;
             const int rows = in && p * 16 < a.D ? ld.kv - key : 0;  // keys that exist
             // and those that the window leaves to some row
@@ -209,8 +210,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn8_stream(const AttnArgs a, c
                 // no two of the lanes that read together meet in a bank
                 const int pk = DP == 128 ? p ^ ((row & 1) << 2) : p;
                 const int pv = DP == 128 ? p ^ ((row >> 1 & 3) << 1) : p ^ (row >> 1 & 3);
-                cp_async16(dst + row * DP + (pk << 4), c.k + (ok ? at : 0), ok);
-                cp_async16(dst + Z::TILE + row * DP + (pv << 4), c.v + (ok ? at : 0), ok);
+                cp_async16(dst + row * DP + (pk << 4), kb + (ok ? at : 0), ok);
+                cp_async16(dst + Z::TILE + row * DP + (pv << 4), vb + (ok ? at : 0), ok);
                 at += RPI * a.token_stride;
             }
             ld_slot = ld_slot + 1 == STAGES ? 0 : ld_slot + 1;
@@ -486,20 +487,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_attn8_stream(const AttnArgs a, c
 }
 
 template <int CODE, bool F16, int DP, int NT>
-cudaError_t launch(const AttnPlan &p, const AttnArgs &a, const Codes &c, cudaStream_t s)
+cudaError_t launch(const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 {
     static std::atomic<bool> done[64];
     auto kern = k_attn8_stream<CODE, F16, DP, NT>;
     const cudaError_t e = allow_smem(kern, Sizes<DP, NT>::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(p.grid), THREADS, Sizes<DP, NT>::SMEM, s, a, c);
+    return launch_dependent(kern, dim3(p.grid), THREADS, Sizes<DP, NT>::SMEM, s, a);
 }
 
 template <int CODE, bool F16>
-cudaError_t launch_rows(const AttnPlan &p, const AttnArgs &a, const Codes &c, cudaStream_t s)
+cudaError_t launch_rows(const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 {
-    if (a.D > 64) return p.tiles == 1 ? launch<CODE, F16, 128, 1>(p, a, c, s) : launch<CODE, F16, 128, 2>(p, a, c, s);
-    return p.tiles == 1 ? launch<CODE, F16, 64, 1>(p, a, c, s) : launch<CODE, F16, 64, 2>(p, a, c, s);
+    if (a.D > 64) return p.tiles == 1 ? launch<CODE, F16, 128, 1>(p, a, s) : launch<CODE, F16, 128, 2>(p, a, s);
+    return p.tiles == 1 ? launch<CODE, F16, 64, 1>(p, a, s) : launch<CODE, F16, 64, 2>(p, a, s);
 }
 
 }  // namespace
@@ -508,16 +509,18 @@ AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count)
 {
     AttnPlan p{};
     p.grid = std::min<int>(sm_count, MOST_CTAS);
+    p.tc = max_fresh > 16 / GQ;
     p.tiles = max_fresh > 8 / GQ ? 2 : 1;
     const size_t slot = (D > 64 ? Sizes<128, 2>::SLOT : Sizes<64, 2>::SLOT) * sizeof(float) / 2 * p.tiles;
-    p.workspace = ATTN_COUNTER_BYTES + 2 * static_cast<size_t>(p.grid) * NW * slot;
+    p.workspace = ATTN_COUNTER_BYTES + (p.tc ? attention_tc_part_bytes(D, p.grid) : 2 * static_cast<size_t>(p.grid) * NW * slot);
     return p;
 }
 
-cudaError_t attention8_launch(const AttnPlan &p, const AttnArgs &a, const Codes &c, q4_code code, bool f16, cudaStream_t s)
+cudaError_t attention8_launch(const AttnPlan &p, const AttnArgs &a, q4_code code, bool f16, cudaStream_t s)
 {
-    if (code == Q4_I8) return f16 ? launch_rows<I8, true>(p, a, c, s) : launch_rows<I8, false>(p, a, c, s);
-    return f16 ? launch_rows<E4M3, true>(p, a, c, s) : launch_rows<E4M3, false>(p, a, c, s);
+    if (p.tc) return attention8_tc_launch(p.grid, a, code, f16, s);
+    if (code == Q4_I8) return f16 ? launch_rows<I8, true>(p, a, s) : launch_rows<I8, false>(p, a, s);
+    return f16 ? launch_rows<E4M3, true>(p, a, s) : launch_rows<E4M3, false>(p, a, s);
 }
 
 }  // namespace q4

@@ -31,7 +31,8 @@ inline int ctas_for(int64_t n, int per) { return static_cast<int>((n + per - 1) 
 
 // One q4_attention call as its kernels see it.
 struct AttnArgs {
-    const uint16_t *q, *k, *v;  // 16-bit elements, bf16 or f16
+    const uint16_t *q, *k, *v;  // 16-bit elements, bf16 or f16 (k, v of an 8-bit cache: bytes)
+    const uint8_t *k_exp, *v_exp;  // an 8-bit cache's exponents
     void *o;
     q4_dtype ot;
     float *lse;  // or null
@@ -135,9 +136,9 @@ struct Read8Args {
 };
 cudaError_t read8_launch(const Read8Args &a, q4_code code, bool f16, bool f32_out, cudaStream_t s);
 
-// One q4_attention8 call: of a, the cache's fields are those in c.
 AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count);
-cudaError_t attention8_launch(const AttnPlan &p, const AttnArgs &a, const Codes &c, q4_code code, bool f16, cudaStream_t s);
+cudaError_t attention8_tc_launch(int grid, const AttnArgs &a, q4_code code, bool f16, cudaStream_t s);
+cudaError_t attention8_launch(const AttnPlan &p, const AttnArgs &a, q4_code code, bool f16, cudaStream_t s);
 
 // Launch with programmatic stream serialization: the kernel may become
 // resident while the previous one drains, and waits (grid_dep_wait) before it
