@@ -262,6 +262,35 @@ __device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y)
     return r;
 }
 
+template <bool F16>
+__device__ __forceinline__ uint32_t fma2x16(uint32_t x, uint32_t y, uint32_t z)
+{
+    uint32_t r;
+    if (F16)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    else
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma2_relu(uint32_t x, uint32_t y, uint32_t z)
+{
+    uint32_t r;
+    asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub2(uint32_t x, uint32_t y)
+{
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+// The upper halves of two binary16 numbers' f32.
+__device__ __forceinline__ uint32_t f16x2_upper(uint32_t x)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+}
+
 __device__ __forceinline__ uint4 lds16(uint32_t at)
 {
     uint4 v;
@@ -273,48 +302,61 @@ __device__ __forceinline__ void sts16(uint32_t at, uint4 v)
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Four codes, times 2^e, as 16-bit numbers (exactly).  `by`, `more`: factors
-// made by widen_factors.
-template <int CODE, bool F16>
-__device__ __forceinline__ void widen_scaled(uint32_t w, uint32_t by, uint32_t more, uint32_t &lo, uint32_t &hi)
+// Factors by which codes become 16-bit numbers times 2^e, exactly: in two
+// steps where 1152 times one would leave binary16.
+struct Widen {
+    uint32_t by, off, more;
+    bool twice;
+};
+template <bool F16>
+__device__ __forceinline__ uint32_t pow2x2(int e)  // a pair of 2^e
 {
-    if (CODE == I8 && F16) {
-        // 1024 + 128 + c, less 1152
-        const uint32_t u = w ^ 0x80808080u;
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0xE480E480u));
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0xE480E480u));
-    } else if (CODE == I8) {
-        // the low 7 bits over 128, less 128 or (negative codes) 256
-        const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a & 0xFF7FFF7Fu), "r"(a & 0xFF80FF80u));
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(b & 0xFF7FFF7Fu), "r"(b & 0xFF80FF80u));
-    } else if (F16) {
-        lo = e4m3_to_f16x2(w);
-        hi = e4m3_to_f16x2(w >> 16);
-    } else {
-        // sign, exponent and mantissa in bf16's places are the number times 2^-120
-        const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
-        lo = (a >> 4 & 0x07F007F0u) | (a & 0x80008000u);
-        hi = (b >> 4 & 0x07F007F0u) | (b & 0x80008000u);
-    }
-    lo = mul2<F16>(lo, by);
-    hi = mul2<F16>(hi, by);
-    if (CODE == E4M3 && !F16 && more != 0x3F803F80u) {
-        lo = mul2<F16>(lo, more);
-        hi = mul2<F16>(hi, more);
-    }
+    const int b = F16 ? (e >= -14 ? e + 15 << 10 : 1 << (e + 24)) : e + 127 << 7;
+    return static_cast<uint32_t>(b) * 0x10001u;
 }
 template <int CODE, bool F16>
-__device__ __forceinline__ void widen_factors(int e, uint32_t &by, uint32_t &more)
+__device__ __forceinline__ Widen widen_factors(int e)
 {
-    more = 0x3F803F80u;
-    if (F16) {
-        by = (e >= -14 ? (e + 15) << 10 : 1 << (e + 24)) * 0x10001u;
-    } else if (CODE == I8) {
-        by = ((e + 127) << 7) * 0x10001u;
-    } else {  // 2^(120 + e), in two where that ends
-        by = ((min(e + 120, 127) + 127) << 7) * 0x10001u;
-        more = ((max(e - 7, 0) + 127) << 7) * 0x10001u;
+    constexpr int MOST = CODE == I8 && F16 ? 5 : 127;
+    Widen f;
+    f.by = pow2x2<F16>(min(e, MOST));
+    f.off = CODE == I8 ? mul2<F16>(f.by, F16 ? 0xE480E480u : 0xC380C380u) : 0u;  // -1152 or -256 times that
+    f.twice = e > MOST;
+    f.more = pow2x2<F16>(max(e - MOST, 0));
+    return f;
+}
+// Four codes.
+template <int CODE, bool F16>
+__device__ __forceinline__ void widen_scaled(uint32_t w, const Widen &f, uint32_t &lo, uint32_t &hi)
+{
+    if (CODE == I8) {
+        const uint32_t u = w ^ 0x80808080u;  // c + 128
+        constexpr uint32_t top = F16 ? 0x64646464u : 0x43434343u;
+        lo = __byte_perm(u, top, 0x4140);
+        hi = __byte_perm(u, top, 0x4342);
+        if (F16) {
+            // 1024 + 128 + c
+            lo = fma2x16<F16>(lo, f.by, f.off);
+            hi = fma2x16<F16>(hi, f.by, f.off);
+        } else {
+            // 256 + c below zero and 256 + 2 c above: what is above 0 halved is c too
+            const uint32_t half = mul2<false>(f.by, 0x3F003F00u), half_off = mul2<false>(f.off, 0x3F003F00u);
+            lo = sub2(fma2x16<F16>(lo, f.by, f.off), fma2_relu(lo, half, half_off));
+            hi = sub2(fma2x16<F16>(hi, f.by, f.off), fma2_relu(hi, half, half_off));
+        }
+    } else {
+        lo = e4m3_to_f16x2(w);
+        hi = e4m3_to_f16x2(w >> 16);
+        if (!F16) {  // their f32 ends in zeros
+            lo = f16x2_upper(lo);
+            hi = f16x2_upper(hi);
+        }
+        lo = mul2<F16>(lo, f.by);
+        hi = mul2<F16>(hi, f.by);
+    }
+    if (CODE == I8 && F16 && f.twice) {
+        lo = mul2<F16>(lo, f.more);
+        hi = mul2<F16>(hi, f.more);
     }
 }
 
@@ -415,8 +457,7 @@ __global__ void __launch_bounds__(Roles<CODE>::THREADS, 1) k_attn_tc(const __gri
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         const int row = first_row + i + row8;
-                        uint32_t by, more;
-                        widen_factors<CODE, F16>(scales[s * 8 + ((first_row + i) >> maps.kb_log)], by, more);
+                        const Widen f = widen_factors<CODE == WIDE ? I8 : CODE, F16>(scales[s * 8 + ((first_row + i) >> maps.kb_log)]);
                         uint4 x[Z::CH];
 #pragma unroll
                         for (int h = 0; h < Z::CH; ++h) x[h] = lds16(slot + Z::CODES + row * 128 + (((c + 4 * h) ^ row8) << 4));
@@ -428,10 +469,10 @@ __global__ void __launch_bounds__(Roles<CODE>::THREADS, 1) k_attn_tc(const __gri
 #pragma unroll
                         for (int h = 0; h < Z::CH; ++h) {
                             uint32_t y[8];
-                            widen_scaled<CODE, F16>(x[h].x, by, more, y[0], y[1]);
-                            widen_scaled<CODE, F16>(x[h].y, by, more, y[2], y[3]);
-                            widen_scaled<CODE, F16>(x[h].z, by, more, y[4], y[5]);
-                            widen_scaled<CODE, F16>(x[h].w, by, more, y[6], y[7]);
+                            widen_scaled<CODE, F16>(x[h].x, f, y[0], y[1]);
+                            widen_scaled<CODE, F16>(x[h].y, f, y[2], y[3]);
+                            widen_scaled<CODE, F16>(x[h].z, f, y[4], y[5]);
+                            widen_scaled<CODE, F16>(x[h].w, f, y[6], y[7]);
                             const uint32_t to = slot + h * Z::CHUNK + row * 128;
                             sts16(to + (((2 * c) ^ row8) << 4), make_uint4(y[0], y[1], y[2], y[3]));
                             sts16(to + (((2 * c + 1) ^ row8) << 4), make_uint4(y[4], y[5], y[6], y[7]));
@@ -457,22 +498,29 @@ __global__ void __launch_bounds__(Roles<CODE>::THREADS, 1) k_attn_tc(const __gri
         int g = 0;
         for (; ok && k.more(rng) && !a.debug_no_copy; k.next(a, rng)) {
             const int *trow = a.table + k.it.b * a.table_stride;
-            auto block_of = [&](int key) { return key < k.kv ? trow[a.by_S.div(key)] : -1; };
-            const int first = (k.kt0 + k.kt) * TK;
-            int blk = boxed ? block_of(first + bk) : -1;
-            for (int j = 0; j < k.nu; ++j, ++g) {
-                const int s = g & 1, key = first + j * TK + bk;
+            int key = (k.kt0 + k.kt) * TK + bk;
+            const int end = min(k.kv, key - bk + k.nu * TK);
+            auto block_of = [&](int key) { return boxed && key < end ? trow[a.by_S.div(key)] : -1; };
+            // the box's block and exponent and the next one's block: asked for a
+            // unit ahead, so that nothing waits for them
+            int blk = block_of(key), next = block_of(key + TK), e = 127;
+            auto ask = [&]() {
+                if (static_cast<unsigned>(blk) < static_cast<unsigned>(a.blocks))
+                    e = exps[static_cast<int64_t>(blk) * a.Hkv + k.it.head];
+            };
+            ask();
+            for (int j = 0; j < k.nu; ++j, ++g, key += TK) {
+                const int s = g & 1;
                 if (g >= 2 && !(ok = warp_wait(&empty[s], ((g >> 1) - 1) & 1))) break;
                 if (boxed) {
                     // a block outside the cache reads as zeros
                     mbar_expect_tx(&full[s], maps.kb * 128);
                     tma_load_4d(ring + s * Z::TILE + Z::CODES + bk * 128, map, 0, key - a.by_S.div(key) * a.S, k.it.head, blk, &full[s]);
-                    const int e = static_cast<unsigned>(blk) < static_cast<unsigned>(a.blocks)
-                                      ? exps[static_cast<int64_t>(blk) * a.Hkv + k.it.head]
-                                      : 127;
-                    blk = j + 1 < k.nu ? block_of(key + TK) : -1;
                     scales[((vals ? 2 : 0) + s) * 8 + lane] = Exponents<CODE == WIDE ? I8 : CODE, F16>::of(e);
                 }
+                blk = next;
+                next = block_of(key + 2 * TK);
+                ask();
                 mbar_arrive(&full[s]);
                 __syncwarp();
             }
