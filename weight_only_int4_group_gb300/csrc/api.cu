@@ -566,6 +566,8 @@ q4_status q4_cache_read8(const q4_kv_cache8 *cache, const int32_t *table, int64_
     if (k_stride < row || v_stride < row) return Q4_ERR_INVALID_ARG;
     if (k_stride > (1LL << 30) || v_stride > (1LL << 30)) return Q4_ERR_UNSUPPORTED;
     if (!aligned16(k_out) || !aligned16(v_out) || k_stride % 8 || v_stride % 8) return Q4_ERR_MISALIGNED;
+    const DevInfo *d = dev_info();
+    if (!d) return cuda_fail(cudaGetLastError());
     Read8Args a{};
     a.c = codes_of(cache);
     a.table = table;
@@ -580,7 +582,8 @@ q4_status q4_cache_read8(const q4_kv_cache8 *cache, const int32_t *table, int64_
     a.k_stride = k_stride;
     a.v_stride = v_stride;
     a.err = debug_err();
-    const cudaError_t e = read8_launch(a, cache->code, cache->type == Q4_F16, ot == Q4_F32, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = read8_launch(a, cache->code, cache->type == Q4_F16, ot == Q4_F32, d->sm_count,
+                                       reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? Q4_OK : cuda_fail(e);
 }
 

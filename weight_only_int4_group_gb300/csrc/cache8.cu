@@ -8,52 +8,56 @@ namespace q4 {
 // Memory-bound: qkv is read once, the queries are written in 16 bits and the
 // keys and values in 8.  What couples tokens is the scale of a block: the run
 // of new tokens in one block is looked at twice, for its largest magnitude and
-// to be quantised; the second look finds it in the first-level cache.
+// to be quantised; the second look finds it in a cache, or, for runs within a
+// chunk, in registers.
 //
-// A CTA takes a chunk of `rows` token rows and some heads of one kind: queries
+// A CTA takes a chunk of 32 token rows and some heads of one kind: queries
 // (rotated and stored), keys, or values.  For keys and values it owns the runs
 // that begin in its chunk, to their ends (a run is at most a block), so that no
-// two CTAs meet in a block.  A thread holds 8 elements of a row; their
+// two CTAs meet in a block.  A thread holds 16 elements of a row: two
+// 8-element loads that the rotation pairs (or that lie side by side), whose
 // angles serve all its heads.  Fractions of a turn are 64-bit integers
 // (position * frequency mod 1 in units of 2^-64): this card's f64 units would
 // take longer than the copy.
 namespace {
 
-constexpr int MOST_ROWS = 64;    // of a chunk
+constexpr int ROWS = 32;         // of a chunk
 constexpr int MOST_HEADS = 16;   // of a CTA
 constexpr int AHEAD = 2;         // heads whose loads are in flight in a thread
 
-// The pair partner's factors: y = x * c + partner * s.
-struct Turn {
-    float c[8], s[8];
-};
+// How a thread's elements are paired: its two vectors with each other; within
+// each, neighbours; or each with one somewhere (rot not a multiple of 16).
+enum Pairs { HALF, NEXT, ANY };
 
-template <bool INTER>
-__device__ __forceinline__ void angles(const Append8Args &a, const uint64_t *freq, int row, int d0, Turn &t)
+// freq / (2 pi) mod 1 in units of 2^-64: the 53-bit mantissa times 2^64 / (2 pi),
+// shifted by the exponent (0 for what is not finite).
+__device__ __forceinline__ uint64_t turns_of(double freq)
 {
-    const int half = a.rot / 2;
-    const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(d0 < a.rot ? a.position[row] : 0));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int d = d0 + i;
-        if (INTER && (i & 1)) {
-            t.c[i] = t.c[i - 1];
-            t.s[i] = -t.s[i - 1];
-            continue;
-        }
-        if (d >= a.rot) {
-            t.c[i] = 1.0f;
-            t.s[i] = 0.0f;
-            continue;
-        }
-        const bool first = INTER || d < half;
-        const uint64_t x = pos * freq[INTER ? d / 2 : first ? d : d - half];
-        float sn, cs;
-        // +-1/2 turn in units of 2^-32
-        sincospif(static_cast<float>(static_cast<int32_t>(x >> 32)) * 4.656612873077393e-10f, &sn, &cs);
-        t.c[i] = cs * a.factor;
-        t.s[i] = (first ? -sn : sn) * a.factor;
-    }
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(freq));
+    const int field = static_cast<int>(b >> 52) & 0x7FF;
+    if (field == 0x7FF) return 0;
+    const uint64_t m = (b & ((1ull << 52) - 1)) | (field ? 1ull << 52 : 0);
+    constexpr uint64_t per = 2935890503282001226ull;
+    const uint64_t hi = __umul64hi(m, per), lo = m * per;
+    const int s = 52 + 1023 - max(field, 1);  // m * per >> s
+    uint64_t f = 0;
+    if (s <= 0)
+        f = s > -64 ? lo << -s : 0;
+    else if (s < 64)
+        f = lo >> s | hi << (64 - s);
+    else if (s < 128)
+        f = hi >> (s - 64);
+    return b >> 63 ? ~f + 1 : f;
+}
+
+// Cosine and sine, times the factor, of pair p's angle.
+__device__ __forceinline__ float2 turn_of(const Append8Args &a, const uint64_t *freq, int64_t pos, int p)
+{
+    const uint64_t x = static_cast<uint64_t>(pos) * freq[p];
+    float sn, cs;
+    // +-1/2 turn in units of 2^-32
+    sincospif(static_cast<float>(static_cast<int32_t>(x >> 32)) * 4.656612873077393e-10f, &sn, &cs);
+    return make_float2(cs * a.factor, sn * a.factor);
 }
 
 __device__ __forceinline__ uint32_t half_of(const uint4 &v, int i)
@@ -62,41 +66,84 @@ __device__ __forceinline__ uint32_t half_of(const uint4 &v, int i)
     return (w >> (16 * (i & 1))) & 0xFFFFu;
 }
 
-// Elements d0 .. d0 + 7 of a head at x and their pair partners, and what the
-// rotation makes of them.  `vec`: the partners are 8 aligned elements too.
-struct Raw {
-    uint4 v, p;
+// A thread's 16 elements: 8 from e[0] on and 8 from e[1] on, which are rotated
+// (`turns`) or not.
+struct Place {
+    int e[2];
+    bool in, turns;
 };
+template <Pairs P>
+__device__ __forceinline__ Place place_of(int u, int D, int rot)
+{
+    Place p;
+    p.in = u * 16 < D;
+    const int pairs = rot / 16;
+    p.turns = P == HALF ? u < pairs : u * 16 < rot;
+    p.e[0] = P == HALF && p.turns ? u * 8 : u * 16;
+    p.e[1] = P == HALF && p.turns ? rot / 2 + u * 8 : u * 16 + 8;
+    return p;
+}
 
-template <bool INTER>
-__device__ __forceinline__ Raw load_raw(const uint16_t *x, int d0, int rot, bool vec)
+struct Raw {
+    uint4 v[2];
+};
+__device__ __forceinline__ Raw load_raw(const uint16_t *x, const Place &p)
 {
     Raw r;
-    r.v = *reinterpret_cast<const uint4 *>(x + d0);
-    r.p = make_uint4(0, 0, 0, 0);
-    if (INTER || d0 >= rot) return r;
-    const int half = rot / 2;
-    if (vec) {
-        r.p = *reinterpret_cast<const uint4 *>(x + (d0 < half ? d0 + half : d0 - half));
-        return r;
-    }
-    uint32_t w[4] = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int d = d0 + i;
-        if (d < rot) w[i / 2] |= static_cast<uint32_t>(x[d < half ? d + half : d - half]) << (16 * (i & 1));
-    }
-    r.p = make_uint4(w[0], w[1], w[2], w[3]);
+    r.v[0] = *reinterpret_cast<const uint4 *>(x + p.e[0]);
+    r.v[1] = *reinterpret_cast<const uint4 *>(x + p.e[1]);
     return r;
 }
 
-template <bool F16, bool INTER>
-__device__ __forceinline__ void rotate(const Raw &r, int d0, int rot, const Turn &t, float (&y)[8])
+// The elements of a head at x, rotated: t holds the angles of 8 pairs (ANY: they
+// are made here, and partners come from memory: `part` is the head as it was).
+template <Pairs P, bool F16>
+__device__ __forceinline__ void rotate(const Append8Args &a, const uint64_t *freq, int64_t pos, const uint16_t *part, const Raw &r,
+                                       const Place &p, int rot, const float2 (&t)[8], float (&y)[2][8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float x = bits_to_f32<F16>(half_of(r.v, i)), p = bits_to_f32<F16>(half_of(INTER ? r.v : r.p, INTER ? i ^ 1 : i));
-        y[i] = d0 + i < rot ? x * t.c[i] + p * t.s[i] : x;
+        const float x0 = bits_to_f32<F16>(half_of(r.v[0], i)), x1 = bits_to_f32<F16>(half_of(r.v[1], i));
+        y[0][i] = x0;
+        y[1][i] = x1;
+        if (P == HALF && p.turns) {
+            y[0][i] = x0 * t[i].x - x1 * t[i].y;
+            y[1][i] = x0 * t[i].y + x1 * t[i].x;
+        }
+    }
+    if (P == NEXT) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            if (p.e[0] + i >= rot) break;
+            float &lo = y[i / 8][i % 8], &hi = y[i / 8][i % 8 + 1];
+            const float x = lo, z = hi;
+            lo = x * t[i / 2].x - z * t[i / 2].y;
+            hi = x * t[i / 2].y + z * t[i / 2].x;
+        }
+    }
+    if (P == ANY) {
+        const int half = rot / 2;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int d = p.e[0] + i;
+            if (d >= rot) break;
+            const bool first = d < half;
+            const float z = bits_to_f32<F16>(part[first ? d + half : d - half]);
+            const float2 c = turn_of(a, freq, pos, first ? d : d - half);
+            float &o = y[i / 8][i % 8];
+            o = o * c.x + z * (first ? -c.y : c.y);
+        }
+    }
+}
+
+template <Pairs P>
+__device__ __forceinline__ void angles(const Append8Args &a, const uint64_t *freq, int64_t pos, const Place &p, int rot, float2 (&t)[8])
+{
+    if (P == ANY || !p.turns) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int pair = P == HALF ? p.e[0] + i : p.e[0] / 2 + i;
+        t[i] = pair < rot / 2 ? turn_of(a, freq, pos, pair) : make_float2(1.0f, 0.0f);
     }
 }
 
@@ -121,81 +168,94 @@ __device__ __forceinline__ bool begins(const int64_t *slot, int64_t slots, int S
 }
 
 struct AppendGrid {
-    int rows, lanes_log;  // token rows of a chunk; threads of a row, log 2
-    int gk, nk, gq;       // heads per CTA and CTAs for keys (and for values); heads per CTA for queries
+    int lanes_log;   // threads of a row, log 2
+    int gk, nk, gq;  // heads per CTA and CTAs for keys (and for values); heads per CTA for queries
 };
 
-template <int CODE, bool F16, bool INTER>
-__global__ void __launch_bounds__(1024) k_append8(const Append8Args a, const AppendGrid g)
+template <int CODE, bool F16, Pairs P>
+__global__ void __launch_bounds__(ROWS * 8, 3) k_append8(const Append8Args a, const AppendGrid g)
 {
     using X = Exponents<CODE, F16>;
     __shared__ uint64_t freq[64];
-    __shared__ unsigned starts[2];                   // rows of the chunk that begin a run
-    __shared__ int end_row;                          // behind the last run
-    __shared__ uint32_t peak[MOST_HEADS][MOST_ROWS]; // of the run that begins at a row
-    __shared__ int8_t scale[MOST_HEADS][MOST_ROWS], growth[MOST_HEADS][MOST_ROWS];
+    __shared__ unsigned starts;                 // rows of the chunk that begin a run
+    __shared__ int end_row;                     // behind the last run
+    __shared__ uint32_t peak[MOST_HEADS][ROWS]; // of the run that begins at a row
+    __shared__ int8_t scale[MOST_HEADS][ROWS], growth[MOST_HEADS][ROWS];
     const int tid = threadIdx.x, S = a.c.S, D = a.c.D;
-    const int d0 = (tid & ((1 << g.lanes_log) - 1)) * 8, i = tid >> g.lanes_log;
-    const int c0 = blockIdx.x * g.rows, rows = min(g.rows, a.T - c0);
-    const int part = blockIdx.y;
-    const bool keys = part < g.nk, queries = part >= 2 * g.nk;
-    const bool vec = a.rot / 2 % 8 == 0;
+    const int i = tid >> g.lanes_log, u = tid & ((1 << g.lanes_log) - 1);
+    const int c0 = blockIdx.x * ROWS, rows = min(ROWS, a.T - c0);
+    const int kind = blockIdx.y;
+    const bool keys = kind < g.nk, queries = kind >= 2 * g.nk;
     const int rot = keys || queries ? a.rot : 0;
+    const Place p = place_of<P>(u, D, rot);
+    const int h0 = queries ? (kind - 2 * g.nk) * g.gq : (keys ? kind : kind - g.nk) * g.gk;
+    const int nh = queries ? min(g.gq, a.Hq - h0) : min(g.gk, a.c.heads - h0);
+    // the CTA's first head in a row of qkv
+    const uint16_t *qkv = a.qkv + static_cast<int64_t>((queries ? 0 : a.Hq + (keys ? 0 : a.c.heads)) + h0) * D;
 
     grid_dep_wait();
     grid_dep_launch_dependents();
-    if (tid < rot / 2) {
-        const double turns = a.freq[tid] * 0.15915494309189535;
-        freq[tid] = __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
-    }
+    Raw raw[AHEAD];
+    auto head = [&](int row, int h) { return qkv + row * a.qkv_stride + h * D; };
+    auto load = [&](int row, int h) {  // heads h .. of the CTA
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n)
+            if (h + n < nh) raw[n] = load_raw(head(row, h + n), p);
+    };
+    if (i < rows && p.in) load(c0 + i, 0);
+    if (tid < rot / 2) freq[tid] = turns_of(a.freq[tid]);
+    float2 t[8];
     if (queries) {
         __syncthreads();
-        if (i >= rows || d0 >= D) return;
-        const int row = c0 + i, h0 = (part - 2 * g.nk) * g.gq, h1 = min(h0 + g.gq, a.Hq);
-        Turn t;
-        angles<INTER>(a, freq, row, d0, t);
-        const uint16_t *x = a.qkv + row * a.qkv_stride;
-        const int64_t at = row * a.q_stride + d0, len = (a.T - 1) * a.q_stride + static_cast<int64_t>(a.Hq) * D;
-        for (int h = h0; h < h1; h += AHEAD) {
-            Raw raw[AHEAD];
+        if (i >= rows) return;  // (whole heads)
+        const int row = c0 + i;
+        const int64_t pos = rot ? a.position[row] : 0;
+        if (p.in) angles<P>(a, freq, pos, p, rot, t);
+        const int64_t at = row * a.q_stride + h0 * D, len = (a.T - 1) * a.q_stride + static_cast<int64_t>(a.Hq) * D;
+        for (int h = 0; h < nh; h += AHEAD) {
+            if (h > 0 && p.in) load(row, h);
+            float y[AHEAD][2][8];
 #pragma unroll
             for (int n = 0; n < AHEAD; ++n)
-                if (h + n < h1) raw[n] = load_raw<INTER>(x + (h + n) * D, d0, rot, vec);
+                if (h + n < nh && p.in) rotate<P, F16>(a, freq, pos, head(row, h + n), raw[n], p, rot, t, y[n]);
             __syncwarp();  // q_out may be qkv: a head's lanes have read it before one writes
 #pragma unroll
             for (int n = 0; n < AHEAD; ++n) {
-                float y[8];
-                rotate<F16, INTER>(raw[n], d0, rot, t, y);
-                if (h + n < h1 && store_ok(at + (h + n) * D + 7, len, a.err))
-                    *reinterpret_cast<uint4 *>(a.q_out + at + (h + n) * D) =
-                        make_uint4(pack16<F16>(y[0], y[1]), pack16<F16>(y[2], y[3]), pack16<F16>(y[4], y[5]),
-                                   pack16<F16>(y[6], y[7]));
+                if (h + n >= nh || !p.in) break;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int64_t to = at + (h + n) * D + p.e[e];
+                    const float (&z)[8] = y[n][e];
+                    if (store_ok(to + 7, len, a.err))
+                        *reinterpret_cast<uint4 *>(a.q_out + to) = make_uint4(pack16<F16>(z[0], z[1]), pack16<F16>(z[2], z[3]),
+                                                                              pack16<F16>(z[4], z[5]), pack16<F16>(z[6], z[7]));
+                }
             }
         }
         return;
     }
 
     // ---- keys or values: the runs
-    const int h0 = (keys ? part : part - g.nk) * g.gk, nh = min(g.gk, a.c.heads - h0);
     uint8_t *codes = keys ? a.c.k : a.c.v, *exps = keys ? a.c.k_exp : a.c.v_exp;
     const int64_t slots = static_cast<int64_t>(a.c.blocks) * S;
     const int64_t codes_len = (a.c.blocks - 1) * a.c.block_stride + (a.c.heads - 1) * a.c.head_stride +
                               (S - 1) * a.c.token_stride + D;
-    const uint16_t *qkv = a.qkv + static_cast<int64_t>(a.Hq + (keys ? 0 : a.c.heads) + h0) * D;
-    if (tid == 0) end_row = min(c0 + rows + S, a.T);
-    if (tid < 64) {
+    if (tid < 32) {
         const unsigned m = __ballot_sync(0xffffffffu, tid < rows && begins(a.slot, slots, S, c0 + tid));
-        if ((tid & 31) == 0) starts[tid >> 5] = m;
+        if (tid == 0) {
+            starts = m;
+            end_row = min(c0 + rows + S, a.T);
+        }
+        for (int h = 0; h < nh; ++h) peak[h][tid] = 0u;
     }
-    for (int n = tid; n < nh * MOST_ROWS; n += blockDim.x) peak[n / MOST_ROWS][n % MOST_ROWS] = 0u;
     __syncthreads();
-    const uint64_t mask = starts[0] | static_cast<uint64_t>(starts[1]) << 32;
+    const unsigned mask = starts;
     if (!mask) return;
-    for (int t = c0 + rows + tid; t < min(c0 + rows + S, a.T); t += blockDim.x)
-        if (begins(a.slot, slots, S, t)) atomicMin(&end_row, t);
+    for (int x = c0 + rows + tid; x < min(c0 + rows + S, a.T); x += blockDim.x)
+        if (begins(a.slot, slots, S, x)) atomicMin(&end_row, x);
     __syncthreads();
     const int end = end_row;
-    // of a row: the chunk's row that its run begins at (-1: another chunk's), and its place
+    // of a row: the chunk's row that its run begins at (-1: none of the chunk's), and its slot
     struct Row {
         int lead;
         int64_t slot;
@@ -203,46 +263,45 @@ __global__ void __launch_bounds__(1024) k_append8(const Append8Args a, const App
     auto row_of = [&](int row) {
         Row r = {-1, -1};
         if (row >= end) return r;
-        const uint64_t upto = row - c0 >= 63 ? mask : mask & ((2ull << (row - c0)) - 1);
+        const unsigned upto = row - c0 >= ROWS - 1 ? mask : mask & ((2u << (row - c0)) - 1);
         if (!upto) return r;
         r.slot = a.slot[row];
-        if (r.slot < 0 || r.slot >= slots) return r;
-        r.lead = 63 - __clzll(static_cast<long long>(upto));
+        if (r.slot >= 0 && r.slot < slots) r.lead = 31 - __clz(upto);
         return r;
     };
+    const bool once = end <= c0 + ROWS && nh <= AHEAD;  // one look: the elements stay in registers
+    Row r;
+    int64_t pos = 0;
     // ---- largest magnitudes
-    for (int r0 = c0; r0 < end; r0 += g.rows) {
-        const Row r = row_of(r0 + i);
-        const bool on = r.lead >= 0 && d0 < D;
-        Turn t;
-        if (on) angles<INTER>(a, freq, r0 + i, keys ? d0 : 128, t);
+    for (int r0 = c0; r0 < end; r0 += ROWS) {
+        r = row_of(r0 + i);
+        const bool on = r.lead >= 0 && p.in;
+        if (on && rot) pos = a.position[r0 + i];
+        if (on) angles<P>(a, freq, pos, p, rot, t);
         for (int h = 0; h < nh; h += AHEAD) {
-            Raw raw[AHEAD];
-#pragma unroll
-            for (int n = 0; n < AHEAD; ++n)
-                if (on && h + n < nh) raw[n] = load_raw<INTER>(qkv + (r0 + i) * a.qkv_stride + (h + n) * D, d0, rot, vec);
+            if (on && (r0 > c0 || h > 0)) load(r0 + i, h);
 #pragma unroll
             for (int n = 0; n < AHEAD; ++n) {
                 if (h + n >= nh) break;
                 float m = 0.0f;
                 if (on) {
-                    float y[8];
-                    rotate<F16, INTER>(raw[n], d0, rot, t, y);
+                    float y[2][8];
+                    rotate<P, F16>(a, freq, pos, head(r0 + i, h + n), raw[n], p, rot, t, y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float v = fabsf(y[e]);
+                    for (int e = 0; e < 16; ++e) {
+                        const float v = fabsf(y[e / 8][e % 8]);
                         m = v <= 3.4028234664e38f ? fmaxf(m, v) : m;  // infinities and NaN do not count
                     }
                 }
                 for (int d = 1 << g.lanes_log >> 1; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                if (r.lead >= 0 && d0 == 0) atomicMax(&peak[h + n][r.lead], __float_as_uint(m));
+                if (r.lead >= 0 && u == 0) atomicMax(&peak[h + n][r.lead], __float_as_uint(m));
             }
         }
     }
     __syncthreads();
     // ---- the runs' scales
-    for (int n = tid; n < nh * g.rows; n += blockDim.x) {
-        const int h = n / g.rows, lead = n - h * g.rows;
+    for (int n = tid; n < nh * ROWS; n += blockDim.x) {
+        const int h = n / ROWS, lead = n % ROWS;
         if (!(mask >> lead & 1)) continue;
         growth[h][lead] = 0;
         const int64_t slot = a.slot[c0 + lead];
@@ -253,7 +312,7 @@ __global__ void __launch_bounds__(1024) k_append8(const Append8Args a, const App
         if (slot != blk * S) {
             const int old = X::of(*at);
             if (e > old)
-                growth[h][lead] = static_cast<int8_t>(min(e - old, 127));
+                growth[h][lead] = static_cast<int8_t>(e - old);
             else
                 e = old;
         }
@@ -262,39 +321,39 @@ __global__ void __launch_bounds__(1024) k_append8(const Append8Args a, const App
     }
     __syncthreads();
     // ---- the new codes
-    for (int r0 = c0; r0 < end; r0 += g.rows) {
-        const Row r = row_of(r0 + i);
-        if (r.lead < 0 || d0 >= D) continue;
-        Turn t;
-        angles<INTER>(a, freq, r0 + i, keys ? d0 : 128, t);
+    for (int r0 = c0; r0 < end; r0 += ROWS) {
+        if (!once) r = row_of(r0 + i);
+        if (r.lead < 0 || !p.in) continue;
+        if (!once && rot) pos = a.position[r0 + i];
+        if (!once) angles<P>(a, freq, pos, p, rot, t);
         const int64_t blk = r.slot / S;
-        const int64_t at = blk * a.c.block_stride + (r.slot - blk * S) * a.c.token_stride + h0 * a.c.head_stride + d0;
+        const int64_t at = blk * a.c.block_stride + (r.slot - blk * S) * a.c.token_stride + h0 * a.c.head_stride;
         for (int h = 0; h < nh; h += AHEAD) {
-            Raw raw[AHEAD];
-#pragma unroll
-            for (int n = 0; n < AHEAD; ++n)
-                if (h + n < nh) raw[n] = load_raw<INTER>(qkv + (r0 + i) * a.qkv_stride + (h + n) * D, d0, rot, vec);
+            if (!once) load(r0 + i, h);
 #pragma unroll
             for (int n = 0; n < AHEAD; ++n) {
                 if (h + n >= nh) break;
-                float y[8];
-                rotate<F16, INTER>(raw[n], d0, rot, t, y);
+                float y[2][8];
+                rotate<P, F16>(a, freq, pos, head(r0 + i, h + n), raw[n], p, rot, t, y);
                 const float inv = pow2(-scale[h + n][r.lead]);
-                const float lo[4] = {y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv};
-                const float hi[4] = {y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv};
-                const int64_t to = at + (h + n) * a.c.head_stride;
-                if (store_ok(to + 7, codes_len, a.err))
-                    *reinterpret_cast<uint2 *>(codes + to) = make_uint2(f32_to_codes<CODE>(lo), f32_to_codes<CODE>(hi));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float lo[4] = {y[e][0] * inv, y[e][1] * inv, y[e][2] * inv, y[e][3] * inv};
+                    const float hi[4] = {y[e][4] * inv, y[e][5] * inv, y[e][6] * inv, y[e][7] * inv};
+                    const int64_t to = at + (h + n) * a.c.head_stride + p.e[e];
+                    if (store_ok(to + 7, codes_len, a.err))
+                        *reinterpret_cast<uint2 *>(codes + to) = make_uint2(f32_to_codes<CODE>(lo), f32_to_codes<CODE>(hi));
+                }
             }
         }
     }
     // ---- codes held already, where the scale grew: a warp per run and head
     const int warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5, pieces = D / 16;
-    for (int n = warp; n < nh * g.rows; n += warps) {
-        const int h = n / g.rows, lead = n - h * g.rows;
+    for (int n = warp; n < nh * ROWS; n += warps) {
+        const int h = n / ROWS, lead = n % ROWS;
         if (!(mask >> lead & 1) || growth[h][lead] == 0) continue;
         const int64_t slot = a.slot[c0 + lead], blk = slot / S;
-        const float f = pow2(-min(static_cast<int>(growth[h][lead]), 126));
+        const float f = pow2(-growth[h][lead]);
         const int64_t base = blk * a.c.block_stride + (h0 + h) * a.c.head_stride;
         for (int u = lane; u < static_cast<int>(slot - blk * S) * pieces; u += 32) {
             const int64_t at = base + u / pieces * a.c.token_stride + u % pieces * 16;
@@ -317,30 +376,39 @@ template <int CODE, bool F16>
 cudaError_t append_launch(const Append8Args &a, bool interleaved, int sm_count, cudaStream_t s)
 {
     AppendGrid g{};
-    g.lanes_log = a.c.D > 64 ? 4 : 3;
-    g.rows = a.c.S >= 64 ? 64 : a.c.S >= 32 ? 32 : 16;
-    const int chunks = ctas_for(a.T, g.rows);
+    g.lanes_log = a.c.D > 64 ? 3 : 2;
+    const int chunks = ctas_for(a.T, ROWS);
     // heads per CTA: fewer where there are few chunks
-    g.gk = std::min({std::max(1, static_cast<int>(static_cast<int64_t>(chunks) * 2 * a.c.heads / (4 * sm_count))), a.c.heads, 8});
+    const auto heads_for = [&](int64_t heads, int most) {
+        return static_cast<int>(std::min<int64_t>({std::max<int64_t>(1, chunks * heads / (6 * sm_count)), heads, most}));
+    };
+    g.gk = heads_for(2 * a.c.heads, std::min(a.c.heads, 4));
     g.nk = ctas_for(a.c.heads, g.gk);
-    g.gq = std::min({std::max(1, static_cast<int>(static_cast<int64_t>(chunks) * a.Hq / (4 * sm_count))), a.Hq, 16});
+    g.gq = heads_for(a.Hq, 16);
     const dim3 grid(chunks, 2 * g.nk + ctas_for(a.Hq, g.gq));
-    const int threads = g.rows << g.lanes_log;
-    return interleaved ? launch_dependent(k_append8<CODE, F16, true>, grid, threads, 0, s, a, g)
-                       : launch_dependent(k_append8<CODE, F16, false>, grid, threads, 0, s, a, g);
+    const int threads = ROWS << g.lanes_log;
+    if (interleaved) return launch_dependent(k_append8<CODE, F16, NEXT>, grid, threads, 0, s, a, g);
+    if (a.rot % 16) return launch_dependent(k_append8<CODE, F16, ANY>, grid, threads, 0, s, a, g);
+    return launch_dependent(k_append8<CODE, F16, HALF>, grid, threads, 0, s, a, g);
 }
 
 // -------------------------------------------------------------- reading back
-// Memory-bound: a byte in, two (or four) out.  A CTA takes 32 token rows, finds
-// their requests (one warp), and each thread widens 16 codes at a time.
-constexpr int READ_ROWS = 32, READ_THREADS = 256;
+// Memory-bound: a byte in, two (or four) out.  A CTA takes up to 32 token rows,
+// finds their requests (one warp), and each thread widens 16 codes at a time,
+// four such pieces in flight.
+constexpr int READ_ROWS = 32, READ_THREADS = 256, READ_AHEAD = 4;
+
+struct ReadGrid {
+    int rows;               // of a CTA
+    FastDiv by_row, by_head;  // pieces of a row's keys and values; of a head
+};
 
 template <int CODE, bool F16, bool F32>
-__global__ void __launch_bounds__(READ_THREADS) k_read8(const Read8Args a)
+__global__ void __launch_bounds__(READ_THREADS) k_read8(const Read8Args a, const ReadGrid g)
 {
     __shared__ int64_t place[READ_ROWS];  // of a row's token in the codes; -1: zeros, -2: no request
     __shared__ int block[READ_ROWS];
-    const int tid = threadIdx.x, t0 = blockIdx.x * READ_ROWS, rows = min(READ_ROWS, a.T - t0);
+    const int tid = threadIdx.x, t0 = blockIdx.x * g.rows, rows = min(g.rows, a.T - t0);
     grid_dep_wait();
     grid_dep_launch_dependents();
     if (tid < 32) {
@@ -374,50 +442,70 @@ __global__ void __launch_bounds__(READ_THREADS) k_read8(const Read8Args a)
         block[tid] = blk;
     }
     __syncthreads();
-    const int pieces = a.c.D / 16, per = a.c.heads * pieces;  // 16-code pieces of a row's keys
-    for (int n = tid; n < rows * 2 * per; n += READ_THREADS) {
-        const int r = n / (2 * per), u = n - r * 2 * per;
-        const int64_t at = place[r];
-        if (at == -2) continue;
-        const bool vals = u >= per;
-        const int w = vals ? u - per : u, h = w / pieces, c = w - h * pieces;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        float f = 1.0f;
-        if (at >= 0) {
-            v = __ldcs(reinterpret_cast<const uint4 *>((vals ? a.c.v : a.c.k) + at + h * a.c.head_stride + c * 16));
-            f = pow2(Exponents<CODE, F16>::of((vals ? a.c.v_exp : a.c.k_exp)[static_cast<int64_t>(block[r]) * a.c.heads + h]));
+    const int per = a.c.heads * (a.c.D / 16);  // pieces of a row's keys
+    const int total = rows * 2 * per;
+    for (int n0 = tid; n0 < total; n0 += READ_AHEAD * READ_THREADS) {
+        uint4 v[READ_AHEAD];
+        int e[READ_AHEAD];
+        int64_t to[READ_AHEAD];  // -1: nothing
+        bool vals[READ_AHEAD];
+#pragma unroll
+        for (int x = 0; x < READ_AHEAD; ++x) {
+            const int n = n0 + x * READ_THREADS, r = g.by_row.div(min(n, total - 1)), u = n - r * 2 * per;
+            const int64_t at = place[r];
+            vals[x] = u >= per;
+            const int w = vals[x] ? u - per : u, h = g.by_head.div(max(w, 0)), c = w - h * (a.c.D / 16);
+            v[x] = make_uint4(0, 0, 0, 0);
+            e[x] = 127;
+            to[x] = n < total && at != -2 ? (t0 + r) * (vals[x] ? a.v_stride : a.k_stride) + w * 16 : -1;
+            if (n < total && at >= 0) {
+                v[x] = __ldcs(reinterpret_cast<const uint4 *>((vals[x] ? a.c.v : a.c.k) + at + h * a.c.head_stride + c * 16));
+                e[x] = (vals[x] ? a.c.v_exp : a.c.k_exp)[static_cast<int64_t>(block[r]) * a.c.heads + h];
+            }
         }
-        const int64_t stride = vals ? a.v_stride : a.k_stride, to = (t0 + r) * stride + w * 16;
-        if (!store_ok(to + 15, (a.T - 1) * stride + static_cast<int64_t>(a.c.heads) * a.c.D, a.err)) continue;
-        void *out = vals ? a.v_out : a.k_out;
-        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-        float x[4][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            codes_to_f32<CODE>(words[e], x[e]);
+        for (int x = 0; x < READ_AHEAD; ++x) {
+            if (to[x] < 0) continue;
+            if (!store_ok(to[x] + 15, (a.T - 1) * (vals[x] ? a.v_stride : a.k_stride) + static_cast<int64_t>(a.c.heads) * a.c.D, a.err))
+                continue;
+            void *out = vals[x] ? a.v_out : a.k_out;
+            const float f = pow2(Exponents<CODE, F16>::of(e[x]));
+            const uint32_t words[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+            float y[16];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) x[e][b] *= f;
-        }
-        if (F32) {
-            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + to);
+            for (int q = 0; q < 4; ++q) {
+                float z[4];
+                codes_to_f32<CODE>(words[q], z);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = make_float4(x[e][0], x[e][1], x[e][2], x[e][3]);
-        } else {
-            uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + to);
+                for (int b = 0; b < 4; ++b) y[4 * q + b] = z[b] * f;
+            }
+            if (F32) {
+                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + to[x]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                o[e] = make_uint4(pack16<F16>(x[2 * e][0], x[2 * e][1]), pack16<F16>(x[2 * e][2], x[2 * e][3]),
-                                  pack16<F16>(x[2 * e + 1][0], x[2 * e + 1][1]), pack16<F16>(x[2 * e + 1][2], x[2 * e + 1][3]));
+                for (int q = 0; q < 4; ++q) __stcs(o + q, make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]));
+            } else {
+                uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + to[x]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    __stcs(o + q, make_uint4(pack16<F16>(y[8 * q], y[8 * q + 1]), pack16<F16>(y[8 * q + 2], y[8 * q + 3]),
+                                             pack16<F16>(y[8 * q + 4], y[8 * q + 5]), pack16<F16>(y[8 * q + 6], y[8 * q + 7])));
+            }
         }
     }
 }
 
 template <int CODE, bool F16>
-cudaError_t read_launch(const Read8Args &a, bool f32_out, cudaStream_t s)
+cudaError_t read_launch(const Read8Args &a, bool f32_out, int sm_count, cudaStream_t s)
 {
-    const dim3 grid(ctas_for(a.T, READ_ROWS));
-    return f32_out ? launch_dependent(k_read8<CODE, F16, true>, grid, READ_THREADS, 0, s, a)
-                   : launch_dependent(k_read8<CODE, F16, false>, grid, READ_THREADS, 0, s, a);
+    ReadGrid g{};
+    const int per = 2 * a.c.heads * (a.c.D / 16);
+    g.by_row.set(per);
+    g.by_head.set(a.c.D / 16);
+    // 16 pieces a thread, fewer where that leaves SMs without a CTA
+    g.rows = std::max(1, std::min({READ_ROWS, 16 * READ_THREADS / per, ctas_for(a.T, 4 * sm_count)}));
+    const dim3 grid(ctas_for(a.T, g.rows));
+    return f32_out ? launch_dependent(k_read8<CODE, F16, true>, grid, READ_THREADS, 0, s, a, g)
+                   : launch_dependent(k_read8<CODE, F16, false>, grid, READ_THREADS, 0, s, a, g);
 }
 
 }  // namespace
@@ -428,10 +516,10 @@ cudaError_t append8_launch(const Append8Args &a, q4_code code, bool f16, bool in
     return f16 ? append_launch<E4M3, true>(a, interleaved, sm_count, s) : append_launch<E4M3, false>(a, interleaved, sm_count, s);
 }
 
-cudaError_t read8_launch(const Read8Args &a, q4_code code, bool f16, bool f32_out, cudaStream_t s)
+cudaError_t read8_launch(const Read8Args &a, q4_code code, bool f16, bool f32_out, int sm_count, cudaStream_t s)
 {
-    if (code == Q4_I8) return f16 ? read_launch<I8, true>(a, f32_out, s) : read_launch<I8, false>(a, f32_out, s);
-    return f16 ? read_launch<E4M3, true>(a, f32_out, s) : read_launch<E4M3, false>(a, f32_out, s);
+    if (code == Q4_I8) return f16 ? read_launch<I8, true>(a, f32_out, sm_count, s) : read_launch<I8, false>(a, f32_out, sm_count, s);
+    return f16 ? read_launch<E4M3, true>(a, f32_out, sm_count, s) : read_launch<E4M3, false>(a, f32_out, sm_count, s);
 }
 
 }  // namespace q4

@@ -134,7 +134,7 @@ struct Read8Args {
     int64_t k_stride, v_stride;
     unsigned int *err;
 };
-cudaError_t read8_launch(const Read8Args &a, q4_code code, bool f16, bool f32_out, cudaStream_t s);
+cudaError_t read8_launch(const Read8Args &a, q4_code code, bool f16, bool f32_out, int sm_count, cudaStream_t s);
 
 AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count);
 cudaError_t attention8_tc_launch(int grid, const AttnArgs &a, q4_code code, bool f16, cudaStream_t s);
