@@ -8,8 +8,8 @@ namespace q4 {
 // Memory-bound: qkv is read once, the queries are written in 16 bits and the
 // keys and values in 8.  What couples tokens is the scale of a block: the run
 // of new tokens in one block is looked at twice, for its largest magnitude and
-// to be quantised; the second look finds it in a cache, or, for runs within a
-// chunk, in registers.
+// to be quantised; the second look finds it in a cache, or, where one head is all
+// that a CTA has of a run within its chunk, in registers.
 //
 // A CTA takes a chunk of 32 token rows and some heads of one kind: queries
 // (rotated and stored), keys, or values.  For keys and values it owns the runs
@@ -22,8 +22,8 @@ namespace q4 {
 namespace {
 
 constexpr int ROWS = 32;         // of a chunk
-constexpr int MOST_HEADS = 16;   // of a CTA
-constexpr int AHEAD = 2;         // heads whose loads are in flight in a thread
+constexpr int MOST_HEADS = 8;    // of a CTA, keys or values
+constexpr int AHEAD = 1;         // heads whose loads are in flight in a thread
 
 // How a thread's elements are paired: its two vectors with each other; within
 // each, neighbours; or each with one somewhere (rot not a multiple of 16).
@@ -53,11 +53,17 @@ __device__ __forceinline__ uint64_t turns_of(double freq)
 // Cosine and sine, times the factor, of pair p's angle.
 __device__ __forceinline__ float2 turn_of(const Append8Args &a, const uint64_t *freq, int64_t pos, int p)
 {
-    const uint64_t x = static_cast<uint64_t>(pos) * freq[p];
-    float sn, cs;
-    // +-1/2 turn in units of 2^-32
-    sincospif(static_cast<float>(static_cast<int32_t>(x >> 32)) * 4.656612873077393e-10f, &sn, &cs);
-    return make_float2(cs * a.factor, sn * a.factor);
+    // The turn's quarter by rounding, what is left as +-1/8 turn in units of 2^-32,
+    // pi / 4 at most: there the Taylor polynomials end within 2e-9 (sine, to the
+    // 9th power) and 2e-10 (cosine, to the 10th).
+    const uint32_t x = static_cast<uint32_t>(static_cast<uint64_t>(pos) * freq[p] >> 32);
+    const uint32_t quarter = (x + 0x20000000u) >> 30;
+    const float r = static_cast<float>(static_cast<int32_t>(x - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+    const float q = r * r;
+    const float sn = fmaf(r * q, fmaf(q, fmaf(q, fmaf(q, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), r);
+    const float cs = fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+    const float c = quarter & 1 ? sn : cs, s = quarter & 1 ? cs : sn;
+    return make_float2((quarter + 1) & 2 ? -c * a.factor : c * a.factor, quarter & 2 ? -s * a.factor : s * a.factor);
 }
 
 __device__ __forceinline__ uint32_t half_of(const uint4 &v, int i)
@@ -173,14 +179,15 @@ struct AppendGrid {
 };
 
 template <int CODE, bool F16, Pairs P>
-__global__ void __launch_bounds__(ROWS * 8, 3) k_append8(const Append8Args a, const AppendGrid g)
+__global__ void __launch_bounds__(ROWS * 8, 4) k_append8(const Append8Args a, const AppendGrid g)
 {
     using X = Exponents<CODE, F16>;
     __shared__ uint64_t freq[64];
-    __shared__ unsigned starts;                 // rows of the chunk that begin a run
+    __shared__ unsigned starts[8];              // rows that begin a run: the chunk's, and those behind it
     __shared__ int end_row;                     // behind the last run
     __shared__ uint32_t peak[MOST_HEADS][ROWS]; // of the run that begins at a row
     __shared__ int8_t scale[MOST_HEADS][ROWS], growth[MOST_HEADS][ROWS];
+    __shared__ int odd;  // some element is not finite, or past the codes at the range's end
     const int tid = threadIdx.x, S = a.c.S, D = a.c.D;
     const int i = tid >> g.lanes_log, u = tid & ((1 << g.lanes_log) - 1);
     const int c0 = blockIdx.x * ROWS, rows = min(ROWS, a.T - c0);
@@ -240,21 +247,42 @@ __global__ void __launch_bounds__(ROWS * 8, 3) k_append8(const Append8Args a, co
     const int64_t slots = static_cast<int64_t>(a.c.blocks) * S;
     const int64_t codes_len = (a.c.blocks - 1) * a.c.block_stride + (a.c.heads - 1) * a.c.head_stride +
                               (S - 1) * a.c.token_stride + D;
-    if (tid < 32) {
-        const unsigned m = __ballot_sync(0xffffffffu, tid < rows && begins(a.slot, slots, S, c0 + tid));
+    {
+        const unsigned m = __ballot_sync(0xffffffffu, c0 + tid < a.T && begins(a.slot, slots, S, c0 + tid));
+        if ((tid & 31) == 0) starts[tid >> 5] = m;
+        if (tid < 32)
+            for (int h = 0; h < nh; ++h) peak[h][tid] = 0u;
         if (tid == 0) {
-            starts = m;
-            end_row = min(c0 + rows + S, a.T);
+            end_row = min(c0 + ROWS + S, a.T);
+            odd = 0;
         }
-        for (int h = 0; h < nh; ++h) peak[h][tid] = 0u;
     }
     __syncthreads();
-    const unsigned mask = starts;
+    const unsigned mask = starts[0];
     if (!mask) return;
-    for (int x = c0 + rows + tid; x < min(c0 + rows + S, a.T); x += blockDim.x)
-        if (begins(a.slot, slots, S, x)) atomicMin(&end_row, x);
-    __syncthreads();
-    const int end = end_row;
+    int end = end_row;
+    for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w)
+        if (starts[w]) {
+            end = min(end, c0 + w * 32 + __ffs(starts[w]) - 1);
+            break;
+        }
+    if (end > c0 + static_cast<int>(blockDim.x)) {  // blocks larger than the look
+        __syncthreads();
+        for (int x = c0 + blockDim.x + tid; x < min(c0 + ROWS + S, a.T); x += blockDim.x)
+            if (begins(a.slot, slots, S, x)) atomicMin(&end_row, x);
+        __syncthreads();
+        end = end_row;
+    }
+    // the exponents of continued blocks, asked for now
+    int old[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int n = tid + x * blockDim.x, lead = n % ROWS;
+        old[x] = 0;
+        if (n >= nh * ROWS || !(mask >> lead & 1)) continue;
+        const int64_t slot = a.slot[c0 + lead];
+        if (slot >= 0 && slot < slots) old[x] = exps[slot / S * a.c.heads + h0 + n / ROWS];
+    }
     // of a row: the chunk's row that its run begins at (-1: none of the chunk's), and its slot
     struct Row {
         int lead;
@@ -270,16 +298,18 @@ __global__ void __launch_bounds__(ROWS * 8, 3) k_append8(const Append8Args a, co
         return r;
     };
     const bool once = end <= c0 + ROWS && nh <= AHEAD;  // one look: the elements stay in registers
+    static_assert(MOST_HEADS * ROWS <= 2 * ROWS * 4, "two of the runs' scales per thread");
     Row r;
     int64_t pos = 0;
     // ---- largest magnitudes
     for (int r0 = c0; r0 < end; r0 += ROWS) {
+        if (r0 > c0 && p.in && r0 + i < a.T) load(r0 + i, 0);
         r = row_of(r0 + i);
         const bool on = r.lead >= 0 && p.in;
         if (on && rot) pos = a.position[r0 + i];
         if (on) angles<P>(a, freq, pos, p, rot, t);
         for (int h = 0; h < nh; h += AHEAD) {
-            if (on && (r0 > c0 || h > 0)) load(r0 + i, h);
+            if (on && h > 0) load(r0 + i, h);
 #pragma unroll
             for (int n = 0; n < AHEAD; ++n) {
                 if (h + n >= nh) break;
@@ -288,9 +318,15 @@ __global__ void __launch_bounds__(ROWS * 8, 3) k_append8(const Append8Args a, co
                     float y[2][8];
                     rotate<P, F16>(a, freq, pos, head(r0 + i, h + n), raw[n], p, rot, t, y);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float v = fabsf(y[e / 8][e % 8]);
-                        m = v <= 3.4028234664e38f ? fmaxf(m, v) : m;  // infinities and NaN do not count
+                    for (int e = 0; e < 16; ++e) m = max_nan(m, fabsf(y[e / 8][e % 8]));
+                    if (!(m <= 3.4028234664e38f)) {  // infinities and NaN do not count
+                        m = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float v = fabsf(y[e / 8][e % 8]);
+                            m = v <= 3.4028234664e38f ? fmaxf(m, v) : m;
+                        }
+                        odd = 1;
                     }
                 }
                 for (int d = 1 << g.lanes_log >> 1; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -300,28 +336,32 @@ __global__ void __launch_bounds__(ROWS * 8, 3) k_append8(const Append8Args a, co
     }
     __syncthreads();
     // ---- the runs' scales
-    for (int n = tid; n < nh * ROWS; n += blockDim.x) {
-        const int h = n / ROWS, lead = n % ROWS;
-        if (!(mask >> lead & 1)) continue;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int n = tid + x * blockDim.x, h = n / ROWS, lead = n % ROWS;
+        if (n >= nh * ROWS || !(mask >> lead & 1)) continue;
         growth[h][lead] = 0;
         const int64_t slot = a.slot[c0 + lead];
         if (slot < 0 || slot >= slots) continue;
         const int64_t blk = slot / S;
         uint8_t *at = exps + blk * a.c.heads + h0 + h;
         int e = needed<CODE, F16>(peak[h][lead]);
+        if (e == X::HI) odd = 1;
         if (slot != blk * S) {
-            const int old = X::of(*at);
-            if (e > old)
-                growth[h][lead] = static_cast<int8_t>(e - old);
+            const int held = X::of(old[x]);
+            if (e > held)
+                growth[h][lead] = static_cast<int8_t>(e - held);
             else
-                e = old;
+                e = held;
         }
         scale[h][lead] = static_cast<int8_t>(e);
         if (store_ok(at - exps, static_cast<int64_t>(a.c.blocks) * a.c.heads, a.err)) *at = static_cast<uint8_t>(e + 127);
     }
     __syncthreads();
     // ---- the new codes
+    const bool special = odd;
     for (int r0 = c0; r0 < end; r0 += ROWS) {
+        if (!once && p.in && r0 + i < a.T) load(r0 + i, 0);
         if (!once) r = row_of(r0 + i);
         if (r.lead < 0 || !p.in) continue;
         if (!once && rot) pos = a.position[r0 + i];
@@ -329,7 +369,7 @@ __global__ void __launch_bounds__(ROWS * 8, 3) k_append8(const Append8Args a, co
         const int64_t blk = r.slot / S;
         const int64_t at = blk * a.c.block_stride + (r.slot - blk * S) * a.c.token_stride + h0 * a.c.head_stride;
         for (int h = 0; h < nh; h += AHEAD) {
-            if (!once) load(r0 + i, h);
+            if (h > 0) load(r0 + i, h);
 #pragma unroll
             for (int n = 0; n < AHEAD; ++n) {
                 if (h + n >= nh) break;
@@ -338,11 +378,19 @@ __global__ void __launch_bounds__(ROWS * 8, 3) k_append8(const Append8Args a, co
                 const float inv = pow2(-scale[h + n][r.lead]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float lo[4] = {y[e][0] * inv, y[e][1] * inv, y[e][2] * inv, y[e][3] * inv};
-                    const float hi[4] = {y[e][4] * inv, y[e][5] * inv, y[e][6] * inv, y[e][7] * inv};
+                    uint32_t w[2];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const float z[4] = {y[e][4 * b], y[e][4 * b + 1], y[e][4 * b + 2], y[e][4 * b + 3]};
+                        if (special) {
+                            const float x[4] = {z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv};
+                            w[b] = f32_to_codes<CODE>(x);
+                        } else {
+                            w[b] = finite_to_codes<CODE>(z, inv);
+                        }
+                    }
                     const int64_t to = at + (h + n) * a.c.head_stride + p.e[e];
-                    if (store_ok(to + 7, codes_len, a.err))
-                        *reinterpret_cast<uint2 *>(codes + to) = make_uint2(f32_to_codes<CODE>(lo), f32_to_codes<CODE>(hi));
+                    if (store_ok(to + 7, codes_len, a.err)) *reinterpret_cast<uint2 *>(codes + to) = make_uint2(w[0], w[1]);
                 }
             }
         }
@@ -380,9 +428,9 @@ cudaError_t append_launch(const Append8Args &a, bool interleaved, int sm_count, 
     const int chunks = ctas_for(a.T, ROWS);
     // heads per CTA: fewer where there are few chunks
     const auto heads_for = [&](int64_t heads, int most) {
-        return static_cast<int>(std::min<int64_t>({std::max<int64_t>(1, chunks * heads / (6 * sm_count)), heads, most}));
+        return static_cast<int>(std::min<int64_t>({std::max<int64_t>(1 + heads / 8192, chunks * heads / (3 * sm_count)), heads, most}));
     };
-    g.gk = heads_for(2 * a.c.heads, std::min(a.c.heads, 4));
+    g.gk = heads_for(2 * a.c.heads, std::min(a.c.heads, MOST_HEADS));
     g.nk = ctas_for(a.c.heads, g.gk);
     g.gq = heads_for(a.Hq, 16);
     const dim3 grid(chunks, 2 * g.nk + ctas_for(a.Hq, g.gq));

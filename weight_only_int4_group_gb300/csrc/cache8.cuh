@@ -75,6 +75,32 @@ __device__ __forceinline__ uint32_t f32_to_codes(const float (&y)[4])
     return r;
 }
 
+// The same of finite numbers that lie within the codes once they are scaled.
+template <int CODE>
+__device__ __forceinline__ uint32_t finite_to_codes(const float (&y)[4], float inv)
+{
+    if (CODE == I8) {
+        uint32_t f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __float_as_uint(fmaf(y[i], inv, 12582912.0f));  // (scaling by a power of two is exact)
+        return __byte_perm(__byte_perm(f[0], f[1], 0x0040), __byte_perm(f[2], f[3], 0x0040), 0x5410);
+    }
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(y[0] * inv), "f"(y[1] * inv), "f"(y[2] * inv), "f"(y[3] * inv));
+    return r;
+}
+
+// The larger one, NaN if one is.
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
 // The least exponent of the range under which a largest magnitude fits the
 // codes: 127 = 1.984375 * 2^6, 448 = 1.75 * 2^8, and a mantissa above theirs
 // carries into the exponent.
