@@ -38,20 +38,25 @@ namespace q4 {
 namespace {
 
 constexpr int TK = 16;       // keys per unit
-constexpr int NW = 12;       // warps
-constexpr int THREADS = NW * 32;
+// Warps: 12 with 8 rows (48 requests of 1001..24576 keys, 64/8 heads of 128: 205
+// us; 8 warps 221, 16 204, but 32 of 101..8192 keys 57, 60 and 63), 8 with 16 (2
+// new tokens after 8000, 32 requests: 115; 12 warps spill: 131).
+template <int NT>
+constexpr int WARPS = NT == 1 ? 12 : 8;
+// (32 keys a unit at head sizes up to 64 gained nothing: 32 requests of 8000, 64/8
+// heads of 64, 62.6 us either way.)
 constexpr int PAD = 4, MIN_UNITS = 4;
 constexpr float LIFT = 7.0f, SLACK = 8.0f;
 constexpr int MERGE = 8, LEVELS = 4, MOST_CTAS = 256;
-static_assert(MERGE * MERGE * MERGE * MERGE >= NW * MOST_CTAS, "levels");
-static_assert(LEVELS * 2 * NW * MOST_CTAS * sizeof(unsigned int) <= ATTN_COUNTER_BYTES, "counters");
+static_assert(MERGE * MERGE * MERGE * MERGE >= WARPS<1> * MOST_CTAS, "levels");
+static_assert(LEVELS * 2 * WARPS<1> * MOST_CTAS * sizeof(unsigned int) <= ATTN_COUNTER_BYTES, "counters");
 
 template <int DP, int NT>
 struct Sizes {
-    static constexpr int STAGES = DP == 128 ? 4 : 6;   // units in flight per warp
+    static constexpr int STAGES = DP == 128 && NT == 1 ? 3 : 6;  // units in flight per warp
     static constexpr int TILE = TK * DP;               // bytes of a unit's keys
     static constexpr int RING = STAGES * 2 * TILE;
-    static constexpr int SMEM = NW * RING + NW * STAGES * 2 * 4;
+    static constexpr int SMEM = WARPS<NT> * (RING + STAGES * 2 * 4);
     static constexpr int SLOT = 128 * NT * (DP / 16 + 1);  // floats of a partial result
 };
 
@@ -107,6 +112,9 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi)
     }
 }
 
+// Adds n parts, the first at x and the others 2 * stride slots on each (a first
+// piece of an item lies in the odd slot of its worker), to the empty sums o, m,
+// l; AHEAD parts' loads are in flight.
 template <int NT, int NO>
 __device__ __forceinline__ void add_parts(const float4 *x, int stride, int n, bool odd, int slot, float (&o)[NT][NO][4],
                                           float (&m)[NT][2], float (&l)[NT][2])
@@ -153,11 +161,11 @@ __device__ __forceinline__ void add_parts(const float4 *x, int stride, int n, bo
 }
 
 template <int CODE, bool F16, int DP, int NT>
-__global__ void __launch_bounds__(THREADS, 1) k_attn8_stream(const AttnArgs a)
+__global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnArgs a)
 {
     using X = Exponents<CODE, F16>;
     using Z = Sizes<DP, NT>;
-    constexpr int R = 8 * NT, STAGES = Z::STAGES;
+    constexpr int R = 8 * NT, STAGES = Z::STAGES, NW = WARPS<NT>;
     constexpr int CH = DP / 16, RPI = 32 / CH, LPT = TK / RPI;  // 16-byte pieces of a key; keys per load; loads
     constexpr int KH = DP / 64;                                 // pieces of a key that a lane takes
     constexpr int NO = DP / 16;                                 // output m tiles
@@ -493,7 +501,7 @@ cudaError_t launch(const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
     auto kern = k_attn8_stream<CODE, F16, DP, NT>;
     const cudaError_t e = allow_smem(kern, Sizes<DP, NT>::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(p.grid), THREADS, Sizes<DP, NT>::SMEM, s, a);
+    return launch_dependent(kern, dim3(p.grid), WARPS<NT> * 32, Sizes<DP, NT>::SMEM, s, a);
 }
 
 template <int CODE, bool F16>
@@ -512,7 +520,7 @@ AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count)
     p.tc = max_fresh > 16 / GQ;
     p.tiles = max_fresh > 8 / GQ ? 2 : 1;
     const size_t slot = (D > 64 ? Sizes<128, 2>::SLOT : Sizes<64, 2>::SLOT) * sizeof(float) / 2 * p.tiles;
-    p.workspace = ATTN_COUNTER_BYTES + (p.tc ? attention_tc_part_bytes(D, p.grid) : 2 * static_cast<size_t>(p.grid) * NW * slot);
+    p.workspace = ATTN_COUNTER_BYTES + (p.tc ? attention_tc_part_bytes(D, p.grid) : 2 * static_cast<size_t>(p.grid) * (p.tiles == 1 ? WARPS<1> : WARPS<2>) * slot);
     return p;
 }
 
