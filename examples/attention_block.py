@@ -5,10 +5,12 @@ W4A16 o product.  A step takes any mix of prompt chunks and single decoded
 tokens; its plan (rows, slots, new blocks) is made on the GPU from the request
 lengths, once per step, and serves every layer.
 
-  python examples/attention_block.py [--steps 8]
+  python examples/attention_block.py [--steps 8] [--cache bf16|int8|e4m3]
 
 prefills four ragged prompts in one step, then decodes a token per request and
-step from a captured CUDA graph, and prints the time per decode step.
+step from a captured CUDA graph, and prints the time per decode step.  With
+--cache int8 or e4m3 keys and values lie in 8 bits: the append quantises them
+and the attention reads the codes; the rest of the program is the same.
 """
 from __future__ import annotations
 
@@ -50,7 +52,7 @@ class Server:
 
 class AttentionBlock:
     def __init__(self, hidden: int, heads: int, kv_heads: int, head_dim: int, max_fresh: int,
-                 blocks: int, block_size: int = 16, dtype=torch.bfloat16, seed: int = 0):
+                 blocks: int, block_size: int = 16, dtype=torch.bfloat16, seed: int = 0, code=None):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def weight(n, k):
@@ -59,9 +61,12 @@ class AttentionBlock:
         self.heads, self.max_fresh = heads, max_fresh
         self.qkv = weight((heads + 2 * kv_heads) * head_dim, hidden)
         self.o = weight(hidden, heads * head_dim)
-        self.cache = q4.KVCache.empty(blocks, kv_heads, block_size, head_dim, dtype)
+        if code is None:
+            self.cache = q4.KVCache.empty(blocks, kv_heads, block_size, head_dim, dtype)
+        else:
+            self.cache = q4.KVCache8.empty(blocks, kv_heads, block_size, head_dim, code, dtype)
         self.freq, self.factor = q4.rope_frequencies(head_dim)
-        self.ws = q4.attention_workspace(max_fresh, heads, kv_heads, head_dim)
+        self.ws = q4.attention_workspace(max_fresh, heads, kv_heads, head_dim, eight_bit=code is not None)
         self.products_ws: dict[int, torch.Tensor] = {}
 
     def _product(self, x: torch.Tensor, w: q4.QWeight) -> torch.Tensor:
@@ -84,10 +89,12 @@ class AttentionBlock:
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=8)
-    steps = ap.parse_args().steps
+    ap.add_argument("--cache", choices=["bf16", "int8", "e4m3"], default="bf16")
+    args = ap.parse_args()
+    steps, code = args.steps, {"bf16": None, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}[args.cache]
     hidden, prompts = 8192, [700, 33, 1, 256]
     server = Server(len(prompts), 512, 16, 256)
-    block = AttentionBlock(hidden, 64, 8, 128, max(prompts), 512)
+    block = AttentionBlock(hidden, 64, 8, 128, max(prompts), 512, code=code)
     x = torch.randn(sum(prompts), hidden, device="cuda").bfloat16()
     fresh = torch.tensor(prompts, dtype=torch.int32, device="cuda")
     y = block(x, server, server.plan(fresh, len(x)))

@@ -536,7 +536,7 @@ typedef struct {
  *            finite x (M = 127 or 448); the range's end where none is
  *     e    = need when o0 = 0, else max(need, the block's e)
  * The run's codes are x / 2^e to the nearest code (ties to even), beyond +-M the
- * end; NaN becomes 0.  Where e grows, the codes at offsets 0 .. o0 - 1 are
+ * end (so infinities too); NaN becomes 0.  Where e grows, the codes at offsets 0 .. o0 - 1 are
  * rounded again, c / 2^(growth) to the nearest: as e grows by whole powers of
  * two, all roundings of an int8 code together are off by less than one step of
  * the last scale, and e4m3 numbers change only where they become subnormal.
@@ -561,7 +561,7 @@ q4_status q4_rope_append8(const void *qkv, int64_t qkv_stride, int64_t T, int64_
  * INVALID_ARG for NULL pointers, sizes < 1, strides shorter than a row, a bad
  * cache; UNSUPPORTED for types and sizes beyond the limits of q4_attention;
  * MISALIGNED unless k_out and v_out are 16-byte aligned and strides multiples
- * of 8.
+ * of 8.  (More than 2^31 - 2^18 rows are UNSUPPORTED here and in the append.)
  */
 q4_status q4_cache_read8(const q4_kv_cache8 *cache, const int32_t *table, int64_t table_stride,
                          int64_t width, const int32_t *q_start, const int32_t *kv_len, int64_t B,
@@ -584,6 +584,15 @@ q4_status q4_attention8(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
                         int64_t max_fresh, float scale, int64_t window, void *o, q4_dtype ot,
                         int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes,
                         q4_stream_t stream);
+
+/* q4_attention_timeout_selftest over an 8-bit cache. */
+q4_status q4_attention8_timeout_selftest(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                                         const q4_kv_cache8 *cache, const int32_t *table,
+                                         int64_t table_stride, int64_t width, const int32_t *q_start,
+                                         const int32_t *kv_len, int64_t B, int64_t max_fresh,
+                                         float scale, int64_t window, void *o, q4_dtype ot,
+                                         int64_t o_stride, float *lse, void *workspace,
+                                         size_t workspace_bytes, q4_stream_t stream);
 
 /* Workspace bytes of q4_attention8, as q4_attention_workspace_bytes. */
 size_t q4_attention8_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads, int64_t head_dim);

@@ -280,6 +280,97 @@ def test_streams_and_graphs():
 
 
 @pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DT)
+def test_bounded_waits_report_a_timeout(dtype, code):
+    """A copy that never comes ends the kernel's waits, all roles leave, nothing is
+    written, and the context goes on."""
+    m = q4()
+    r = Requests8([(300, 150), (7, 20)], 8, 2, 128, 16, dtype, code, seed=14)
+    ws = m.attention_workspace(r.max_fresh, 8, 2, 128, eight_bit=True)
+    out = torch.full_like(r.q, 5.0)
+    m.attention_timeout_selftest(r.q, r.cache(), r.table, r.q_start, r.kv_len, r.max_fresh, out, ws)
+    assert m.check() == m.ERR_TIMEOUT
+    assert (out == 5.0).all()
+    ws.zero_()
+    check(r, ws=ws)
+    one = Requests8([(30, 1)], 8, 2, 128, 16, dtype, code, seed=15)
+    with pytest.raises(m.Q4Error):
+        m.attention_timeout_selftest(one.q, one.cache(), one.table, one.q_start, one.kv_len, 1, torch.empty_like(one.q), ws)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DT)
+def test_every_code_and_exponent(dtype, code):
+    """All 254 or 255 codes, subnormal e4m3 among them, under every exponent of
+    the range, come to the output exactly: one visible key per request."""
+    from cache8_ref import RANGE
+    lo, hi = RANGE[code, dtype]
+    for D, n in ((64, 1), (128, 40)):
+        es = list(range(lo, hi + 1))
+        r = Requests8([(0, n)] * len(es), 8, 1, D, 16, dtype, code, seed=3)
+        codes = torch.arange(256, device="cuda").to(torch.uint8)
+        if code == torch.int8:
+            codes = codes[codes != 0x80]
+        else:
+            codes = codes[(codes & 0x7F) != 0x7F]
+        raw(r.k).zero_()
+        for b, e in enumerate(es):
+            # every token of the request holds the same value row
+            for j in range(-(-n // 16)):
+                blk = r.table[b, j].item()
+                r.v_exp[blk] = 127 + e
+                raw(r.v)[blk, 0] = codes[(torch.arange(D, device="cuda") + b * D) % len(codes)]
+        o, _ = run(r, out_dtype=torch.float32)
+        vals = r.values()[1]
+        for b in range(len(es)):
+            want = vals[r.table[b, 0].item(), 0, 0]
+            got = o[r.start[b]:r.start[b + 1]].double()
+            # equal weights sum to 1 within 2^-22 (a sum of at most 40 of them in f32)
+            assert ((got - want).abs() <= want.abs() * 2.0 ** -20).all(), (es[b], n)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its workspace, and an append beside them."""
+    m = q4()
+    rs = [Requests8(ls, 8, 2, 128, 16, torch.bfloat16, c, seed=i) for i, (ls, c) in
+          enumerate([([(9000, 1), (40, 1)], CODES[0]), ([(3000, 120)], CODES[1])])]
+    want = [run(r)[0] for r in rs]
+    streams = [torch.cuda.Stream() for _ in rs]
+    spaces = [m.attention_workspace(r.max_fresh, 8, 2, 128, eight_bit=True) for r in rs]
+    caches = [r.cache() for r in rs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        outs = [m.attention(r.q, c, r.table, r.q_start, r.kv_len, r.max_fresh, ws=w, stream=s)
+                for r, c, w, s in zip(rs, caches, spaces, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want)) and m.check() == m.OK
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_attention_block_example(code):
+    """The example's block with an 8-bit cache: decoding token by token is near the
+    same block over 16 bits (its codes are within 2^-4 of each value, or a step)."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    from attention_block import AttentionBlock, Server
+    outs = []
+    for c in (None, code):
+        server = Server(2, 20, 16, 8)
+        block = AttentionBlock(256, 4, 2, 64, 40, 20, dtype=torch.float16, code=c)
+        g = torch.Generator(device="cuda").manual_seed(1)
+        for fresh in ([30, 5], [1, 1], [1, 0], [3, 1]):
+            x = torch.randn(sum(fresh), 256, generator=g, device="cuda").half()
+            y = block(x, server, server.plan(torch.tensor(fresh, dtype=torch.int32, device="cuda"), len(x)))
+        outs.append(y.float())
+    assert q4().check() == q4().OK and torch.isfinite(outs[1]).all()
+    # values are off by 2^-4 of themselves at most (e4m3; int8 in blocks of normal
+    # numbers less), weights by factors of as little on scores near 1
+    rel = float((outs[0] - outs[1]).norm() / outs[0].norm())
+    assert rel < 2.0 ** -3, rel
+
+
+@pytest.mark.parametrize("code", CODES)
 def test_a_layer_in_8_bits(code):
     """Plan, quantising append, attention and read-back together, as a server
     runs them: a prompt step, then decode steps in a graph."""

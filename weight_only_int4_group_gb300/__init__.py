@@ -109,6 +109,7 @@ def _load():
     lib.q4_rope_append8.argtypes = [P, I, I, I, I, S, P, F, P, P, P, I, C8, P]
     lib.q4_cache_read8.argtypes = [C8, P, I, I, P, P, I, I, P, I, P, I, S, P]
     lib.q4_attention8.argtypes = [P, I, I, I, C8, P, I, I, P, P, I, I, F, I, P, S, I, P, P, Z, P]
+    lib.q4_attention8_timeout_selftest.argtypes = lib.q4_attention8.argtypes
     lib.q4_attention8_workspace_bytes.argtypes = [I, I, I, I]
     lib.q4_attention8_workspace_bytes.restype = Z
     lib.q4_check.argtypes = [P]
@@ -121,6 +122,7 @@ def _load():
               "q4_gemm", "q4_gemm_timeout_selftest", "q4_gemv_noalloc", "q4_check",
               "q4_cache_plan", "q4_rope_append", "q4_attention",
               "q4_attention_timeout_selftest", "q4_rope_append8", "q4_cache_read8", "q4_attention8",
+              "q4_attention8_timeout_selftest",
               "q4_debug_bounds_selftest"):
         getattr(lib, f).restype = S
     return lib
@@ -399,6 +401,7 @@ class KVCache:
 
     _append, _append_name = _lib.q4_rope_append, "q4_rope_append"
     _attend, _attend_name, _eight_bit = _lib.q4_attention, "q4_attention", False
+    _attend_selftest = _lib.q4_attention_timeout_selftest
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         for t, n in ((k, "k"), (v, "v")):
@@ -434,6 +437,7 @@ class KVCache8:
 
     _append, _append_name = _lib.q4_rope_append8, "q4_rope_append8"
     _attend, _attend_name, _eight_bit = _lib.q4_attention8, "q4_attention8", True
+    _attend_selftest = _lib.q4_attention8_timeout_selftest
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor,
                  dtype=torch.bfloat16):
@@ -627,19 +631,23 @@ def cache_read(cache: KVCache8, table: torch.Tensor, q_start: torch.Tensor, kv_l
     [heads][head_dim] each, of the cache's dtype or float32.  Rows q_start[b] ..
     q_start[b + 1] are request b's last tokens of the kv_len[b] it holds, in
     order: all of them where q_start is the running sum of kv_len."""
-    if not isinstance(cache, KVCache8):
+    if type(cache) is not KVCache8:
         raise TypeError("cache must be a KVCache8: a 16-bit cache holds its values as they are")
     dev = _current_device()
     if cache._on != dev:
         _elsewhere("cache", cache._on, dev)
     B = kv_len.numel()
     tp, ts, width = _table(table, B, dev)
+    row = cache.heads * cache.head_dim
     if out is None:
-        shape = (T, cache.heads, cache.head_dim)
-        out = tuple(_empty(shape, out_dtype or cache.dtype, table.device, stream) for _ in "kv")
-    (kp, Tk, nk, ks), (vp, Tv, nv, vs) = (_rows(t, "out", out[0].dtype, dev) for t in out)
-    if Tk != T or Tv != T or nk != cache.heads * cache.head_dim or nv != nk:
-        raise ValueError("out must be two tensors of T rows of heads * head_dim")
+        shape, dtype = (T, cache.heads, cache.head_dim), out_dtype or cache.dtype
+        out = _empty(shape, dtype, table.device, stream), _empty(shape, dtype, table.device, stream)
+        kp, vp, ks, vs = out[0].data_ptr(), out[1].data_ptr(), row, row
+    else:
+        kp, Tk, nk, ks = _rows(out[0], "out", out[0].dtype, dev)
+        vp, Tv, nv, vs = _rows(out[1], "out", out[0].dtype, dev)
+        if Tk != T or Tv != T or nk != row or nv != row:
+            raise ValueError("out must be two tensors of T rows of heads * head_dim")
     _ok(_lib.q4_cache_read8(cache._ref, tp, ts, width, _array(q_start, "q_start", torch.int32, dev, B + 1),
                             _array(kv_len, "kv_len", torch.int32, dev, B), B, T, kp, ks, vp, vs,
                             _DTYPE.get(out[0].dtype, -1), _raw_stream(stream, dev)), "q4_cache_read8")
@@ -699,11 +707,11 @@ def attention(q: torch.Tensor, cache: KVCache | KVCache8, table: torch.Tensor, q
     return (out, lse) if lse is not None else out
 
 
-def attention_timeout_selftest(q: torch.Tensor, cache: KVCache, table: torch.Tensor, q_start: torch.Tensor,
+def attention_timeout_selftest(q: torch.Tensor, cache: KVCache | KVCache8, table: torch.Tensor, q_start: torch.Tensor,
                                kv_len: torch.Tensor, max_fresh: int, out: torch.Tensor, ws: torch.Tensor,
                                stream=None) -> None:
     attention(q, cache, table, q_start, kv_len, max_fresh, out=out, ws=ws, stream=stream,
-              _call=_lib.q4_attention_timeout_selftest)
+              _call=cache._attend_selftest)
 
 
 def check(stream=None) -> int:

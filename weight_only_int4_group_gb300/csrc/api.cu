@@ -738,6 +738,19 @@ q4_status q4_attention8(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
                             stream, 0, 2000000000ull);
 }
 
+q4_status q4_attention8_timeout_selftest(const void *q, int64_t q_stride, int64_t T, int64_t Hq,
+                                         const q4_kv_cache8 *cache, const int32_t *table,
+                                         int64_t table_stride, int64_t width, const int32_t *q_start,
+                                         const int32_t *kv_len, int64_t B, int64_t max_fresh,
+                                         float scale, int64_t window, void *o, q4_dtype ot,
+                                         int64_t o_stride, float *lse, void *workspace,
+                                         size_t workspace_bytes, q4_stream_t stream)
+{
+    return attention_common(q, q_stride, T, Hq, cache, table, table_stride, width, q_start, kv_len, B,
+                            max_fresh, scale, window, o, ot, o_stride, lse, workspace, workspace_bytes,
+                            stream, 1, 20000000ull);
+}
+
 size_t q4_attention8_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads, int64_t head_dim)
 {
     if (!attention_sizes_ok(max_fresh, Hq, heads, head_dim) || head_dim % 16) return 0;
