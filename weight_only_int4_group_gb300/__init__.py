@@ -615,9 +615,11 @@ def rope_append(qkv: torch.Tensor, cache: KVCache | KVCache8, position: torch.Te
         raise ValueError(f"qkv rows have {n} elements, not (heads + 2 * cache heads) * head_dim")
     if out is None:
         out = _empty((T, heads, cache.head_dim), cache.dtype, qkv.device, stream)
-    op, To, no, ostride = _rows(out, "out", cache.dtype, dev)
-    if To != T or no != heads * cache.head_dim:
-        raise ValueError("out must be T rows of heads * head_dim")
+        op, ostride = out.data_ptr(), heads * cache.head_dim
+    else:
+        op, To, no, ostride = _rows(out, "out", cache.dtype, dev)
+        if To != T or no != heads * cache.head_dim:
+            raise ValueError("out must be T rows of heads * head_dim")
     _ok(cache._append(qp, stride, T, heads, 2 * freq.numel(), ROPE_INTERLEAVED if interleaved else ROPE_HALF,
                       _array(freq, "freq", torch.float64, dev), factor, _array(position, "position", torch.int32, dev, T),
                       _array(slot, "slot", torch.int64, dev, T), op, ostride, cache._ref,
@@ -691,9 +693,11 @@ def attention(q: torch.Tensor, cache: KVCache | KVCache8, table: torch.Tensor, q
     tp, ts, width = _table(table, B, dev)
     if out is None:
         out = _empty((T, heads, D), out_dtype or cache.dtype, q.device, stream)
-    op, To, no, ostride = _rows(out, "out", out.dtype, dev)
-    if To != T or no != n:
-        raise ValueError("out must be T rows of heads * head_dim")
+        op, ostride = out.data_ptr(), n
+    else:
+        op, To, no, ostride = _rows(out, "out", out.dtype, dev)
+        if To != T or no != n:
+            raise ValueError("out must be T rows of heads * head_dim")
     if return_lse and lse is None:
         lse = _empty((T, heads), torch.float32, q.device, stream)
     if ws is None:

@@ -31,6 +31,13 @@
 // Work.  As in the 16-bit kernel (attention.cu): all units of the call form one
 // sequence cut into an equal range per warp; a ring of units per warp filled by
 // cp.async; split items meet in a tree, in sequence order.
+//
+// Measured (64 query / 8 KV heads of 128, bf16, graph): 48 requests of 1001..24576
+// keys, int8, 206 us, 6.1 TB/s (0.90 of the measured copy bandwidth; over 16 bits
+// 384 us); 32 of 101..8192 keys, e4m3, 57 us (0.70; 96 us over 16 bits); 32 of
+// 8001 96 us int8, 91 e4m3, 63 with heads of 64; one of 65536 39 us; one of 777
+// keys (32 heads) 13.7 us, which is latency.  DRAM reads are 1.004 of the codes;
+// the arithmetic pipe of the bytes' permutations is 46% busy.
 #include "attention.cuh"
 #include "cache8.cuh"
 

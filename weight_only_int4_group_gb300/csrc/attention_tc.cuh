@@ -25,6 +25,12 @@
 //                   make scores that are masked), and queries whose group of
 //                   heads does not divide 128;
 //   warp 11         allocates tensor memory; one thread issues the MMAs.
+// Over an 8-bit cache there are four warps more, and keys and values come as
+// codes, with the exponents of their blocks, which the producers ask for a unit
+// ahead:
+//   warps 12-15     widen them to the queries' type, times 2^e: exact, so that
+//                   all else is as over 16 bits.  Codes land in the slot that
+//                   they are widened in.
 // Tensor memory (512 columns): the two subtiles' scores (128 columns each)
 // and outputs (head_dim each).  While one subtile's softmax runs, the other's
 // products do: the issue order is P0 V(j), Q0 K(j+1), P1 V(j), Q1 K(j+1), on
@@ -59,6 +65,22 @@
 // which come one after the other with its MMAs, as those queue only a few deep.
 // The CTA's range stays in shared memory: held in registers it made the softmax
 // warps spill (188 us against 186).
+//
+// 8-bit caches (same shapes): 512 new tokens after 16384 in 241 us (int8), 234
+// (e4m3), 229 and 220 with f16; the prompt of 4096 in 138 (e4m3), the 12 mixed
+// requests in 104.  The widening binds: without it the kernel takes 177 us on the
+// first, with its loads and stores but no arithmetic 187 (timing-only copies).
+// Its four warps take some 1000 cycles a tile, and a slot's turn (copies 1700
+// cycles, widening, products) is as long as two units.  Measured and not kept:
+// - codes widened to binary16 whatever the type, unscaled, with all groups'
+//   scales in the softmax: 239 and 224, the prompt 147; with groups brought to
+//   their tile's or piece's scale: 232 to 262, the prompt 166 to 171 (masked
+//   tiles take longer);
+// - two warps each for keys and values: 227 to 237, the prompt 148;
+// - codes landing apart from the slots, in the output staging's place: 242 to
+//   263;
+// - a pass ahead that widens long prompts' keys and values into the workspace,
+//   128 MB: 225 and 219, but 224, 222 with f16 and 148 for the prompt.
 #pragma once
 
 #include <type_traits>

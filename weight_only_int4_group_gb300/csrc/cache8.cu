@@ -19,6 +19,13 @@ namespace q4 {
 // angles serve all its heads.  Fractions of a turn are 64-bit integers
 // (position * frequency mod 1 in units of 2^-64): this card's f64 units would
 // take longer than the copy.
+//
+// Measured (graph): 8192 rows of 64 + 2 * 8 heads of 128 in 68 us, 4.7 TB/s (0.69 of
+// the measured copy bandwidth: the CTAs' beginnings and the second look are waits
+// that four CTAs per SM do not hide; three with twice the loads in flight took 74);
+// 1001 rows of 32 + 2 * 32 heads 20 us; 512 decoding requests 7 us, 4 of them 4.9,
+// which is latency.  A loop of two looks per head, which reads each row once,
+// waits at two barriers per head: 91 and 46 us.
 namespace {
 
 constexpr int ROWS = 32;         // of a chunk
@@ -426,7 +433,9 @@ cudaError_t append_launch(const Append8Args &a, bool interleaved, int sm_count, 
     AppendGrid g{};
     g.lanes_log = a.c.D > 64 ? 3 : 2;
     const int chunks = ctas_for(a.T, ROWS);
-    // heads per CTA: fewer where there are few chunks
+    // Heads per CTA: as many as leave about three CTAs of a kind per SM (8192 rows,
+    // 64/8 heads: 68.5 us; six 67.2, but 1001 rows of 32/32 heads 20.4 and 22, 2048
+    // of 64/8 19.6 and 23; twelve 73, 31 and 25).
     const auto heads_for = [&](int64_t heads, int most) {
         return static_cast<int>(std::min<int64_t>({std::max<int64_t>(1 + heads / 8192, chunks * heads / (3 * sm_count)), heads, most}));
     };
@@ -443,7 +452,9 @@ cudaError_t append_launch(const Append8Args &a, bool interleaved, int sm_count, 
 // -------------------------------------------------------------- reading back
 // Memory-bound: a byte in, two (or four) out.  A CTA takes up to 32 token rows,
 // finds their requests (one warp), and each thread widens 16 codes at a time,
-// four such pieces in flight.
+// four such pieces in flight.  Measured: 24 requests of 900..8100 tokens, 8 heads
+// of 128, in 110 us, 0.89 of the measured copy bandwidth; 777 tokens of 32 heads
+// in 8.9 us.
 constexpr int READ_ROWS = 32, READ_THREADS = 256, READ_AHEAD = 4;
 
 struct ReadGrid {
