@@ -298,6 +298,23 @@ def test_bounded_waits_report_a_timeout(dtype, code):
         m.attention_timeout_selftest(one.q, one.cache(), one.table, one.q_start, one.kv_len, 1, torch.empty_like(one.q), ws)
 
 
+@pytest.mark.parametrize("n", [1, 2, 40])
+@pytest.mark.parametrize("code", CODES)
+def test_large_queries_against_empty_codes(n, code):
+    """Queries of 2^127 and keys that are all 0 under the largest scale: all
+    scores are 0 and each visible key has the same weight.  (n rows: all kernels.)"""
+    from cache8_ref import RANGE
+    for scale in (None, -0.125):
+        r = Requests8([(100, n)], 8, 1, 128, 16, torch.bfloat16, code, seed=4)
+        raw(r.k).zero_()
+        r.k_exp.fill_(127 + RANGE[code, torch.bfloat16][1])
+        r.q.fill_(2.0 ** 127)
+        o, lse = check(r, scale=scale)
+        # the sum of up to 140 equal weights, f32
+        want = torch.log(torch.arange(101, 101 + n, device="cuda", dtype=torch.float64))
+        assert ((lse.double() - want[:, None]).abs() <= 2.0 ** -18).all()
+
+
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("dtype", DT)
 def test_every_code_and_exponent(dtype, code):

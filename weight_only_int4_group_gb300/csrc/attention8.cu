@@ -35,7 +35,7 @@
 // Measured (64 query / 8 KV heads of 128, bf16, graph): 48 requests of 1001..24576
 // keys, int8, 206 us, 6.1 TB/s (0.90 of the measured copy bandwidth; over 16 bits
 // 384 us); 32 of 101..8192 keys, e4m3, 57 us (0.70; 96 us over 16 bits); 32 of
-// 8001 96 us int8, 91 e4m3, 63 with heads of 64; one of 65536 39 us; one of 777
+// 8001 95 us int8, 90 e4m3, 64 with heads of 64; one of 65536 39 us; one of 777
 // keys (32 heads) 13.7 us, which is latency.  DRAM reads are 1.004 of the codes;
 // the arithmetic pipe of the bytes' permutations is 46% busy.
 #include "attention.cuh"
@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                 peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
                 ex = peak ? min(max(static_cast<int>(peak >> 7) - 127 - 14, -126), 126) : 0;
                 const float f = pow2(-ex);
+                if (peak >= 0x7F80u) ex = 0;  // scores of a row that is not finite are not either, whatever their factor
 #pragma unroll
                 for (int i = 0; i < KH * 4; ++i)
 #pragma unroll
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                     const int j = e & 1, key = key0 + lg + (e >> 1) * 8;
                     float x = fmaf(sc[t][e], cr[t][j] * fk, fv);
                     if (part && !(key <= place[t][j] && (a.window == 0 || key > place[t][j] - a.window))) x = -INFINITY;
-                    past |= x > m[t][j] + SLACK;
+                    past |= !(x <= m[t][j] + SLACK);
                     sc[t][e] = x;
                 }
             if (__any_sync(0xffffffffu, past)) {
@@ -349,6 +350,11 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                     float f[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
+                        // NaN of a factor past f32 (2^113 of the queries times 2^48) and a score of 0
+                        if (!F16 && isinf(cr[t][j] * fk)) {
+                            if (isnan(sc[t][j])) sc[t][j] = fv;
+                            if (isnan(sc[t][2 + j])) sc[t][2 + j] = fv;
+                        }
                         float mx = fmaxf(sc[t][j], sc[t][2 + j]);
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
