@@ -200,6 +200,33 @@ def test_in_place_queries(inter):
         assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
 
 
+@pytest.mark.parametrize("D,rot", [(80, 40), (96, 2), (128, 120), (64, 0)])
+def test_in_place_queries_whose_pairs_lie_apart(D, rot):
+    """The same where a pair's elements belong to different threads' pieces."""
+    m = q4()
+    g = torch.Generator().manual_seed(8)
+    T, heads = 70, 20
+    slot, pos = slots_of([(0, T)], 16, -(-T // 16))
+    freq = (10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))).cuda()
+    qkv = torch.randn(T, (heads + 2) * D, generator=g).half().cuda()
+    caches = [m.KVCache8.empty(-(-T // 16), 1, 16, D, dtype=torch.float16) for _ in range(2)]
+    want = m.rope_append(qkv, caches[0], pos, slot, freq, heads)
+    rows = qkv[:, :heads * D]
+    m.rope_append(qkv, caches[1], pos, slot, freq, heads, out=rows)
+    assert torch.equal(rows.reshape(T, heads, D), want)
+    for n in ("k_exp", "v_exp"):
+        assert torch.equal(getattr(caches[0], n), getattr(caches[1], n))
+    live = slot.cpu()
+    for x, y in ((caches[0].k, caches[1].k), (caches[0].v, caches[1].v)):
+        assert torch.equal(x.transpose(1, 2).reshape(-1, D).cpu()[live], y.transpose(1, 2).reshape(-1, D).cpu()[live])
+
+
+def test_many_heads():
+    """More heads than one CTA's share of each kind, several times over."""
+    append([(5, 2)], 20000, 600, 16, 16, torch.bfloat16, torch.int8, seed=9)
+    append([(0, 1), (17, 1)], 3, 300, 128, 16, torch.float16, torch.float8_e4m3fn, seed=10)
+
+
 def test_queries_agree_with_the_16_bit_append():
     m = q4()
     g = torch.Generator().manual_seed(6)
@@ -354,3 +381,48 @@ def test_repeated_append_is_the_same():
     two = clones(cache)
     for (a, b), (c, d) in zip(one, two):
         assert torch.equal(raw(a), raw(c)) and torch.equal(b, d)
+
+
+@pytest.mark.parametrize("far", ["blocks", "heads", "tokens"])
+def test_offsets_past_32_bits(far):
+    """A cache whose codes lie more than 2^32 apart gives what a dense one gives:
+    append, reading back, attention with few and with many rows."""
+    m = q4()
+    blocks, heads, S, D = 6, 2, 16, 64
+    shape = (blocks, heads, S, D)
+    dense = [1024 * heads, 1024, D]
+    stride = list(dense)
+    i = ("blocks", "heads", "tokens").index(far)
+    n = shape[i]
+    stride[i] = -(-(2 ** 32 + 2 ** 20) // (n - 1) // 16) * 16
+    if far == "heads":
+        stride[0] = 1024
+    if far == "tokens":
+        stride[0], stride[1] = heads * D, D
+    size = sum((a - 1) * b for a, b in zip(shape, stride)) + D
+    assert size > 2 ** 32
+    big = []
+    for _ in "kv":
+        big.append(torch.zeros(size, dtype=torch.int8, device="cuda").as_strided(shape, stride + [1]))
+    exps = [torch.zeros(blocks, heads, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    wide = m.KVCache8(*big, *exps[:2])
+    near = m.KVCache8(*(torch.zeros(shape, dtype=torch.int8, device="cuda") for _ in "kv"), *exps[2:])
+    g = torch.Generator().manual_seed(12)
+    T = blocks * S - 3
+    table = torch.tensor([[4, 1, 5, 0, 3, 2]], dtype=torch.int32, device="cuda")
+    place = torch.arange(T, device="cuda")
+    slot = table[0].long()[place // S] * S + place % S
+    freq, _ = m.rope_frequencies(D)
+    qkv = torch.randn(T, (6 + 2 * heads) * D, generator=g).bfloat16().cuda()
+    q = [m.rope_append(qkv, c, place.int(), slot, freq, 6) for c in (wide, near)]
+    assert torch.equal(*q)
+    assert torch.equal(wide.k, near.k) and torch.equal(wide.v, near.v)
+    assert torch.equal(exps[0], exps[2]) and torch.equal(exps[1], exps[3])
+    kv = torch.tensor([T], dtype=torch.int32, device="cuda")
+    for rows in (1, 4, T):
+        start = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        a, b = (m.cache_read(c, table, start, kv, rows) for c in (wide, near))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        a, b = (m.attention(q[0][T - rows:], c, table, start, kv, rows) for c in (wide, near))
+        assert torch.equal(a, b) and a.isfinite().all()
+    assert m.check() == m.OK
