@@ -298,6 +298,50 @@ def test_bounded_waits_report_a_timeout(dtype, code):
         m.attention_timeout_selftest(one.q, one.cache(), one.table, one.q_start, one.kv_len, 1, torch.empty_like(one.q), ws)
 
 
+MIDDLE = [  # heads, KV heads, dims, lengths: 17 to 32 rows per KV head
+    (16, 2, 128, [(i * 37 % 500, 1 + i % 4) for i in range(40)]),
+    (16, 2, 128, [(i * 53 % 90, 3 + i % 2) for i in range(31)]),
+    (20, 1, 64, [(i * 61 % 700, 1) for i in range(70)]),
+    (32, 1, 128, [(i * 61 % 700, i % 2) for i in range(70)]),
+    (4, 4, 96, [(i * 29 % 300, 1 + i * 7 % 32) for i in range(20)]),
+    (64, 8, 128, [(5000 + 3 * i, 4) for i in range(8)]),
+    (24, 8, 48, [(40000, 9)] + [(0, 0)] * 6 + [(3, 9)]),
+]
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("case", MIDDLE, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{len(c[3])}")
+def test_up_to_32_rows(case, dtype, code):
+    """Both kernels' side of the requests times heads that choose between them, with
+    one workspace, and with windows."""
+    heads, kv, D, lengths = case
+    ws = q4().attention_workspace(max(n for _, n in lengths), heads, kv, D, eight_bit=True)
+    for part in (lengths, lengths[:3]):
+        r = Requests8(part, heads, kv, D, 32, dtype, code, seed=len(part))
+        for window in (0, 19):
+            check(r, window, ws=ws, max_fresh=max(n for _, n in lengths))
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_up_to_32_rows_repeat_and_use_every_scale(code):
+    """The same bits at each call, splits over many warps; keys and values of all
+    the scales of bf16; queries past 2^80 against zero codes."""
+    r = Requests8([(3000, 4)] * 8, 64, 8, 128, 16, torch.bfloat16, code, seed=5)
+    ws = q4().attention_workspace(4, 64, 8, 128, eight_bit=True)
+    a, la = run(r, ws=ws)
+    for _ in range(5):
+        b, lb = run(r, ws=ws)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    r = Requests8([(200, 4)] * 64, 8, 1, 128, 16, torch.bfloat16, code, seed=6, exps=(-30, 20))
+    r.k_exp.copy_(torch.randint(127 - 10, 127 - 3, r.k_exp.shape, device="cuda"))
+    check(r)
+    raw(r.k).zero_()
+    r.k_exp.fill_(127 + 48)
+    r.q.fill_(2.0 ** 127)
+    check(r)
+
+
 @pytest.mark.parametrize("n", [1, 2, 40])
 @pytest.mark.parametrize("code", CODES)
 def test_large_queries_against_empty_codes(n, code):

@@ -608,13 +608,13 @@ size_t q4_attention_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t heads
 }  // extern "C"
 
 // What differs between the caches.
-static AttnPlan plan_for(const q4_kv_cache *c, int64_t max_fresh, int64_t Hq, int sm_count)
+static AttnPlan plan_for(const q4_kv_cache *c, int64_t max_fresh, int64_t Hq, int64_t, int sm_count)
 {
     return attention_plan(max_fresh, Hq / c->heads, c->head_dim, sm_count);
 }
-static AttnPlan plan_for(const q4_kv_cache8 *c, int64_t max_fresh, int64_t Hq, int sm_count)
+static AttnPlan plan_for(const q4_kv_cache8 *c, int64_t max_fresh, int64_t Hq, int64_t B, int sm_count)
 {
-    return attention8_plan(max_fresh, Hq / c->heads, c->head_dim, sm_count);
+    return attention8_plan(max_fresh, Hq / c->heads, c->head_dim, B * c->heads, sm_count);
 }
 static cudaError_t launch_for(const q4_kv_cache *c, const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 {
@@ -655,7 +655,7 @@ static q4_status attention_common(const void *q, int64_t q_stride, int64_t T, in
         return Q4_ERR_MISALIGNED;
     const DevInfo *d = dev_info();
     if (!d) return cuda_fail(cudaGetLastError());
-    const AttnPlan plan = plan_for(cache, max_fresh, Hq, d->sm_count);
+    const AttnPlan plan = plan_for(cache, max_fresh, Hq, B, d->sm_count);
     if (debug_no_copy && !plan.tc) return Q4_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < plan.workspace) return Q4_ERR_INVALID_ARG;
     AttnArgs a{};
@@ -756,7 +756,7 @@ size_t q4_attention8_workspace_bytes(int64_t max_fresh, int64_t Hq, int64_t head
     if (!attention_sizes_ok(max_fresh, Hq, heads, head_dim) || head_dim % 16) return 0;
     const DevInfo *d = dev_info();
     if (!d) return 0;
-    return attention8_plan(max_fresh, Hq / heads, head_dim, d->sm_count).workspace;
+    return attention8_plan(max_fresh, Hq / heads, head_dim, 0, d->sm_count).workspace;
 }
 
 q4_status q4_check(q4_stream_t stream)

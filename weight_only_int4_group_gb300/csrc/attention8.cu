@@ -2,7 +2,7 @@
 // head: the decode kernel.
 //
 // Rows.  The n new tokens of a request and the GQ query heads that share a KV
-// head form n * GQ rows that read the same keys, in row tiles of 8 or 16.  Bound:
+// head form n * GQ rows that read the same keys, in row tiles of 8, 16 or 32.  Bound:
 // with one tile the codes are read once; HBM bounds the call as long as a
 // byte's work, twice what a byte of a 16-bit cache brings, fits beside its load.
 //
@@ -33,11 +33,14 @@
 // cp.async; split items meet in a tree, in sequence order.
 //
 // Measured (64 query / 8 KV heads of 128, bf16, graph): 48 requests of 1001..24576
-// keys, int8, 206 us, 6.1 TB/s (0.90 of the measured copy bandwidth; over 16 bits
+// keys, int8, 198 us, 6.4 TB/s (0.94 of the measured copy bandwidth; over 16 bits
 // 384 us); 32 of 101..8192 keys, e4m3, 57 us (0.70; 96 us over 16 bits); 32 of
-// 8001 95 us int8, 90 e4m3, 64 with heads of 64; one of 65536 39 us; one of 777
+// 8001 94 us int8, 91 e4m3, 61 with heads of 64; one of 65536 39 us; one of 777
 // keys (32 heads) 13.7 us, which is latency.  DRAM reads are 1.004 of the codes;
 // the arithmetic pipe of the bytes' permutations is 46% busy.
+// Rows cost: 32 requests of 8000, int8, with 2 new tokens (16 rows) 112 us, with 4
+// (32) 165: four row tiles leave room for 8 warps, which issue 0.4 instructions per
+// cycle and scheduler (dependent ones), and mma.sync is half busy.
 #include "attention.cuh"
 #include "cache8.cuh"
 
@@ -47,9 +50,11 @@ namespace {
 constexpr int TK = 16;       // keys per unit
 // Warps: 12 with 8 rows (48 requests of 1001..24576 keys, 64/8 heads of 128: 205
 // us; 8 warps 221, 16 204, but 32 of 101..8192 keys 57, 60 and 63), 8 with 16 (2
-// new tokens after 8000, 32 requests: 115; 12 warps spill: 131).
+// new tokens after 8000, 32 requests: 115; 12 warps spill: 131, or with the queries
+// in shared memory 119) and 32.
 template <int NT>
 constexpr int WARPS = NT == 1 ? 12 : 8;
+static_assert(WARPS<2> == WARPS<4>, "workspace");
 // (32 keys a unit at head sizes up to 64 gained nothing: 32 requests of 8000, 64/8
 // heads of 64, 62.6 us either way.)
 constexpr int PAD = 4, MIN_UNITS = 4;
@@ -60,10 +65,11 @@ static_assert(LEVELS * 2 * WARPS<1> * MOST_CTAS * sizeof(unsigned int) <= ATTN_C
 
 template <int DP, int NT>
 struct Sizes {
-    static constexpr int STAGES = DP == 128 && NT == 1 ? 3 : 6;  // units in flight per warp
+    static constexpr int STAGES = DP == 128 ? (NT == 1 ? 3 : NT == 2 ? 6 : 4) : 6;  // units in flight per warp
     static constexpr int TILE = TK * DP;               // bytes of a unit's keys
     static constexpr int RING = STAGES * 2 * TILE;
-    static constexpr int SMEM = WARPS<NT> * (RING + STAGES * 2 * 4);
+    static constexpr int QUERIES = NT == 4 ? NT * DP * 16 : 0;  // of a warp, where registers are too few
+    static constexpr int SMEM = WARPS<NT> * (RING + QUERIES + STAGES * 2 * 4);
     static constexpr int SLOT = 128 * NT * (DP / 16 + 1);  // floats of a partial result
 };
 
@@ -119,25 +125,31 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi)
     }
 }
 
-// Adds n parts, the first at x and the others 2 * stride slots on each (a first
-// piece of an item lies in the odd slot of its worker), to the empty sums o, m,
-// l; AHEAD parts' loads are in flight.
-template <int NT, int NO>
-__device__ __forceinline__ void add_parts(const float4 *x, int stride, int n, bool odd, int slot, float (&o)[NT][NO][4],
+// Adds NT row tiles of n parts, the first at x and the others 2 * stride slots on
+// each (a first piece of an item lies in the odd slot of its worker), to empty
+// sums; the tiles' references and sums lie ml on.  AHEAD parts' loads are in flight.
+template <int NT, int NO, int AHEAD>
+__device__ __forceinline__ void add_parts(const float4 *x, int ml, int stride, int n, bool odd, int slot, float (&o)[NT][NO][4],
                                           float (&m)[NT][2], float (&l)[NT][2])
 {
-    constexpr int AHEAD = NT == 1 ? 2 : 1;
     const float4 *even = x - (odd ? slot / 4 : 0);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        m[t][0] = m[t][1] = -INFINITY;
+        l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NO; ++k) o[t][k][0] = o[t][k][1] = o[t][k][2] = o[t][k][3] = 0.0f;
+    }
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += AHEAD) {
-        float4 y[AHEAD][NT][NO], ml[AHEAD][NT];
+        float4 y[AHEAD][NT][NO], r[AHEAD][NT];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const bool in = i0 + i < n;
             const float4 *p = i0 + i == 0 ? x : even + static_cast<int64_t>(i0 + i) * stride * (slot / 2);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                ml[i][t] = in ? __ldcg(p + (NT * NO + t) * 32) : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+                r[i][t] = in ? __ldcg(p + ml + t * 32) : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
 #pragma unroll
                 for (int k = 0; k < NO; ++k) y[i][t][k] = in ? __ldcg(p + (t * NO + k) * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
@@ -149,7 +161,7 @@ __device__ __forceinline__ void add_parts(const float4 *x, int stride, int n, bo
                 float g0[2], g1[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float mi = j ? ml[i][t].z : ml[i][t].x, li = j ? ml[i][t].w : ml[i][t].y;
+                    const float mi = j ? r[i][t].z : r[i][t].x, li = j ? r[i][t].w : r[i][t].y;
                     const float mn = fmaxf(m[t][j], mi), ref = mn == -INFINITY ? 0.0f : mn;
                     g0[j] = ex2(m[t][j] - ref);
                     g1[j] = ex2(mi - ref);
@@ -191,7 +203,8 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
     using Pieces = Walk<R, TK, PAD>;
     Pieces k(a, rng), ld = k;  // being summed; being loaded
     const uint32_t ring = smem_u32(smem) + warp * Z::RING;
-    int *const scales = reinterpret_cast<int *>(smem + NW * Z::RING) + warp * STAGES * 2;  // (ek, ev) per slot
+    int *const scales = reinterpret_cast<int *>(smem + NW * (Z::RING + Z::QUERIES)) + warp * STAGES * 2;  // (ek, ev) per slot
+    uint4 *const queries = reinterpret_cast<uint4 *>(smem + NW * Z::RING + warp * Z::QUERIES) + lane;  // [piece][tiles 2t, 2t + 1][lane]
     const uint8_t *const kb = reinterpret_cast<const uint8_t *>(a.k), *const vb = reinterpret_cast<const uint8_t *>(a.v);
     int ld_i = 0, ld_slot = 0;  // unit of ld, ring slot
     int exp_slot = -1;  // exponents on their way (lanes 0-15 keys', 16-31 values'):
@@ -285,15 +298,13 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) cr[t][j] = a.scale_log2 * pow2(__shfl_sync(0xffffffffu, ex, 4 * (2 * lt + j)));
-        }
-        int place[NT][2];  // the rows' places in the request (their last visible keys)
+            if (NT == 4) {  // (read by the same lane alone)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = k.row0 + 8 * t + 2 * lt + j;
-                place[t][j] = r < k.row1 ? k.base + a.by_GQ.div(r) : -1;
+                for (int i = 0; i < KH * 4; ++i)
+                    *reinterpret_cast<uint2 *>(reinterpret_cast<uint32_t *>(queries + (i * NT / 2 + t / 2) * 32) + 2 * (t & 1)) =
+                        make_uint2(qf[t][i][0], qf[t][i][1]);
             }
+        }
         const int lo_place = k.base + a.by_GQ.div(k.row0), hi_place = k.base + a.by_GQ.div(k.row1 - 1);
 
         float o[NT][NO][4], m[NT][2], l[NT][2];
@@ -325,6 +336,15 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                     uint32_t f[4];
                     widen<CODE>(xw[w], f[0], f[2]);
                     widen<CODE>(yw[w], f[1], f[3]);
+                    if (NT == 4) {
+#pragma unroll
+                        for (int t = 0; t < NT; t += 2) {
+                            const uint4 b = lds16(smem_u32(queries + ((h * 4 + w) * NT + t) / 2 * 32));
+                            mma16816(sc[t], f, b.x, b.y);
+                            mma16816(sc[(t + 1) % NT], f, b.z, b.w);
+                        }
+                        continue;
+                    }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) mma16816(sc[t], f, qf[t][h * 4 + w][0], qf[t][h * 4 + w][1]);
                 }
@@ -333,17 +353,28 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
             const int key0 = (k.kt0 + k.kt + i) * TK;
             const bool part = key0 + TK - 1 > lo_place || (a.window > 0 && key0 <= hi_place - a.window);
             const float fk = pow2(ek), fv = static_cast<float>(ev), undo = pow2(-ev);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[t][e] = fmaf(sc[t][e], cr[t][e & 1] * fk, fv);
+            if (part) {  // (a branch: as selects the unmasked units took 4% longer, with 32 rows 20%)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = k.row0 + 8 * t + 2 * lt + j, at = r < k.row1 ? k.base + a.by_GQ.div(r) : -1;
+#pragma unroll
+                        for (int e = j; e < 4; e += 2) {
+                            const int key = key0 + lg + (e >> 1) * 8;
+                            if (!(key <= at && (a.window == 0 || key > at - a.window))) sc[t][e] = -INFINITY;
+                        }
+                    }
+            }
             bool past = false;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = e & 1, key = key0 + lg + (e >> 1) * 8;
-                    float x = fmaf(sc[t][e], cr[t][j] * fk, fv);
-                    if (part && !(key <= place[t][j] && (a.window == 0 || key > place[t][j] - a.window))) x = -INFINITY;
-                    past |= !(x <= m[t][j] + SLACK);
-                    sc[t][e] = x;
-                }
+                for (int e = 0; e < 4; ++e) past |= !(sc[t][e] <= m[t][e & 1] + SLACK);
             if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
@@ -426,8 +457,32 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                 l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], 16);
             }
 
-        bool store = k.whole();
-        if (!store) {
+        // a row tile's outputs
+        auto store = [&](int t, const float (&o)[NO][4], const float (&m)[2], const float (&l)[2]) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = k.row0 + 8 * t + 2 * lt + j;
+                if (r >= k.row1) continue;
+                const int tok = a.by_GQ.div(r), h = k.it.head * a.GQ + r - tok * a.GQ;
+                const float inv = inverse(l[j]);
+                float y[2 * NO];
+#pragma unroll
+                for (int n = 0; n < NO; ++n) {
+                    y[2 * n] = o[n][j] * inv;
+                    y[2 * n + 1] = o[n][2 + j] * inv;
+                }
+                store_dims<F16, 2 * NO>(a, k.t0 + tok, h, lg * 2 * NO, y);
+                if (lg == 0) store_lse(a, k.t0 + tok, h, m[j] - LIFT, l[j]);
+            }
+        };
+        auto store_all = [&]() {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) store(t, o[t], m[t], l[t]);
+        };
+        const bool split = !k.whole();
+        bool whole = !split;  // the registers hold the item's sum
+        if (NT == 4 && whole) store_all();
+        if (split) {
             // as in the 16-bit kernel: the item's pieces are the leaves of a tree
             // of MERGE-fold nodes over the workers that hold them; whoever
             // completes a node adds its parts in order, leaves the sum in the
@@ -439,19 +494,23 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
             auto slot_of = [&](int w) {
                 return reinterpret_cast<float4 *>(a.part + (2 * static_cast<int64_t>(w) + (w == w0)) * Z::SLOT) + lane;
             };
+            auto keep = [&](float4 *ps, int t, const float (&o)[NO][4], const float (&m)[2], const float (&l)[2]) {
+                if (!store_ok(reinterpret_cast<float *>(ps - lane) + Z::SLOT - 1 - a.part, a.part_len, a.err)) return;
+#pragma unroll
+                for (int n = 0; n < NO; ++n) ps[(t * NO + n) * 32] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+                ps[(NT * NO + t) * 32] = make_float4(m[0], l[0], m[1], l[1]);
+            };
             int at = me;            // where this warp's sum goes
             int nodes = w1 - w0 + 1, idx = me - w0, stride = 1;  // of the level
             unsigned int *count = a.count;
-            for (;;) {
+            auto keep_all = [&]() {
                 float4 *ps = slot_of(at);
-                if (store_ok(reinterpret_cast<float *>(ps - lane) + Z::SLOT - 1 - a.part, a.part_len, a.err)) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                        for (int n = 0; n < NO; ++n) ps[(t * NO + n) * 32] = make_float4(o[t][n][0], o[t][n][1], o[t][n][2], o[t][n][3]);
-                        ps[(NT * NO + t) * 32] = make_float4(m[t][0], l[t][0], m[t][1], l[t][1]);
-                    }
-                }
+                for (int t = 0; t < NT; ++t) keep(ps, t, o[t], m[t], l[t]);
+            };
+            if (NT == 4) keep_all();
+            do {
+                if (NT < 4) keep_all();
                 __threadfence();
                 __syncwarp();
                 const int first = idx / MERGE * MERGE, n_parts = min(MERGE, nodes - first);
@@ -465,43 +524,30 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                 }
                 if (!__shfl_sync(0xffffffffu, last, 0)) break;
                 __syncwarp();  // lane 0's acquire holds for the other lanes' reads too: a shuffle orders no memory
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    m[t][0] = m[t][1] = -INFINITY;
-                    l[t][0] = l[t][1] = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < NO; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
-                }
-                add_parts<NT, NO>(slot_of(at), stride, n_parts, w0 == at, Z::SLOT, o, m, l);
                 idx = first / MERGE;
                 nodes = (nodes + MERGE - 1) / MERGE;
+                float4 *ps = slot_of(at);
+                if constexpr (NT == 4) {
+                    // a tile at a time, so that registers hold four parts' loads (all
+                    // tiles of a part: 1 request of 30000 61.5 us, this way 55)
+#pragma unroll 1
+                    for (int t = 0; t < NT; ++t) {
+                        float x[1][NO][4], mx[1][2], lx[1][2];
+                        add_parts<1, NO, 4>(ps + t * NO * 32, (NT * NO + t - t * NO) * 32, stride, n_parts, w0 == at, Z::SLOT, x, mx, lx);
+                        if (nodes == 1)
+                            store(t, x[0], mx[0], lx[0]);
+                        else
+                            keep(ps, t, x[0], mx[0], lx[0]);
+                    }
+                } else {
+                    add_parts<NT, NO, NT * NO <= 4 ? 2 : 1>(ps, NT * NO * 32, stride, n_parts, w0 == at, Z::SLOT, o, m, l);
+                    whole = nodes == 1;
+                }
                 stride *= MERGE;
                 count += 2 * NW * gridDim.x;
-                if (nodes == 1) {
-                    store = true;
-                    break;
-                }
-            }
+            } while (nodes > 1);
         }
-        if (store) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = k.row0 + 8 * t + 2 * lt + j;
-                    if (r >= k.row1) continue;
-                    const int tok = a.by_GQ.div(r), h = k.it.head * a.GQ + r - tok * a.GQ;
-                    const float inv = inverse(l[t][j]);
-                    float y[2 * NO];
-#pragma unroll
-                    for (int n = 0; n < NO; ++n) {
-                        y[2 * n] = o[t][n][j] * inv;
-                        y[2 * n + 1] = o[t][n][2 + j] * inv;
-                    }
-                    store_dims<F16, 2 * NO>(a, k.t0 + tok, h, lg * 2 * NO, y);
-                    if (lg == 0) store_lse(a, k.t0 + tok, h, m[t][j] - LIFT, l[t][j]);
-                }
-        }
+        if (NT < 4 && whole) store_all();
         __syncwarp();
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -520,20 +566,32 @@ cudaError_t launch(const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 template <int CODE, bool F16>
 cudaError_t launch_rows(const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 {
+    if (p.tiles == 4) return a.D > 64 ? launch<CODE, F16, 128, 4>(p, a, s) : launch<CODE, F16, 64, 4>(p, a, s);
     if (a.D > 64) return p.tiles == 1 ? launch<CODE, F16, 128, 1>(p, a, s) : launch<CODE, F16, 128, 2>(p, a, s);
     return p.tiles == 1 ? launch<CODE, F16, 64, 1>(p, a, s) : launch<CODE, F16, 64, 2>(p, a, s);
 }
 
 }  // namespace
 
-AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count)
+// Up to 16 rows per KV head go to this kernel, more than 32 to the tensor cores'
+// (attention8_tc.cu); between them it is this one if there are many requests and
+// heads, as one with few splits each over many warps, whose 32 rows take long to
+// join: 4 new tokens (32 rows) after 8000, int8, 8 KV heads, 4 requests 50 us here
+// and 42 there, 8 requests 63 and 68, 32 requests 165 and 200; after 500, 8 requests
+// 22 and 19, 64 requests 40 and 68.
+static constexpr int64_t MANY = 64;
+
+AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int64_t items, int sm_count)
 {
     AttnPlan p{};
     p.grid = std::min<int>(sm_count, MOST_CTAS);
-    p.tc = max_fresh > 16 / GQ;
-    p.tiles = max_fresh > 8 / GQ ? 2 : 1;
-    const size_t slot = (D > 64 ? Sizes<128, 2>::SLOT : Sizes<64, 2>::SLOT) * sizeof(float) / 2 * p.tiles;
-    p.workspace = ATTN_COUNTER_BYTES + (p.tc ? attention_tc_part_bytes(D, p.grid) : 2 * static_cast<size_t>(p.grid) * (p.tiles == 1 ? WARPS<1> : WARPS<2>) * slot);
+    p.tc = max_fresh > 32 / GQ || (max_fresh > 16 / GQ && items < MANY);
+    p.tiles = max_fresh > 16 / GQ ? 4 : max_fresh > 8 / GQ ? 2 : 1;
+    // the same whatever the number of requests
+    const size_t slot = (D > 64 ? Sizes<128, 1>::SLOT : Sizes<64, 1>::SLOT) * sizeof(float) * p.tiles;
+    const size_t here = max_fresh > 32 / GQ ? 0 : 2 * static_cast<size_t>(p.grid) * (p.tiles == 1 ? WARPS<1> : WARPS<2>) * slot;
+    const size_t there = p.tiles == 4 ? attention_tc_part_bytes(D, p.grid) : 0;
+    p.workspace = ATTN_COUNTER_BYTES + std::max(here, there);
     return p;
 }
 

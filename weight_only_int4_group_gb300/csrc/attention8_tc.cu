@@ -1,7 +1,8 @@
 // attention8_tc.cu -- the tensor-core attention kernel over an 8-bit cache
-// (attention_tc.cuh), for more than 16 rows per KV head: its tiles of 256 rows
-// read the codes once where the streaming kernel's of 16 would read them again
-// for each (16 requests of 4000 keys, 4 new tokens, 64/8 heads: 68 us).
+// (attention_tc.cuh), for more than 32 rows per KV head, and for 17 to 32 with few
+// requests (attention8.cu): its tiles of 256 rows read the codes once where the
+// streaming kernel's of 32 would read them again for each (16 requests of 4000
+// keys, 8 new tokens, 64/8 heads: 71 us, there 94 to 110).
 #include "attention_tc.cuh"
 
 namespace q4 {

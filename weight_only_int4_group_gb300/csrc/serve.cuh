@@ -136,7 +136,8 @@ struct Read8Args {
 };
 cudaError_t read8_launch(const Read8Args &a, q4_code code, bool f16, bool f32_out, int sm_count, cudaStream_t s);
 
-AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int sm_count);
+// items: requests times KV heads (0: for the workspace alone)
+AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int64_t items, int sm_count);
 cudaError_t attention8_tc_launch(int grid, const AttnArgs &a, q4_code code, bool f16, cudaStream_t s);
 cudaError_t attention8_launch(const AttnPlan &p, const AttnArgs &a, q4_code code, bool f16, cudaStream_t s);
 
