@@ -323,6 +323,17 @@ def test_up_to_32_rows(case, dtype, code):
             check(r, window, ws=ws, max_fresh=max(n for _, n in lengths))
 
 
+def test_a_workspace_serves_smaller_steps():
+    m = q4()
+    for D in (16, 64, 80, 128):
+        for GQ in (1, 2, 3, 5, 8, 11, 16, 17, 31, 32, 33, 64):
+            size = [m.attention_workspace_bytes(n, 2 * GQ, 2, D, eight_bit=True) for n in (*range(1, 40), 64, 1000, 10 ** 6)]
+            assert size[0] > 0 and size == sorted(size), (D, GQ)
+    ws = m.attention_workspace(512, 64, 8, 128, eight_bit=True)
+    for n in (1, 2, 4, 40, 4):
+        check(Requests8([(500, n)] * 8, 64, 8, 128, 16, torch.bfloat16, torch.int8, seed=n), ws=ws)
+
+
 @pytest.mark.parametrize("code", CODES)
 def test_up_to_32_rows_repeat_and_use_every_scale(code):
     """The same bits at each call, splits over many warps; keys and values of all

@@ -587,9 +587,9 @@ AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int64_t items
     p.grid = std::min<int>(sm_count, MOST_CTAS);
     p.tc = max_fresh > 32 / GQ || (max_fresh > 16 / GQ && items < MANY);
     p.tiles = max_fresh > 16 / GQ ? 4 : max_fresh > 8 / GQ ? 2 : 1;
-    // the same whatever the number of requests
+    // for any number of requests, and for steps of fewer new tokens too
     const size_t slot = (D > 64 ? Sizes<128, 1>::SLOT : Sizes<64, 1>::SLOT) * sizeof(float) * p.tiles;
-    const size_t here = max_fresh > 32 / GQ ? 0 : 2 * static_cast<size_t>(p.grid) * (p.tiles == 1 ? WARPS<1> : WARPS<2>) * slot;
+    const size_t here = GQ > 32 ? 0 : 2 * static_cast<size_t>(p.grid) * (p.tiles == 1 ? WARPS<1> : WARPS<2>) * slot;
     const size_t there = p.tiles == 4 ? attention_tc_part_bytes(D, p.grid) : 0;
     p.workspace = ATTN_COUNTER_BYTES + std::max(here, there);
     return p;
