@@ -492,3 +492,37 @@ def test_a_layer_in_8_bits(code):
         graph.replay()
         assert_attention(o, None, reference(q, p), "decode")
     assert length.tolist() == [n + 21 for n in prompts] and m.check() == m.OK
+
+
+def within(r, o, few, window=0):
+    """o (f32) against the definition, where weights carry 11 bits with few rows
+    whatever the type, and the type's with many: off by (u + e) sum p |v| / sum p
+    (serving_ref.py), with nothing added that small values could hide behind."""
+    from serving_ref import U, attention_reference
+    args = (*r.values(), r.table, r.start, r.total, r.q.shape[2] ** -0.5, window)
+    want, _, typed, _ = attention_reference(r.q, *args)
+    free = attention_reference(r.q.float(), *args)[2]  # e sum p |v| / sum p: no weight is rounded
+    limit = free + (typed - free) * (2.0 ** -11 / U[r.dtype] if few else 1.0)
+    err = (o.double() - want).abs()
+    assert not torch.isnan(err).any() and (err <= limit).all(), float((err / limit.clamp(min=1e-300)).max())
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 40])
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DT)
+def test_blocks_outside_the_cache_beside_the_smallest_scales(dtype, code, n):
+    """Their values are 0, whatever the scales of the blocks beside them."""
+    from cache8_ref import RANGE
+    lo = RANGE[code, dtype][0]
+    r = Requests8([(150, n)] * 8, 64, 8, 64, 16, dtype, code, seed=n, exps=(lo, lo + 2), q_scale=0.25)
+    r.k_exp.copy_(torch.randint(127 - 7, 127 - 3, r.k_exp.shape, device="cuda"))
+    used = set(r.table[r.table < r.k.shape[0]].tolist())
+    spare = next(i for i in range(r.k.shape[0]) if i not in used)
+    raw(r.k)[spare] = 0
+    raw(r.v)[spare] = 0
+    r.table[:4, 0] = -1
+    r.table[4:, 5] = 2 ** 31 - 1
+    o, _ = run(r, out_dtype=torch.float32)
+    r.table[:4, 0] = spare
+    r.table[4:, 5] = spare
+    within(r, o, n <= 4)

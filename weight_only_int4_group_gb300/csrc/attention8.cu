@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
             int64_t at = in ? blk * a.block_stride + (key - a.by_S.div(key) * a.S + hi) * a.token_stride +
                                   ld.it.head * a.head_stride + p * 16
                             : 0;
-            exp = in ? (lane < 16 ? a.k_exp : a.v_exp)[static_cast<int64_t>(blk) * a.Hkv + ld.it.head] : 127;
+            // (outside the cache the least one: zeros lift no reference over real values)
+            exp = in ? (lane < 16 ? a.k_exp : a.v_exp)[static_cast<int64_t>(blk) * a.Hkv + ld.it.head] : 0;
             exp_slot = ld_slot;
             const int rows = in && p * 16 < a.D ? ld.kv - key : 0;  // keys that exist
             // and those that the window leaves to some row
