@@ -526,3 +526,33 @@ def test_blocks_outside_the_cache_beside_the_smallest_scales(dtype, code, n):
     r.table[:4, 0] = spare
     r.table[4:, 5] = spare
     within(r, o, n <= 4)
+
+
+@pytest.mark.parametrize("n", [4, 8, 16, 40])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DT)
+def test_a_large_scale_whose_codes_are_zero(dtype, code, D, n):
+    """One block's value scale lies 8 to 96 powers of two above the others', and all
+    its codes but dim 0's are 0: the other dims hold the small values, wherever the
+    block stands and however the keys are split, with equal scores and others."""
+    from cache8_ref import RANGE
+    lo, hi = RANGE[code, dtype]
+    for q_scale in (0.0, 0.25):
+        for at in (0, 4, 9):  # the block, of 10
+            r = Requests8([(159 - n + b % 2, n) for b in range(8)], 16, 8, D, 16, dtype, code, seed=n, q_scale=q_scale)
+            r.k_exp.copy_(torch.randint(127 - 7, 127 - 3, r.k_exp.shape, device="cuda"))
+            r.v_exp.fill_(127 + lo)
+            for b in range(8):
+                blk = r.table[b, at].item()
+                r.v_exp[blk] = 127 + min(hi, lo + 8 + b * (hi - lo - 8) // 7 + b % 2)
+                raw(r.v)[blk, :, :, 1:] = 0
+            o, _ = run(r, out_dtype=torch.float32)
+            within(r, o, n <= 16)
+    # seven scales in turn, two requests
+    r = Requests8([(2000, n), (700, n)], 2, 1, D, 32, dtype, code, seed=5, q_scale=0.25)
+    r.k_exp.copy_(torch.randint(127 - 7, 127 - 3, r.k_exp.shape, device="cuda"))
+    r.v_exp.copy_(127 + lo + (torch.arange(len(r.v_exp), device="cuda") % 7 * (hi - lo) // 6)[:, None])
+    raw(r.v)[torch.arange(len(r.v), device="cuda") % 7 > 0, :, :, 8:] = 0
+    o, _ = run(r, out_dtype=torch.float32)
+    within(r, o, n <= 8)

@@ -23,10 +23,14 @@
 // Scales.  A unit is 16 keys, all of one block, so its two scales are uniform:
 // 2^ek goes into the factor of the scores, 2^ev into the weights' exponent: with
 // x_j = s_j + ev the second product sums 2^(x_j - ref) c_j and the row sum
-// 2^(x_j - ref) 2^-ev, both under one running reference that follows x.  So
-// weights in binary16 (which end at 2^16 and 2^-25) are large where their
-// contribution is, whatever the scales of other blocks.  The reference lies 2^7
-// below the x that it was taken from and moves when that is passed by 2^8.
+// 2^(x_j - ref) 2^-ev, both under one running reference that follows x.  The
+// reference lies 2^7 below the x that it was taken from and moves when that is
+// passed by 2^8, so the weights in binary16 (which end at 2^16 and 2^-25) are at
+// least 2^(7 - d) times their softmax weight (1 at most), where ev lies d below
+// the largest so far.  At the first unit with d > 7 the piece goes on in a careful
+// loop, where each unit has its own reference and its product is added in f32.  So
+// a weight is off by 2^-12 of itself or 2^-25 of the largest, whatever the scales:
+// what a dim holds beside zero codes of a large scale is kept.
 //
 // Work.  As in the 16-bit kernel (attention.cu): all units of the call form one
 // sequence cut into an equal range per warp; a ring of units per warp filled by
@@ -59,6 +63,7 @@ static_assert(WARPS<2> == WARPS<4>, "workspace");
 // heads of 64, 62.6 us either way.)
 constexpr int PAD = 4, MIN_UNITS = 4;
 constexpr float LIFT = 7.0f, SLACK = 8.0f;
+constexpr int NEAR = 7;  // powers of two that scales under one reference lie below the largest
 constexpr int MERGE = 8, LEVELS = 4, MOST_CTAS = 256;
 static_assert(MERGE * MERGE * MERGE * MERGE >= WARPS<1> * MOST_CTAS, "levels");
 static_assert(LEVELS * 2 * WARPS<1> * MOST_CTAS * sizeof(unsigned int) <= ATTN_COUNTER_BYTES, "counters");
@@ -317,16 +322,8 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
             for (int i = 0; i < NO; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
         }
 
-        for (int i = 0; i < k.nu; ++i) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-            __syncwarp();  // the other lanes' copies too; and all lanes are done with the slot below
-            issue();
-            const uint32_t ks = ring + slot * 2 * Z::TILE, vs = ks + Z::TILE;
-            const int ek = scales[slot * 2], ev = scales[slot * 2 + 1];
-            slot = slot + 1 == STAGES ? 0 : slot + 1;
-            float sc[NT][4];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+        // Codes of the lane's two keys as A fragments, 4 dims of each half at a time.
+        auto keys = [&](uint32_t ks, auto &&each) {
 #pragma unroll
             for (int h = 0; h < KH; ++h) {
                 const int p = DP == 128 ? (lt + 4 * h) ^ ((lg & 1) << 2) : lt;
@@ -337,22 +334,87 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                     uint32_t f[4];
                     widen<CODE>(xw[w], f[0], f[2]);
                     widen<CODE>(yw[w], f[1], f[3]);
-                    if (NT == 4) {
-#pragma unroll
-                        for (int t = 0; t < NT; t += 2) {
-                            const uint4 b = lds16(smem_u32(queries + ((h * 4 + w) * NT + t) / 2 * 32));
-                            mma16816(sc[t], f, b.x, b.y);
-                            mma16816(sc[(t + 1) % NT], f, b.z, b.w);
-                        }
-                        continue;
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) mma16816(sc[t], f, qf[t][h * 4 + w][0], qf[t][h * 4 + w][1]);
+                    each(h * 4 + w, f);
                 }
             }
+        };
+        // The lane's dims of keys 2 lt, 2 lt + 1, and those + 8, two m tiles at a time:
+        // dims 4w, 4w + 1 and 4w + 2, 4w + 3.
+        auto values = [&](uint32_t vs, auto &&each) {
+            uint32_t v[4][NO / 2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = 2 * lt + (e & 1) + (e >> 1) * 8;
+                if (DP == 128) {
+                    const uint4 x = lds16(vs + key * DP + ((lg ^ ((key >> 1 & 3) << 1)) << 4));
+                    v[e][0] = x.x;
+                    v[e][1] = x.y;
+                    v[e][NO / 2 - 2] = x.z;
+                    v[e][NO / 2 - 1] = x.w;
+                } else {
+                    const uint2 x = lds8(vs + key * DP + (((lg >> 1) ^ (key >> 1 & 3)) << 4) + (lg & 1) * 8);
+                    v[e][0] = x.x;
+                    v[e][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < NO / 2; ++w) {
+                uint32_t f[2][4];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    widen<CODE>(__byte_perm(v[2 * b][w], v[2 * b + 1][w], 0x5140), f[0][2 * b], f[0][2 * b + 1]);
+                    widen<CODE>(__byte_perm(v[2 * b][w], v[2 * b + 1][w], 0x7362), f[1][2 * b], f[1][2 * b + 1]);
+                }
+                each(2 * w, f[0]);
+                each(2 * w + 1, f[1]);
+            }
+        };
+        // Of a unit from key0 on: whether some row does not see all of it; and the mask.
+        auto in_part = [&](int key0) { return key0 + TK - 1 > lo_place || (a.window > 0 && key0 <= hi_place - a.window); };
+        auto mask = [&](int key0, int t, float (&x)[4]) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = k.row0 + 8 * t + 2 * lt + j, at = r < k.row1 ? k.base + a.by_GQ.div(r) : -1;
+#pragma unroll
+                for (int e = j; e < 4; e += 2) {
+                    const int key = key0 + lg + (e >> 1) * 8;
+                    if (!(key <= at && (a.window == 0 || key > at - a.window))) x[e] = -INFINITY;
+                }
+            }
+        };
+        auto of_warp = [](float x) {  // the largest of a row's keys
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        };
+
+        int i = 0, top = -128;  // the unit, the largest ev so far
+        for (; i < k.nu; ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+            __syncwarp();  // the other lanes' copies too; and all lanes are done with the slot below
+            issue();
+            const uint32_t ks = ring + slot * 2 * Z::TILE, vs = ks + Z::TILE;
+            const int ek = scales[slot * 2], ev = scales[slot * 2 + 1];
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            float sc[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+            keys(ks, [&](int c, const uint32_t (&f)[4]) {
+                if (NT == 4) {
+#pragma unroll
+                    for (int t = 0; t < NT; t += 2) {
+                        const uint4 b = lds16(smem_u32(queries + (c * NT + t) / 2 * 32));
+                        mma16816(sc[t], f, b.x, b.y);
+                        mma16816(sc[(t + 1) % NT], f, b.z, b.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma16816(sc[t], f, qf[t][c][0], qf[t][c][1]);
+                }
+            });
             // ---- mask and weights in units of log 2
             const int key0 = (k.kt0 + k.kt + i) * TK;
-            const bool part = key0 + TK - 1 > lo_place || (a.window > 0 && key0 <= hi_place - a.window);
+            const bool part = in_part(key0);
             const float fk = pow2(ek), fv = static_cast<float>(ev), undo = pow2(-ev);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -360,23 +422,17 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                 for (int e = 0; e < 4; ++e) sc[t][e] = fmaf(sc[t][e], cr[t][e & 1] * fk, fv);
             if (part) {  // (a branch: as selects the unmasked units took 4% longer, with 32 rows 20%)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int r = k.row0 + 8 * t + 2 * lt + j, at = r < k.row1 ? k.base + a.by_GQ.div(r) : -1;
-#pragma unroll
-                        for (int e = j; e < 4; e += 2) {
-                            const int key = key0 + lg + (e >> 1) * 8;
-                            if (!(key <= at && (a.window == 0 || key > at - a.window))) sc[t][e] = -INFINITY;
-                        }
-                    }
+                for (int t = 0; t < NT; ++t) mask(key0, t, sc[t]);
             }
-            bool past = false;
+            const bool far = ev < top - NEAR;
+            top = max(top, ev);
+            bool past = far;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) past |= !(sc[t][e] <= m[t][e & 1] + SLACK);
             if (__any_sync(0xffffffffu, past)) {
+                if (far) break;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     float f[2];
@@ -387,11 +443,7 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                             if (isnan(sc[t][j])) sc[t][j] = fv;
                             if (isnan(sc[t][2 + j])) sc[t][2 + j] = fv;
                         }
-                        float mx = fmaxf(sc[t][j], sc[t][2 + j]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float mn = fmaxf(m[t][j], mx), ref = mn == -INFINITY ? 0.0f : mn;
+                        const float mn = fmaxf(m[t][j], of_warp(fmaxf(sc[t][j], sc[t][2 + j]))), ref = mn == -INFINITY ? 0.0f : mn;
                         f[j] = ex2(m[t][j] - ref);
                         m[t][j] = mn;
                         l[t][j] *= f[j];
@@ -418,35 +470,61 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
                 p[t][0] = transposed(pack2<true>(sc[t][0], sc[t][1]));
                 p[t][1] = transposed(pack2<true>(sc[t][2], sc[t][3]));
             }
-            // ---- values: the lane's dims of keys 2 lt, 2 lt + 1, and those + 8
-            uint32_t v[4][NO / 2];
+            values(vs, [&](int n, const uint32_t (&f)[4]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = 2 * lt + (e & 1) + (e >> 1) * 8;
-                if (DP == 128) {
-                    const uint4 x = lds16(vs + key * DP + ((lg ^ ((key >> 1 & 3) << 1)) << 4));
-                    v[e][0] = x.x;
-                    v[e][1] = x.y;
-                    v[e][NO / 2 - 2] = x.z;
-                    v[e][NO / 2 - 1] = x.w;
-                } else {
-                    const uint2 x = lds8(vs + key * DP + (((lg >> 1) ^ (key >> 1 & 3)) << 4) + (lg & 1) * 8);
-                    v[e][0] = x.x;
-                    v[e][1] = x.y;
-                }
+                for (int t = 0; t < NT; ++t) mma16816(o[t][n], f, p[t][0], p[t][1]);
+            });
+        }
+        // ---- the careful loop, a tile at a time.  (As a branch of the loop above it
+        // cost that one 2 to 11%, with the sums set aside in local memory 2 to 12%,
+        // this way 0 to 2.5%: 48 long decodes 197.9 -> 202.4 us.  A piece that goes
+        // through here takes 1.05 (8 rows) to 2 times (32) as long.)
+        for (bool landed = true; i < k.nu; ++i, landed = false) {
+            if (!landed) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+                __syncwarp();
+                issue();
+                slot = slot + 1 == STAGES ? 0 : slot + 1;
             }
+            const int at = slot == 0 ? STAGES - 1 : slot - 1, key0 = (k.kt0 + k.kt + i) * TK;
+            const uint32_t ks = ring + at * 2 * Z::TILE, vs = ks + Z::TILE;
+            const int ev = scales[at * 2 + 1];
+            const float fk = pow2(scales[at * 2]), undo = pow2(-ev);
 #pragma unroll
-            for (int w = 0; w < NO / 2; ++w) {
-                uint32_t f[2][4];  // two m tiles: dims 4w, 4w + 1 and 4w + 2, 4w + 3
+            for (int t = 0; t < NT; ++t) {
+                float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                keys(ks, [&](int c, const uint32_t (&f)[4]) {
+                    if (NT == 4) {
+                        const uint2 b = lds8(smem_u32(queries + (c * NT + t) / 2 * 32) + 8 * (t & 1));
+                        mma16816(x, f, b.x, b.y);
+                    } else {
+                        mma16816(x, f, qf[t][c][0], qf[t][c][1]);
+                    }
+                });
+                // (in this order a product of 0 stays 0, whatever the factors)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    widen<CODE>(__byte_perm(v[2 * b][w], v[2 * b + 1][w], 0x5140), f[0][2 * b], f[0][2 * b + 1]);
-                    widen<CODE>(__byte_perm(v[2 * b][w], v[2 * b + 1][w], 0x7362), f[1][2 * b], f[1][2 * b + 1]);
+                for (int e = 0; e < 4; ++e) x[e] = fmaf(x[e] * cr[t][e & 1], fk, static_cast<float>(ev));
+                if (in_part(key0)) mask(key0, t, x);
+                float f[2], g[2];  // factors of what was summed and of the unit
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float mx = of_warp(fmaxf(x[j], x[2 + j])), own = mx == -INFINITY ? 0.0f : mx;
+                    const float mn = fmaxf(m[t][j], mx), ref = mn == -INFINITY ? 0.0f : mn;
+                    f[j] = ex2(m[t][j] - ref);
+                    g[j] = ex2(mx - ref);
+                    m[t][j] = mn;
+                    x[j] = ex2((x[j] - own) + LIFT);
+                    x[2 + j] = ex2((x[2 + j] - own) + LIFT);
+                    l[t][j] = fmaf((x[j] + x[2 + j]) * undo, g[j], l[t][j] * f[j]);
                 }
+                const uint32_t p0 = transposed(pack2<true>(x[0], x[1])), p1 = transposed(pack2<true>(x[2], x[3]));
+                values(vs, [&](int n, const uint32_t (&w)[4]) {
+                    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma16816(y, w, p0, p1);
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) mma16816(o[t][2 * w + e], f[e], p[t][0], p[t][1]);
+                    for (int e = 0; e < 4; ++e) o[t][n][e] = fmaf(y[e], g[e & 1], o[t][n][e] * f[e & 1]);
+                });
+                __syncwarp();  // (keeps the tiles' code apart: without it 32 rows spill, 169 -> 186 us)
             }
         }
 #pragma unroll
