@@ -556,3 +556,27 @@ def test_a_large_scale_whose_codes_are_zero(dtype, code, D, n):
     raw(r.v)[torch.arange(len(r.v), device="cuda") % 7 > 0, :, :, 8:] = 0
     o, _ = run(r, out_dtype=torch.float32)
     within(r, o, n <= 8)
+
+
+@pytest.mark.parametrize("n", [4, 8, 16, 40])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("code", CODES)
+def test_small_query_elements_beside_large_ones(code, D, n):
+    """Query elements 2^28 to 2^120 times as large as the others meet zero codes:
+    the scores come from the small ones."""
+    r = Requests8([(100 + b, n) for b in range(8)], 16, 8, D, 16, torch.bfloat16, code, seed=n)
+    raw(r.k)[:, :, :, :2] = 0
+    for b, e in enumerate((28, 31, 32, 33, 36, 40, 60, 120)):
+        rows = r.q[r.start[b]:r.start[b + 1]]
+        rows[..., 0] = 1.5 * 2.0 ** e
+        rows[:, ::3, 1] = -2.0 ** (e - 5)
+        rows[:, 1::4, :2] = 0.25  # and heads without one
+    o, lse = run(r, out_dtype=torch.float32)
+    ref = r.reference()
+    assert_attention(o, lse, ref, f"{n}")
+    within(r, o, n <= 16)
+    # elements as small as 2^-100, that large codes bring back
+    r.q *= 2.0 ** -100
+    r.q[r.start[7]:] *= 2.0 ** -20
+    r.k_exp.fill_(127 + 48)
+    check(r, scale=2.0 ** 45 * D ** -0.5)

@@ -17,8 +17,10 @@
 //            keys and pairs the keys' bytes; it ends with 16 consecutive dims of
 //            its two rows.  The weights turn by movmatrix in between.
 // Queries in bf16 are scaled by a power of two per row, so that their largest
-// lies in [2^14, 2^15), and go to binary16 without rounding (below 2^-39 of the
-// largest they lose bits; a sum in f32 holds no more).
+// lies in [2^14, 2^15), and go to binary16 without rounding as long as no other one
+// lies more than 2^31 below it.  Otherwise (the large ones may meet zero codes) the
+// piece is summed by the careful loop below, where queries stay in bf16 and codes
+// are widened to that.
 //
 // Scales.  A unit is 16 keys, all of one block, so its two scales are uniform:
 // 2^ek goes into the factor of the scores, 2^ev into the weights' exponent: with
@@ -98,12 +100,19 @@ __device__ __forceinline__ uint2 lds8(uint32_t at)
     return v;
 }
 
+template <bool F16 = true>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x)
@@ -262,55 +271,67 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
 
     int slot = 0;
     for (; k.more(rng); k.next(a, rng)) {
-        // ---- queries as B fragments: row lg of a tile, the lane's pieces of it
+        // ---- queries as B fragments: row lg of a tile, the lane's pieces of it; in
+        // binary16, or as they are (bf16 from 2^111 on by up to 2^-17: no sum of 128
+        // products with 448 passes f32).  True if binary16 would lose some of them.
         uint32_t qf[NT][KH * 4][2];
         float cr[NT][2];  // scores' factor of rows 2 lt and 2 lt + 1
+        auto load_queries = [&](auto as_they_are) {
+            constexpr bool ALIKE = decltype(as_they_are)::value;
+            bool lossy = false;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int r = k.row0 + 8 * t + lg;
-            const bool in = r < k.row1;
-            const int tok = in ? a.by_GQ.div(r) : 0;
-            const uint16_t *q = a.q + (k.t0 + tok) * a.q_stride + static_cast<int64_t>(k.it.head * a.GQ + r - tok * a.GQ) * a.D;
-            uint32_t peak = 0;
+            for (int t = 0; t < NT; ++t) {
+                const int r = k.row0 + 8 * t + lg;
+                const bool in = r < k.row1;
+                const int tok = in ? a.by_GQ.div(r) : 0;
+                const uint16_t *q = a.q + (k.t0 + tok) * a.q_stride + static_cast<int64_t>(k.it.head * a.GQ + r - tok * a.GQ) * a.D;
+                uint32_t peak = 0, least = ~0u;  // (less 1, so that zeros do not count)
 #pragma unroll
-            for (int h = 0; h < KH; ++h) {
-                const int d = (lt + 4 * h) * 16;
-                uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                if (in && d < a.D) {
-                    x = *reinterpret_cast<const uint4 *>(q + d);
-                    y = *reinterpret_cast<const uint4 *>(q + d + 8);
-                }
-                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    qf[t][h * 4 + i / 2][i & 1] = w[i];
-                    if (!F16) peak = max(peak, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
-                }
-            }
-            int ex = 0;
-            if (!F16) {
-                peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
-                peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
-                ex = peak ? min(max(static_cast<int>(peak >> 7) - 127 - 14, -126), 126) : 0;
-                const float f = pow2(-ex);
-                if (peak >= 0x7F80u) ex = 0;  // scores of a row that is not finite are not either, whatever their factor
-#pragma unroll
-                for (int i = 0; i < KH * 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t w = qf[t][i][j];
-                        qf[t][i][j] = pack2<true>(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+                for (int h = 0; h < KH; ++h) {
+                    const int d = (lt + 4 * h) * 16;
+                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                    if (in && d < a.D) {
+                        x = *reinterpret_cast<const uint4 *>(q + d);
+                        y = *reinterpret_cast<const uint4 *>(q + d + 8);
                     }
-            }
+                    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int j = 0; j < 2; ++j) cr[t][j] = a.scale_log2 * pow2(__shfl_sync(0xffffffffu, ex, 4 * (2 * lt + j)));
-            if (NT == 4) {  // (read by the same lane alone)
+                    for (int i = 0; i < 8; ++i) {
+                        qf[t][h * 4 + i / 2][i & 1] = w[i];
+                        const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
+                        if (!F16) peak = max(peak, max(lo, hi));
+                        if (!F16 && !ALIKE) least = min(least, min(lo - 1, hi - 1));
+                    }
+                }
+                int ex = 0;
+                if (!F16) {
+                    peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+                    peak = max(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
+                    const int top = static_cast<int>(peak >> 7) - 127;
+                    if (!ALIKE) lossy |= static_cast<int>(least + 1 >> 7) - 127 < top - 31 && least != ~0u;
+                    ex = ALIKE ? max(top - 110, 0) : peak ? min(max(top - 14, -126), 126) : 0;
+                    const float f = pow2(-ex);
+                    if (peak >= 0x7F80u) ex = 0;  // scores of a row that is not finite are not either, whatever their factor
 #pragma unroll
-                for (int i = 0; i < KH * 4; ++i)
-                    *reinterpret_cast<uint2 *>(reinterpret_cast<uint32_t *>(queries + (i * NT / 2 + t / 2) * 32) + 2 * (t & 1)) =
-                        make_uint2(qf[t][i][0], qf[t][i][1]);
+                    for (int i = 0; i < KH * 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t w = qf[t][i][j];
+                            qf[t][i][j] = pack2<!ALIKE>(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) cr[t][j] = a.scale_log2 * pow2(__shfl_sync(0xffffffffu, ex, 4 * (2 * lt + j)));
+                if (NT == 4) {  // (read by the same lane alone)
+#pragma unroll
+                    for (int i = 0; i < KH * 4; ++i)
+                        *reinterpret_cast<uint2 *>(reinterpret_cast<uint32_t *>(queries + (i * NT / 2 + t / 2) * 32) + 2 * (t & 1)) =
+                            make_uint2(qf[t][i][0], qf[t][i][1]);
+                }
             }
-        }
+            return __any_sync(0xffffffffu, lossy) != 0;
+        };
+        const bool lossy = load_queries(std::false_type{});
         const int lo_place = k.base + a.by_GQ.div(k.row0), hi_place = k.base + a.by_GQ.div(k.row1 - 1);
 
         float o[NT][NO][4], m[NT][2], l[NT][2];
@@ -389,7 +410,7 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
         };
 
         int i = 0, top = -128;  // the unit, the largest ev so far
-        for (; i < k.nu; ++i) {
+        for (; !lossy && i < k.nu; ++i) {
             asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
             __syncwarp();  // the other lanes' copies too; and all lanes are done with the slot below
             issue();
@@ -477,9 +498,11 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
         }
         // ---- the careful loop, a tile at a time.  (As a branch of the loop above it
         // cost that one 2 to 11%, with the sums set aside in local memory 2 to 12%,
-        // this way 0 to 2.5%: 48 long decodes 197.9 -> 202.4 us.  A piece that goes
-        // through here takes 1.05 (8 rows) to 2 times (32) as long.)
-        for (bool landed = true; i < k.nu; ++i, landed = false) {
+        // this way 0 to 5%: 48 long decodes 197.7 -> 201.0 us, 32 requests with 2 new
+        // tokens 112.2 -> 115.8, with 4 164.8 -> 173.4.  Where all pieces go through
+        // here they take 1.2 (8 rows) to 3 times (32) as long.)
+        if (!F16 && i < k.nu) load_queries(std::true_type{});
+        for (bool landed = !lossy; i < k.nu; ++i, landed = false) {
             if (!landed) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
                 __syncwarp();
@@ -488,17 +511,19 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
             }
             const int at = slot == 0 ? STAGES - 1 : slot - 1, key0 = (k.kt0 + k.kt + i) * TK;
             const uint32_t ks = ring + at * 2 * Z::TILE, vs = ks + Z::TILE;
-            const int ev = scales[at * 2 + 1];
-            const float fk = pow2(scales[at * 2]), undo = pow2(-ev);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                const int ev = scales[at * 2 + 1];
+                const float fk = pow2(scales[at * 2]), undo = pow2(-ev);
                 float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 keys(ks, [&](int c, const uint32_t (&f)[4]) {
-                    if (NT == 4) {
-                        const uint2 b = lds8(smem_u32(queries + (c * NT + t) / 2 * 32) + 8 * (t & 1));
+                    uint2 b = make_uint2(qf[t][c][0], qf[t][c][1]);
+                    if (NT == 4) b = lds8(smem_u32(queries + (c * NT + t) / 2 * 32) + 8 * (t & 1));
+                    if (F16) {
                         mma16816(x, f, b.x, b.y);
                     } else {
-                        mma16816(x, f, qf[t][c][0], qf[t][c][1]);
+                        const uint32_t g[4] = {f16x2_upper(f[0]), f16x2_upper(f[1]), f16x2_upper(f[2]), f16x2_upper(f[3])};
+                        mma16816<false>(x, g, b.x, b.y);
                     }
                 });
                 // (in this order a product of 0 stays 0, whatever the factors)
@@ -524,7 +549,7 @@ __global__ void __launch_bounds__(WARPS<NT> * 32, 1) k_attn8_stream(const AttnAr
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[t][n][e] = fmaf(y[e], g[e & 1], o[t][n][e] * f[e & 1]);
                 });
-                __syncwarp();  // (keeps the tiles' code apart: without it 32 rows spill, 169 -> 186 us)
+                __syncwarp();  // (keeps the tiles' code apart: without it 32 rows spill more, 169 -> 186 us)
             }
         }
 #pragma unroll

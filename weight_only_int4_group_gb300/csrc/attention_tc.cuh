@@ -306,13 +306,6 @@ __device__ __forceinline__ uint32_t sub2(uint32_t x, uint32_t y)
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
     return r;
 }
-// The upper halves of two binary16 numbers' f32.
-__device__ __forceinline__ uint32_t f16x2_upper(uint32_t x)
-{
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-}
-
 __device__ __forceinline__ uint4 lds16(uint32_t at)
 {
     uint4 v;

@@ -30,6 +30,13 @@ __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t codes)
     return r;
 }
 
+// The upper halves of two binary16 numbers' f32: of codes, as bf16.
+__device__ __forceinline__ uint32_t f16x2_upper(uint32_t x)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+}
+
 // Four codes of a word as f32.
 template <int CODE>
 __device__ __forceinline__ void codes_to_f32(uint32_t w, float (&x)[4])
