@@ -580,3 +580,14 @@ def test_small_query_elements_beside_large_ones(code, D, n):
     r.q[r.start[7]:] *= 2.0 ** -20
     r.k_exp.fill_(127 + 48)
     check(r, scale=2.0 ** 45 * D ** -0.5)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("heads,kv,D", [(8, 1, 128), (14, 2, 64), (4, 4, 80)])
+def test_few_rows_keep_11_bits_of_the_weights(heads, kv, D, dtype, code):
+    """Of bf16 caches too, and whether items are split or not."""
+    for lengths in ([(776, 1)], [(5000, 1), (3, 2)], [(i * 37 % 500, 1) for i in range(70)], [(90, 2), (0, 1), (17, 2)]):
+        r = Requests8(lengths, heads, kv, D, 16, dtype, code, seed=len(lengths), q_scale=0.5)
+        within(r, run(r, out_dtype=torch.float32)[0], True)
+        within(r, run(r, window=33, out_dtype=torch.float32)[0], True, 33)
