@@ -574,7 +574,9 @@ q4_status q4_cache_read8(const q4_kv_cache8 *cache, const int32_t *table, int64_
  * for.  The codes are widened to 16 bits exactly and products summed in f32 by
  * the tensor cores; weights are rounded to binary16 with 16 rows (new tokens
  * times query heads per KV head) or fewer, to the queries' type with more than
- * 32, and between them to one or the other by the number of requests and heads.
+ * 32, and between them to one or the other by the number of requests and heads
+ * (binary16: off by 2^-12 of themselves or 2^-25 of the row's largest, whatever
+ * the scales of the blocks).
  * Workspace: q4_attention8_workspace_bytes; one of the larger size may serve
  * q4_attention and q4_attention8 calls of one stream in turn.  Codes behind a
  * request's end and before every row's window never matter; the two e4m3 codes

@@ -507,14 +507,14 @@ def within(r, o, few, window=0):
     assert not torch.isnan(err).any() and (err <= limit).all(), float((err / limit.clamp(min=1e-300)).max())
 
 
-@pytest.mark.parametrize("n", [1, 2, 4, 40])
+@pytest.mark.parametrize("n", [4, 8, 16, 40])
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("dtype", DT)
 def test_blocks_outside_the_cache_beside_the_smallest_scales(dtype, code, n):
     """Their values are 0, whatever the scales of the blocks beside them."""
     from cache8_ref import RANGE
     lo = RANGE[code, dtype][0]
-    r = Requests8([(150, n)] * 8, 64, 8, 64, 16, dtype, code, seed=n, exps=(lo, lo + 2), q_scale=0.25)
+    r = Requests8([(150, n)] * 8, 16, 8, 64, 16, dtype, code, seed=n, exps=(lo, lo + 2), q_scale=0.25)
     r.k_exp.copy_(torch.randint(127 - 7, 127 - 3, r.k_exp.shape, device="cuda"))
     used = set(r.table[r.table < r.k.shape[0]].tolist())
     spare = next(i for i in range(r.k.shape[0]) if i not in used)
@@ -525,7 +525,7 @@ def test_blocks_outside_the_cache_beside_the_smallest_scales(dtype, code, n):
     o, _ = run(r, out_dtype=torch.float32)
     r.table[:4, 0] = spare
     r.table[4:, 5] = spare
-    within(r, o, n <= 4)
+    within(r, o, n <= 16)
 
 
 @pytest.mark.parametrize("n", [4, 8, 16, 40])
@@ -538,17 +538,16 @@ def test_a_large_scale_whose_codes_are_zero(dtype, code, D, n):
     block stands and however the keys are split, with equal scores and others."""
     from cache8_ref import RANGE
     lo, hi = RANGE[code, dtype]
-    for q_scale in (0.0, 0.25):
-        for at in (0, 4, 9):  # the block, of 10
-            r = Requests8([(159 - n + b % 2, n) for b in range(8)], 16, 8, D, 16, dtype, code, seed=n, q_scale=q_scale)
-            r.k_exp.copy_(torch.randint(127 - 7, 127 - 3, r.k_exp.shape, device="cuda"))
-            r.v_exp.fill_(127 + lo)
-            for b in range(8):
-                blk = r.table[b, at].item()
-                r.v_exp[blk] = 127 + min(hi, lo + 8 + b * (hi - lo - 8) // 7 + b % 2)
-                raw(r.v)[blk, :, :, 1:] = 0
-            o, _ = run(r, out_dtype=torch.float32)
-            within(r, o, n <= 16)
+    for q_scale, at in ((0.0, 4), (0.25, 0), (0.25, 9)):  # at: the block, of 10
+        r = Requests8([(159 - n + b % 2, n) for b in range(8)], 16, 8, D, 16, dtype, code, seed=n, q_scale=q_scale)
+        r.k_exp.copy_(torch.randint(127 - 7, 127 - 3, r.k_exp.shape, device="cuda"))
+        r.v_exp.fill_(127 + lo)
+        for b in range(8):
+            blk = r.table[b, at].item()
+            r.v_exp[blk] = 127 + min(hi, lo + 8 + b * (hi - lo - 8) // 7 + b % 2)
+            raw(r.v)[blk, :, :, 1:] = 0
+        o, _ = run(r, out_dtype=torch.float32)
+        within(r, o, n <= 16)
     # seven scales in turn, two requests
     r = Requests8([(2000, n), (700, n)], 2, 1, D, 32, dtype, code, seed=5, q_scale=0.25)
     r.k_exp.copy_(torch.randint(127 - 7, 127 - 3, r.k_exp.shape, device="cuda"))
@@ -587,7 +586,7 @@ def test_small_query_elements_beside_large_ones(code, D, n):
 @pytest.mark.parametrize("heads,kv,D", [(8, 1, 128), (14, 2, 64), (4, 4, 80)])
 def test_few_rows_keep_11_bits_of_the_weights(heads, kv, D, dtype, code):
     """Of bf16 caches too, and whether items are split or not."""
-    for lengths in ([(776, 1)], [(5000, 1), (3, 2)], [(i * 37 % 500, 1) for i in range(70)], [(90, 2), (0, 1), (17, 2)]):
+    for lengths in ([(776, 1)], [(5000, 1), (3, 2)], [(i * 37 % 500, 1) for i in range(33)], [(90, 2), (0, 1), (17, 2)]):
         r = Requests8(lengths, heads, kv, D, 16, dtype, code, seed=len(lengths), q_scale=0.5)
         within(r, run(r, out_dtype=torch.float32)[0], True)
         within(r, run(r, window=33, out_dtype=torch.float32)[0], True, 33)

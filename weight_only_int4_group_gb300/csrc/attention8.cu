@@ -39,14 +39,16 @@
 // cp.async; split items meet in a tree, in sequence order.
 //
 // Measured (64 query / 8 KV heads of 128, bf16, graph): 48 requests of 1001..24576
-// keys, int8, 198 us, 6.4 TB/s (0.94 of the measured copy bandwidth; over 16 bits
+// keys, int8, 200 us, 6.3 TB/s (0.93 of the measured copy bandwidth; over 16 bits
 // 384 us); 32 of 101..8192 keys, e4m3, 57 us (0.70; 96 us over 16 bits); 32 of
-// 8001 94 us int8, 91 e4m3, 61 with heads of 64; one of 65536 39 us; one of 777
-// keys (32 heads) 13.7 us, which is latency.  DRAM reads are 1.004 of the codes;
-// the arithmetic pipe of the bytes' permutations is 46% busy.
-// Rows cost: 32 requests of 8000, int8, with 2 new tokens (16 rows) 112 us, with 4
-// (32) 165: four row tiles leave room for 8 warps, which issue 0.4 instructions per
-// cycle and scheduler (dependent ones), and mma.sync is half busy.
+// 8001 92 us int8, 90 e4m3, 62 with heads of 64; one of 65536 40 us; one of 777
+// keys (32 heads) 14 us, which is latency.  DRAM reads are 1.004 of the codes;
+// the arithmetic pipe of the bytes' permutations is 45% busy.
+// Rows cost: 32 requests of 8000, int8, with 2 new tokens (16 rows) 116 us, with 4
+// (32) 174: four row tiles leave room for 8 warps, which issue 0.46 instructions per
+// cycle and scheduler (dependent ones), and mma.sync is at 29% of its rate.
+#include <type_traits>
+
 #include "attention.cuh"
 #include "cache8.cuh"
 
@@ -681,8 +683,8 @@ cudaError_t launch_rows(const AttnPlan &p, const AttnArgs &a, cudaStream_t s)
 // (attention8_tc.cu); between them it is this one if there are many requests and
 // heads, as one with few splits each over many warps, whose 32 rows take long to
 // join: 4 new tokens (32 rows) after 8000, int8, 8 KV heads, 4 requests 50 us here
-// and 42 there, 8 requests 63 and 68, 32 requests 165 and 200; after 500, 8 requests
-// 22 and 19, 64 requests 40 and 68.
+// and 43 there, 8 requests 66 and 69, 32 requests 174 and 201; after 500, 8 requests
+// 23 and 19, 64 requests 43 and 68.
 static constexpr int64_t MANY = 64;
 
 AttnPlan attention8_plan(int64_t max_fresh, int64_t GQ, int64_t D, int64_t items, int sm_count)

@@ -11,7 +11,7 @@ constexpr int I8 = Q4_I8, E4M3 = Q4_E4M3;
 // Exponents that keep every c * 2^e a number of the 16-bit type.  binary16:
 // 2^-24 is its smallest step (an e4m3 code is a multiple of 2^-9), 127 * 2^9 and
 // 448 * 2^7 lie below 65504.  bf16 has the room of f32; 2^+-48 leaves weights
-// and sums in units of any of these scales room too.
+// and sums in f32 in units of any of these scales room too.
 template <int CODE, bool F16>
 struct Exponents {
     static constexpr int LO = F16 ? (CODE == I8 ? -24 : -15) : -48;
